@@ -9,6 +9,9 @@ library is not built or no GPU is present the calls raise.
     cb = Codebook.lloyd_max(d, bits)                    # one per (d, bits), data-free
     w_codes, w_norms = fold_weights(W, rot, cb_w)       # offline
     Y = linear(X, rot, cb_a, w_codes, w_norms, cb_w)    # online
+
+The attention-side operators (rotary positions, the 8-bit key/value cache, attention over it) are in
+attention.py and reached from here as well: orbq.rope, orbq.kv_append, orbq.kv_attention, ...
 """
 from __future__ import annotations
 
@@ -24,6 +27,7 @@ __all__ = [
     "rpbh_quantize", "lut_gemm", "linear_workspace_bytes", "linear", "linear_noalloc", "test_rotate", "test_quantize_t",
     "test_mfma_rate",
     "F32", "BF16",
+    "Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_read", "kv_attention", "kv_attention_workspace_bytes",
 ]
 
 F32, BF16 = 0, 1
@@ -82,6 +86,12 @@ _SIGS = {
     "orbq_linear_a16": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(_Rpbh), _P, _P, ctypes.POINTER(_Codebook),
                                        _I64, _P, ctypes.c_size_t, _P, ctypes.c_int, _I64, _P]),
     "orbq_rht_passes": (ctypes.c_int32, [ctypes.c_float, ctypes.c_float, _I32, _I32]),
+    "orbq_rope_apply": (ctypes.c_int, [_P, _P, _I64, _I64, _I32, _P, _I32, ctypes.c_int, _I32, _P]),
+    "orbq_kv_append": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, ctypes.c_int, _P]),
+    "orbq_kv_read": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, ctypes.c_int, _P]),
+    "orbq_kv_attention_workspace_bytes": (ctypes.c_size_t, [_P, _I32, _I64, _I32, _I32, _I64, _I32, _I32]),
+    "orbq_kv_attention": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _I64, _P, _I64, _I64, _I32, _P, _I64, _I64, _P,
+                                         ctypes.c_int, _F, _I32, _I32, _P, ctypes.c_size_t, _P]),
     "orbq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "orbq_last_error": (ctypes.c_char_p, []),
     "orbq_test_rotate": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(_Rpbh), _P, _P, _P]),
@@ -403,3 +413,18 @@ def test_mfma_rate(workgroups: int, iters: int, sink=None, device=None) -> float
     _check(load().orbq_test_mfma_rate(workgroups, iters, sink.data_ptr(), ctypes.byref(flops), _stream(torch, dev)),
            "orbq_test_mfma_rate")
     return flops.value
+
+
+# ------------------------------------------------------------------------ the attention-side operators
+_ATTENTION = ("Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_read", "kv_attention",
+              "kv_attention_workspace_bytes")
+
+
+def __getattr__(name: str):
+    # attention.py needs torch, which this module imports only where a call needs it
+    if name in _ATTENTION:
+        from . import attention
+        for n in _ATTENTION:
+            globals()[n] = getattr(attention, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -461,6 +461,17 @@ ORBQ_API const char* orbq_status_string(int status) {
 
 ORBQ_API const char* orbq_last_error(void) { return g_last_error; }
 
+namespace orbq {
+int set_error(int status, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  std::vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
+  va_end(ap);
+  return status;
+}
+int set_ok() { return ok(); }
+}  // namespace orbq
+
 ORBQ_API int orbq_test_rotate(const void* X, int64_t n, int64_t d, int64_t ldx, const orbq_rpbh* rot, float* x_rot,
                               float* x_norms, void* stream) {
   const char* what = "orbq_test_rotate";

@@ -7,6 +7,11 @@
 
 namespace orbq {
 
+// api.cpp: records the detail that orbq_last_error returns (of this host thread) and gives back
+// `status`; set_ok clears it and gives back ORBQ_OK.
+int set_error(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int set_ok();
+
 constexpr int kMaxPosBoundaries = 31;  // 6-bit codebooks: N/2 - 1 positive decision boundaries
 constexpr int kMaxTableHalf = 256;     // quantizer table holds buckets -J..J-1, J <= 256
 // 2-, 3- and 4-bit codebooks: the quantize kernel's table covers every bucket of t' in

@@ -1,0 +1,45 @@
+// kv_attention: which form a call takes and how its keys are split.  Kernels: kv_attention_kernel.h.
+#include <algorithm>
+
+#include "attention.h"
+
+namespace orbq {
+
+template <> int launch_attn<64>(const AttnArgs&, const AttnPlan&, hipStream_t);
+template <> int launch_attn<128>(const AttnArgs&, const AttnPlan&, hipStream_t);
+template <> int launch_attn<256>(const AttnArgs&, const AttnPlan&, hipStream_t);
+
+AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t kv_heads, int32_t d, int64_t max_len,
+                        int32_t causal_block, int32_t window, int cus) {
+  AttnPlan p{};
+  const int64_t rows = static_cast<int64_t>(max_new) * (heads / kv_heads);
+  p.many = rows > 32;
+  p.rt = rows > 16 ? 2 : 1;
+  const int tile_rows = p.many ? 128 : 16 * p.rt;
+  p.row_tiles = static_cast<int32_t>((rows + tile_rows - 1) / tile_rows);
+  // the keys that one row tile can see, in 64-key tiles
+  int64_t span = max_len;
+  if (window) span = std::min<int64_t>(span, static_cast<int64_t>(window) + max_new + causal_block);
+  const int64_t tiles = std::max<int64_t>(1, (span + 63) / 64 + 1);
+  const int64_t groups = static_cast<int64_t>(batch) * kv_heads * p.row_tiles;
+  const int64_t want = static_cast<int64_t>(cus) * (p.many ? 2 : 8), least = p.many ? 8 : 4;
+  int64_t splits = 1;
+  if (groups < want) splits = std::min((want + groups - 1) / groups, (tiles + least - 1) / least);
+  p.chunk = static_cast<int32_t>((tiles + splits - 1) / splits);
+  p.splits = static_cast<int32_t>((tiles + p.chunk - 1) / p.chunk);
+  (void)d;
+  return p;
+}
+
+int launch_kv_attention(AttnArgs a, const AttnPlan& p, hipStream_t stream) {
+  a.row_tiles = p.row_tiles;
+  a.splits = p.splits;
+  a.chunk = p.chunk;
+  switch (a.c.d) {
+    case 64: return launch_attn<64>(a, p, stream);
+    case 128: return launch_attn<128>(a, p, stream);
+    default: return launch_attn<256>(a, p, stream);
+  }
+}
+
+}  // namespace orbq

@@ -77,7 +77,9 @@ typedef enum {
   ORBQ_ERR_CODEBOOK = -6      /* codebook not ascending, not antisymmetric, not finite */
 } orbq_status;
 
-typedef enum { ORBQ_F32 = 0, ORBQ_BF16 = 1 } orbq_dtype;
+/* ORBQ_F16 is taken by the attention-side operators (orbq_rope_apply, orbq_kv_*) only; the other
+ * calls refuse it with ORBQ_ERR_INVALID_ARG. */
+typedef enum { ORBQ_F32 = 0, ORBQ_BF16 = 1, ORBQ_F16 = 2 } orbq_dtype;
 
 /* Activation applied to the product before it is stored (Nunchaku / SVDQuant in Diffusers,
  * ai-papers.net, section on quantizing one's own model: GELU fused with the MLP).  The
@@ -265,6 +267,127 @@ int orbq_rpbh_flatness(const void* X, int64_t n, int64_t d, int64_t ldx, float* 
  * count is a per-layer choice, not a per-token one.  Negative statistics or d < 2:
  * ORBQ_ERR_INVALID_ARG. */
 int32_t orbq_rht_passes(float rho3, float rhoinf, int32_t d, int32_t vector_quantization);
+
+/* ==== attention-side operators ================================================================
+ * What a transformer block has between its quantized QKV projection and its quantized output
+ * projection: rotary positions over several axes, a key/value cache in 8 bits, attention over it.
+ *
+ * Head tensors are [token][head][head_dim] with the last dimension contiguous and any
+ * non-negative token and head strides (in elements), so the parts of a fused projection are taken
+ * where they lie.
+ * Packed rows: the rows of a batch lie one sequence after the other; sequence b has rows
+ * cu[b] .. cu[b + 1] - 1 (cu [device] int32[batch + 1], ascending from 0 to `total`; NULL: total / batch
+ * rows each).  The counts live on the device, so a captured graph follows them; the host gives
+ * their bound (max_new, max_tokens), and rows of a sequence beyond it are not processed.
+ * Device arrays of indices are read, never validated: a sequence's rows are kept inside [0, total),
+ * a page outside [0, num_pages) or beyond max_pages is taken as absent (nothing written; read as
+ * zero; not attended to), so a wrong table gives wrong results but no access out of bounds. */
+
+/* Rotary positions with several axes (time, height, width of image and video tokens).
+ *   axes    1..4;  dims[a]: entries of a head that axis a turns, even, in order from entry 0;
+ *           R = sum dims <= head_dim, entries R .. head_dim - 1 pass through
+ *   freqs   [device] float[R / 2], radians per unit of position for each pair, axis after axis
+ *   layout  ORBQ_ROPE_PAIRS: pair i is entries (2 i, 2 i + 1);
+ *           ORBQ_ROPE_HALVES: entries (i, i + R / 2) */
+typedef enum { ORBQ_ROPE_PAIRS = 0, ORBQ_ROPE_HALVES = 1 } orbq_rope_layout;
+typedef struct {
+  int32_t axes;
+  int32_t dims[4];
+  const float* freqs;
+  orbq_rope_layout layout;
+} orbq_rope;
+
+/* One head tensor, read at x and written at y (y == x with the same strides: in place; any other
+ * overlap is undefined). */
+typedef struct {
+  const void* x;
+  void* y;
+  int32_t heads;
+  int64_t x_token, x_head, y_token, y_head;
+} orbq_heads;
+
+/* (a, b) -> (a cos t - b sin t, a sin t + b cos t) for pair i of axis A of every head, with
+ * t = positions[token % n_positions][A] * freqs[i]; evaluated in fp32 from an angle reduced in 64 bits,
+ * rounded once.
+ *   positions [device] float[n_positions][axes], whole or fractional; n_positions divides n (a batch of
+ *             equal grids shares one set)
+ *   tensors   [host] 1 or 2 head tensors (q and k in one launch), each with its own number of heads
+ *   inverse   non-zero turns by -t: the transpose of the forward map, so applied to the gradients of the
+ *             outputs it gives the gradients of the inputs
+ * head_dim even, at most 512; type f32, bf16 or f16.  Addresses and strides need the type's own
+ * alignment; 16-byte columns are used where all of them allow it. */
+int orbq_rope_apply(const orbq_rope* rope, const float* positions, int64_t n_positions, int64_t n, int32_t head_dim,
+                    const orbq_heads* tensors, int32_t count, orbq_dtype type, int32_t inverse, void* stream);
+
+/* The 8-bit paged cache.  Page p holds page_tokens tokens of one sequence; each (page, head) has one
+ * fp32 scale for keys and one for values; an entry is code * scale.
+ *   k_codes  [device] int8[num_pages][kv_heads][page_tokens][head_dim], 16-byte aligned
+ *   v_codes  [device] int8[num_pages][kv_heads][head_dim][page_tokens], 16-byte aligned (the order in which
+ *            attention's second product takes its operand)
+ *   k_scales, v_scales  [device] float[num_pages][kv_heads], positive (orbq_kv_attention takes a value scale
+ *            below 2^-64 as 2^-64, the least that orbq_kv_append writes)
+ * page_tokens in {16, 32, 64, 128}, head_dim in {64, 128, 256}.  No buffer needs to be initialised. */
+typedef struct {
+  int8_t* k_codes;
+  int8_t* v_codes;
+  float* k_scales;
+  float* v_scales;
+  int32_t num_pages, kv_heads, page_tokens, head_dim;
+} orbq_kv_cache;
+
+/* table [device] int32[batch][ld]: page of tokens i * page_tokens .. of each sequence, i < max_pages <= ld.
+ * max_pages * page_tokens at most 2^30, batch at most 65535.  Sequences may share pages that are only
+ * read; a page that orbq_kv_append writes belongs to one sequence. */
+typedef struct {
+  const int32_t* table;
+  int64_t ld;
+  int32_t max_pages, batch;
+} orbq_page_table;
+
+/* Writes new tokens behind the start[b] ([device] int32[batch]) tokens that sequence b holds.  For each
+ * page and head touched: A = the largest finite magnitude among the new entries,
+ * need = max(A * (1/127), 2^-64); the scale is `need` on a page without earlier tokens, else the old
+ * one if need <= old, else max(need, 1.25 old), and then the page's earlier codes become
+ * rint(code * (old / scale)) (over any number of such steps at most 2.5 steps of the last scale are lost).
+ * code = rint(x * (1 / scale)) clamped to +-127 (ties to even, fp32); a NaN is written as code 0, an
+ * infinity as +-127.  The result does not depend on how the work is scheduled.
+ *   k, v  [device] head tensors of `total` packed rows, type f32, bf16 or f16, addresses and strides
+ *         multiples of 16 bytes
+ *   max_new  no sequence has more new tokens */
+int orbq_kv_append(const orbq_kv_cache* cache, const orbq_page_table* table, const int32_t* start, const int32_t* cu,
+                   int64_t total, int32_t max_new, const void* k, int64_t k_token, int64_t k_head, const void* v,
+                   int64_t v_token, int64_t v_head, orbq_dtype type, void* stream);
+
+/* Reads tokens first[b] .. of each sequence (cu gives how many) back as code * scale, rounded to `type`.
+ *   k, v  [device] head tensors of `total` packed rows, written; addresses and strides multiples of 16 bytes */
+int orbq_kv_read(const orbq_kv_cache* cache, const orbq_page_table* table, const int32_t* first, const int32_t* cu,
+                 int64_t total, int32_t max_tokens, void* k, int64_t k_token, int64_t k_head, void* v, int64_t v_token,
+                 int64_t v_head, orbq_dtype type, void* stream);
+
+/* Attention of packed queries over the cache: O = softmax(scale q K^T) V over each query's visible
+ * tokens.  Query i of the n of sequence b stands at position lens[b] - n + i, so the cache holds
+ * the queries' own tokens already (orbq_kv_append first).  Visible are tokens lo <= j < hi:
+ *   hi = lens[b] with causal_block = 0; else min(lens[b], (position / causal_block + 1) * causal_block), and 0 at
+ *        a negative position (1: causal; tokens a frame: each frame sees itself and earlier ones)
+ *   lo = max(0, hi - window), or 0 with window = 0
+ * A query that sees nothing gets O = 0, lse = -infinity.  Tokens that are not visible have no influence,
+ * whatever their codes and scales hold.
+ *   lens  [device] int32[batch], tokens held (kept inside [0, max_pages * page_tokens])
+ *   q, o  [device] head tensors of `total` packed rows and `heads` heads, bf16 or f16; heads a multiple of
+ *         kv_heads, query head h reads cache head h / (heads / kv_heads).  q 16-byte, o 8-byte addresses
+ *         and strides.  Products on the codes in f16 with fp32 accumulation, softmax in fp32.
+ *   lse   [device] float[total][heads] or NULL: natural log of the sum of exponentials
+ *   max_new  bound of the queries of a sequence;  max_len  expected bound of lens (0: the page table's);
+ *         it only chooses how the work is split, any value gives the same result up to rounding
+ *   workspace [device] >= orbq_kv_attention_workspace_bytes of the same arguments (max_len given as used:
+ *         the page table's bound if 0), 256-byte aligned, where that is not 0: parts of split sequences
+ * Few queries take a form bound by the cache's bytes, many one bound by the matrix cores. */
+size_t orbq_kv_attention_workspace_bytes(const orbq_kv_cache* cache, int32_t batch, int64_t total, int32_t max_new,
+                                         int32_t heads, int64_t max_len, int32_t causal_block, int32_t window);
+int orbq_kv_attention(const orbq_kv_cache* cache, const orbq_page_table* table, const int32_t* lens, const int32_t* cu,
+                      int64_t total, int32_t max_new, int64_t max_len, const void* q, int64_t q_token, int64_t q_head,
+                      int32_t heads, void* o, int64_t o_token, int64_t o_head, float* lse, orbq_dtype type, float scale,
+                      int32_t causal_block, int32_t window, void* workspace, size_t ws_bytes, void* stream);
 
 /* Human-readable name of a status code, and the detail of the last error on this thread. */
 const char* orbq_status_string(int status);
