@@ -123,8 +123,8 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
 __device__ __forceinline__ void block_scales(const AttnArgs& a, int64_t slot, float* c, float* lv, float* iv) {
   *c = a.c.ks[slot] * a.scale_log2e;
   const float v = __builtin_fmaxf(a.c.vs[slot], kScaleFloor);
-  *lv = __builtin_log2f(v);
-  *iv = 1.0f / v;
+  *lv = __builtin_amdgcn_logf(v);  // log2, exact to a unit of its last place for a normal number
+  *iv = __builtin_amdgcn_rcpf(v);
 }
 
 __device__ __forceinline__ void store4(const AttnArgs& a, int64_t at, f32x4_t v) {
@@ -376,7 +376,7 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
 
 // ----------------------------------------------------------------------------------------- many
 template <int D> struct Many {
-  static constexpr int kWaves = 4, kRows = 32 * kWaves, kThreads = 64 * kWaves;
+  static constexpr int kWaves = D == 128 ? 8 : 4, kRows = 32 * kWaves, kThreads = 64 * kWaves;
   // LDS of one tile in 16-byte pieces: keys [d / 8][64 + 1], values [8][d + 2] (pieces of 8 keys).
   // A wave's operand reads are 32 consecutive pieces; the pitches spread the writers over banks.
   static constexpr int kKPitch = 65, kVPitch = D + 2;
@@ -467,39 +467,40 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, D <= 128 ? 2 : 
 
   // staging: 16 codes a load; keys (key, 16 entries), values (entry, 16 keys)
   const int page_mask = a.c.page - 1;
+  const int32_t* table = a.c.table + b * a.c.ldt;
   u32x4_t kr[NL], vr[NL];
   int kpg[NL], vpg;
   float sc[3];
+  // Loads never branch: where a block is absent the first of the cache is read, and its weight is zero.
+  const int64_t block_bytes = static_cast<int64_t>(D) * a.c.page;
+  const auto page_at = [&](int key) {  // the table's entry for a key of this sequence, -1: absent
+    const int p = key >> a.page_shift;
+    const int32_t pg = table[p < a.c.max_pages ? p : a.c.max_pages - 1];
+    return key < s.len && static_cast<uint32_t>(pg) < static_cast<uint32_t>(a.c.pages) ? pg : -1;
+  };
   const auto pages = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int key = 64 * t + (i * NT + tid) / (D / 16);
-      kpg[i] = t < t1 && key < s.len ? page_of(a.c, b, key >> a.page_shift) : -1;
-    }
-    const int key = 64 * t + 16 * (tid & 3);
-    vpg = t < t1 && key < s.len ? page_of(a.c, b, key >> a.page_shift) : -1;
+    for (int i = 0; i < NL; ++i) kpg[i] = page_at(64 * t + (i * NT + tid) / (D / 16));
+    vpg = page_at(64 * t + 16 * (tid & 3));
+  };
+  const auto block_of = [&](int pg) {  // (pg heads + kvh) blocks, pg < 0 as 0
+    return (static_cast<uint64_t>(static_cast<uint32_t>(pg < 0 ? 0 : pg)) * static_cast<uint32_t>(a.c.heads) + kvh) * block_bytes;
   };
   const auto load = [&](int t) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       const int at = i * NT + tid, key = 64 * t + at / (D / 16), u = at % (D / 16);
-      kr[i] = u32x4_t{0, 0, 0, 0};
-      if (kpg[i] >= 0)
-        kr[i] = *reinterpret_cast<const u32x4_t*>(
-            a.c.k + ((static_cast<int64_t>(kpg[i]) * a.c.heads + kvh) * a.c.page + (key & page_mask)) * D + 16 * u);
+      kr[i] = *reinterpret_cast<const u32x4_t*>(a.c.k + block_of(kpg[i]) + (key & page_mask) * D + 16 * u);
     }
+    const int8_t* v = a.c.v + block_of(vpg) + ((64 * t + 16 * (tid & 3)) & page_mask) + (tid >> 2) * a.c.page;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int d = (i * NT + tid) >> 2;
-      vr[i] = u32x4_t{0, 0, 0, 0};
-      if (vpg >= 0)
-        vr[i] = *reinterpret_cast<const u32x4_t*>(
-            a.c.v + ((static_cast<int64_t>(vpg) * a.c.heads + kvh) * D + d) * a.c.page + ((64 * t + 16 * (tid & 3)) & page_mask));
-    }
+    for (int i = 0; i < NL; ++i) vr[i] = *reinterpret_cast<const u32x4_t*>(v + (i * NT / 4) * a.c.page);
     if (tid < 4) {
-      sc[0] = sc[2] = 0.0f;
-      sc[1] = -__builtin_inff();  // a block that is absent has no weight
-      if (vpg >= 0) block_scales(a, static_cast<int64_t>(vpg) * a.c.heads + kvh, &sc[0], &sc[1], &sc[2]);
+      block_scales(a, static_cast<int64_t>(vpg < 0 ? 0 : vpg) * a.c.heads + kvh, &sc[0], &sc[1], &sc[2]);
+      if (vpg < 0) {  // a block that is absent has no weight
+        sc[0] = sc[2] = 0.0f;
+        sc[1] = -__builtin_inff();
+      }
     }
   };
   const auto stage = [&](int buf) {
@@ -546,16 +547,8 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, D <= 128 ? 2 : 
         st[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k1, q[i], st[1], 0, 0, 0);
       }
       // register 8 (g & 1) + 4 k + j of st[g / 2]: key 16 g + 8 k + 4 hi32 + j
-      float top = -__builtin_inff();
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float c = lsc[buf][g][0] * qs, v = lsc[buf][g][1];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          st[g >> 1][8 * (g & 1) + j] = __builtin_fmaf(st[g >> 1][8 * (g & 1) + j], c, v);
-        }
-      }
       if (64 * t < all_lo || 64 * t + 64 > all_hi) {
+        asm volatile("; masked tile");  // keeps this a branch: few tiles take it
 #pragma unroll
         for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -564,8 +557,18 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, D <= 128 ? 2 : 
             if (key < lo || key >= hi) st[g >> 1][8 * (g & 1) + j] = -__builtin_inff();
           }
       }
+      // c is positive (a factor of zero is taken as the least normal number, so that a masked score stays
+      // at -infinity): a block's largest weight is its largest score's
+      float c[4], v[4], top = -__builtin_inff();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) top = __builtin_fmaxf(top, __builtin_fmaxf(st[0][j], st[1][j]));
+      for (int g = 0; g < 4; ++g) {
+        c[g] = __builtin_fmaxf(lsc[buf][g][0] * qs, 0x1p-126f);
+        v[g] = lsc[buf][g][1];
+        float x = st[g >> 1][8 * (g & 1)];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) x = __builtin_fmaxf(x, st[g >> 1][8 * (g & 1) + j]);
+        top = __builtin_fmaxf(top, __builtin_fmaf(x, c[g], v[g]));
+      }
       top = __builtin_fmaxf(top, __shfl_xor(top, 32));
       if (__any(top > m + kSlack)) {
         const float mn = __builtin_fmaxf(m, top), by = exp2_fast(m - mn);
@@ -577,10 +580,11 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, D <= 128 ? 2 : 
       half8_t p[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
+        const float y = v[g] - m;
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float w = exp2_fast(st[g >> 1][8 * (g & 1) + j] - m);
+          const float w = exp2_fast(__builtin_fmaf(st[g >> 1][8 * (g & 1) + j], c[g], y));
           sum += w;
           p[g][j] = static_cast<_Float16>(w);
         }
