@@ -80,6 +80,9 @@ struct AttnArgs {
   float* part_ml;                    // [total * heads][splits][2]
 };
 
+// rows of a workgroup in the form for many rows, 32 a wave
+constexpr int many_rows(int d) { return d == 128 ? 256 : 128; }
+
 struct AttnPlan {
   int32_t many;    // the form for many rows (else few)
   int32_t rt;      // few: 16-row tiles a workgroup

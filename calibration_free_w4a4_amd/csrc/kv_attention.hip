@@ -15,7 +15,7 @@ AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t k
   const int64_t rows = static_cast<int64_t>(max_new) * (heads / kv_heads);
   p.many = rows > 32;
   p.rt = rows > 16 ? 2 : 1;
-  const int tile_rows = p.many ? 128 : 16 * p.rt;
+  const int tile_rows = p.many ? many_rows(d) : 16 * p.rt;
   p.row_tiles = static_cast<int32_t>((rows + tile_rows - 1) / tile_rows);
   // the keys that one row tile can see, in 64-key tiles
   int64_t span = max_len;
@@ -27,7 +27,6 @@ AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t k
   if (groups < want) splits = std::min((want + groups - 1) / groups, (tiles + least - 1) / least);
   p.chunk = static_cast<int32_t>((tiles + splits - 1) / splits);
   p.splits = static_cast<int32_t>((tiles + p.chunk - 1) / p.chunk);
-  (void)d;
   return p;
 }
 

@@ -119,12 +119,13 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
   return s;
 }
 
-// one value a lane that covers a block's keys: c = ks |scale| log2(e), log2(vs), 1/vs
-__device__ __forceinline__ void block_scales(const AttnArgs& a, int64_t slot, float* c, float* lv, float* iv) {
-  *c = a.c.ks[slot] * a.scale_log2e;
-  const float v = __builtin_fmaxf(a.c.vs[slot], kScaleFloor);
-  *lv = __builtin_amdgcn_logf(v);  // log2, exact to a unit of its last place for a normal number
-  *iv = __builtin_amdgcn_rcpf(v);
+// one value a lane that covers a block's keys: c = ks |scale| log2(e), log2(vs), 1/vs; a block that is absent
+// has no weight
+__device__ __forceinline__ void block_scales(const AttnArgs& a, float ks, float vs, bool have, float* c, float* lv, float* iv) {
+  const float v = __builtin_fmaxf(vs, kScaleFloor);
+  *c = have ? ks * a.scale_log2e : 0.0f;
+  *lv = have ? __builtin_amdgcn_logf(v) : -__builtin_inff();  // log2, exact to a unit of its last place for a normal number
+  *iv = have ? __builtin_amdgcn_rcpf(v) : 0.0f;
 }
 
 __device__ __forceinline__ void store4(const AttnArgs& a, int64_t at, f32x4_t v) {
@@ -230,19 +231,14 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
     for (int i = 0; i < ND; ++i)
       vr[i] = pg >= 0 ? *reinterpret_cast<const u32x4_t*>(p + static_cast<int64_t>(16 * i) * a.c.page) : u32x4_t{0, 0, 0, 0};
   };
-  const auto load_s = [&](int pg, float* c, float* lv, float* iv) {
-    *c = *iv = 0.0f;
-    *lv = -__builtin_inff();  // a block that is absent has no weight
-    if (pg >= 0) block_scales(a, static_cast<int64_t>(pg) * a.c.heads + kvh, c, lv, iv);
-  };
-
   int t = t0 + wave;
   pages(t, &kpg, &vpg);
   load_k(t, kpg);
   for (; t < t1; t += kFewWaves) {
     load_v(t, vpg);
-    float sc, lv, iv;
-    load_s(vpg, &sc, &lv, &iv);
+    const bool have = vpg >= 0;
+    const int64_t slot = static_cast<int64_t>(have ? vpg : 0) * a.c.heads + kvh;
+    const float ks = a.c.ks[slot], vs = a.c.vs[slot];
     pages(t + kFewWaves, &kpg, &vpg);
     // S^T: accumulator register 4 i + j of this lane is key 16 g + 4 i + j of row l15
     f32x4_t st[RT][4];
@@ -261,6 +257,8 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
       }
     }
     load_k(t + kFewWaves, kpg);
+    float sc, lv, iv;
+    block_scales(a, ks, vs, have, &sc, &lv, &iv);
     const bool whole = 64 * t >= lo_most && 64 * t + 64 <= hi_least;
     half8_t p[RT][2];
 #pragma unroll
@@ -376,74 +374,100 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
 
 // ----------------------------------------------------------------------------------------- many
 template <int D> struct Many {
-  static constexpr int kWaves = D == 128 ? 8 : 4, kRows = 32 * kWaves, kThreads = 64 * kWaves;
+  static constexpr int kRows = many_rows(D), kWaves = kRows / 32, kThreads = 64 * kWaves;
   // LDS of one tile in 16-byte pieces: keys [d / 8][64 + 1], values [8][d + 2] (pieces of 8 keys).
   // A wave's operand reads are 32 consecutive pieces; the pitches spread the writers over banks.
   static constexpr int kKPitch = 65, kVPitch = D + 2;
   static constexpr int kKPieces = D / 8 * kKPitch, kVPieces = 8 * kVPitch;
-  static constexpr int kLoads = D / (16 * kWaves);  // 16-byte loads a thread, keys; values the same
+  static constexpr int kLoads = 4 * D / kThreads;  // 16-byte loads a thread for a tile's keys, and for its values
 };
 
-template <int D> __global__ __launch_bounds__(Many<D>::kThreads, D <= 128 ? 2 : 1) void k_many(const AttnArgs a, int streams) {
+struct Factors {  // of each 16 keys of a tile: on raw scores, log2 of the value scale, 1 / value scale
+  float c[4], lv[4], iv[4];
+};
+
+// One workgroup's rows, its part of the keys, and one wave's 32 rows of them: lane l31 of either half
+// holds row l31.  Everything here is inlined; the members live in registers.
+template <int D> struct ManyRows {
   using M = Many<D>;
-  constexpr int NL = M::kLoads, NT = M::kThreads, NS = D / 16, ND = D / 32;
-  __shared__ __attribute__((aligned(16))) half8_t lk[2][M::kKPieces], lv[2][M::kVPieces];
-  __shared__ float lsc[2][4][3];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l31 = lane & 31, hi32 = lane >> 5;
-
-  // Workgroups are given out to the eight dies in turn: the row tiles of one stream (sequence, head,
-  // split) go to one die, whose L2 then reads their keys and values once; a launch of few streams is
-  // spread tile by tile.  Long rows of a causal mask come first.
-  int stream, tile;
-  if (streams >= 16) {
-    const int total = streams * a.row_tiles, per = (total + 7) >> 3;
-    const int lin = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (lin >= total || static_cast<int>(blockIdx.x >> 3) >= per) return;
-    stream = lin / a.row_tiles;
-    tile = lin - stream * a.row_tiles;
-  } else {
-    if (static_cast<int>(blockIdx.x) >= streams * a.row_tiles) return;
-    tile = blockIdx.x / streams;
-    stream = blockIdx.x - tile * streams;
-  }
-  tile = a.row_tiles - 1 - tile;
-  const int split = stream % a.splits, kvh = stream / a.splits % a.c.heads, b = stream / a.splits / a.c.heads;
-  const Seq s = seq_of(a, b);
-  const int64_t all = static_cast<int64_t>(s.rows) * a.group;
-  const int64_t r0 = static_cast<int64_t>(tile) * M::kRows;
-  if (r0 >= all) return;
-  const int64_t r1 = r0 + M::kRows < all ? r0 + M::kRows : all;
-  const int64_t base = static_cast<int64_t>(s.len) - s.rows;
-
-  int32_t first, last, x0, x1;
-  visible(a, base + r0 / a.group, s.len, &first, &x0);
-  visible(a, base + (r1 - 1) / a.group, s.len, &x1, &last);
-  const int t_first = first / 64, t_end = (last + 63) / 64;
-  const int t0 = t_first + split * a.chunk;
-  const int t1 = split + 1 < a.splits && t0 + a.chunk < t_end ? t0 + a.chunk : t_end;
-
-  // this lane's row
-  const int64_t row_local = r0 + 32 * wave + l31;
-  const bool live = row_local < r1;
-  const int64_t rr = live ? row_local : r0;
-  const int64_t tok = rr / a.group;
-  const int h = kvh * a.group + static_cast<int>(rr - tok * a.group);
-  const int64_t row = (s.row0 + tok) * a.heads + h;
-  int32_t lo, hi;
-  visible(a, base + tok, s.len, &lo, &hi);
-  if (!live) hi = 0;
-  // the wave's: keys from any_lo to any_hi are visible to some row, from all_lo to all_hi to all
-  int32_t any_lo, any_hi, all_lo, all_hi;
-  {
-    const int64_t w0 = r0 + 32 * wave < r1 ? r0 + 32 * wave : r1 - 1, w1 = r0 + 32 * wave + 31 < r1 ? r0 + 32 * wave + 31 : r1 - 1;
-    visible(a, base + w0 / a.group, s.len, &any_lo, &all_hi);
-    visible(a, base + w1 / a.group, s.len, &all_lo, &any_hi);
-    if (r0 + 32 * wave >= r1) any_hi = 0;
-  }
-
+  static constexpr int NS = D / 16, ND = D / 32, NL = M::kLoads;
+  const AttnArgs& a;
+  half8_t (*lk)[M::kKPieces];   // [2]: tile t in t & 1
+  half8_t (*lv)[M::kVPieces];   // [2]
+  f32x4_t (*lsc)[4];            // [4]: tile t in t & 3; for each 16 keys ks |scale| log2(e), log2(vs), 1 / vs
+  int tid, wave, lane, l31, hi32;
+  int b, kvh, split, h;
+  Seq s;
+  bool live;
+  int64_t tok, row;
+  int t0, t1;                   // 64-key tiles of this workgroup
+  int32_t lo, hi;               // this lane's visible keys
+  int32_t all_lo, all_hi;       // keys from all_lo to all_hi are visible to all rows of this wave
   half8_t q[NS];
-  float qs;
-  {
+  float qs, m, l;
+  f32x16_t o[ND];
+  // staging
+  const int32_t* table;
+  int64_t block_bytes;
+  int page_mask;
+  uint32_t k_off[NL], v_off[NL];
+  u32x4_t kr[NL], vr[NL];
+  int kpg[NL], vpg, spg;        // table entries of the next tiles' keys, values and scales
+  float ks, vs;                 // scales of the keys to stage next, of 16 keys a lane (tid < 4)
+  bool have;
+
+  __device__ __forceinline__ ManyRows(const AttnArgs& args, half8_t (*k)[M::kKPieces], half8_t (*v)[M::kVPieces], f32x4_t (*sc4)[4])
+      : a(args), lk(k), lv(v), lsc(sc4) {}
+
+  // false: this workgroup has no rows
+  __device__ __forceinline__ bool begin(int streams) {
+    tid = threadIdx.x;
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    lane = tid & 63;
+    l31 = tid & 31;
+    hi32 = (tid >> 5) & 1;
+    // Workgroups are given out to the eight dies in turn: the row tiles of one stream (sequence, head,
+    // split) go to one die, whose L2 then reads their keys and values once; a launch of few streams is
+    // spread tile by tile.  Long rows of a causal mask come first.
+    int stream, tile;
+    if (streams >= 16) {
+      const int total = streams * a.row_tiles, per = (total + 7) >> 3;
+      const int lin = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+      if (lin >= total || static_cast<int>(blockIdx.x >> 3) >= per) return false;
+      stream = lin / a.row_tiles;
+      tile = lin - stream * a.row_tiles;
+    } else {
+      if (static_cast<int>(blockIdx.x) >= streams * a.row_tiles) return false;
+      tile = blockIdx.x / streams;
+      stream = blockIdx.x - tile * streams;
+    }
+    tile = a.row_tiles - 1 - tile;
+    split = stream % a.splits;
+    kvh = stream / a.splits % a.c.heads;
+    b = stream / a.splits / a.c.heads;
+    s = seq_of(a, b);
+    const int64_t all = static_cast<int64_t>(s.rows) * a.group, r0 = static_cast<int64_t>(tile) * M::kRows;
+    if (r0 >= all) return false;
+    const int64_t r1 = r0 + M::kRows < all ? r0 + M::kRows : all;
+    const int64_t base = static_cast<int64_t>(s.len) - s.rows;
+    int32_t first, last, x;
+    visible(a, base + r0 / a.group, s.len, &first, &x);
+    visible(a, base + (r1 - 1) / a.group, s.len, &x, &last);
+    const int t_end = (last + 63) / 64;
+    t0 = first / 64 + split * a.chunk;
+    t1 = split + 1 < a.splits && t0 + a.chunk < t_end ? t0 + a.chunk : t_end;
+    const int64_t mine = r0 + 32 * wave + l31;
+    live = mine < r1;
+    const int64_t rr = live ? mine : r0;
+    tok = rr / a.group;
+    h = kvh * a.group + static_cast<int>(rr - tok * a.group);
+    row = (s.row0 + tok) * a.heads + h;
+    visible(a, base + tok, s.len, &lo, &hi);
+    if (!live) hi = 0;
+    const int64_t w0 = r0 + 32 * wave < r1 ? r0 + 32 * wave : r1 - 1, w1 = r0 + 32 * wave + 31 < r1 ? r0 + 32 * wave + 31 : r1 - 1;
+    visible(a, base + w0 / a.group, s.len, &x, &all_hi);
+    visible(a, base + w1 / a.group, s.len, &all_lo, &x);
+
     const int64_t at = (s.row0 + tok) * a.qt + h * a.qh;
     float most = 0.0f;
 #pragma unroll
@@ -456,179 +480,290 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, D <= 128 ? 2 : 
     const float by = (a.negative ? -1.0f : 1.0f) / qs;
 #pragma unroll
     for (int i = 0; i < NS; ++i) q[i] = q_scaled(q[i], a.f16, by);
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+    m = kNone;
+    l = 0.0f;
+    table = a.c.table + b * a.c.ldt;
+    block_bytes = static_cast<int64_t>(D) * a.c.page;
+    page_mask = a.c.page - 1;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int at = i * M::kThreads + tid;
+      k_off[i] = (at / (D / 16) & 15) * D + at % (D / 16) * 16;
+      v_off[i] = entry_of(i) * a.c.page;
+    }
+    return true;
   }
 
-  f32x16_t o[ND];
-#pragma unroll
-  for (int i = 0; i < ND; ++i)
-#pragma unroll
-    for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-  float m = kNone, l = 0.0f;
-
-  // staging: 16 codes a load; keys (key, 16 entries), values (entry, 16 keys)
-  const int page_mask = a.c.page - 1;
-  const int32_t* table = a.c.table + b * a.c.ldt;
-  u32x4_t kr[NL], vr[NL];
-  int kpg[NL], vpg;
-  float sc[3];
-  // Loads never branch: where a block is absent the first of the cache is read, and its weight is zero.
-  const int64_t block_bytes = static_cast<int64_t>(D) * a.c.page;
-  const auto page_at = [&](int key) {  // the table's entry for a key of this sequence, -1: absent
+  // Loads of a tile: 16 codes each; keys (key, 16 entries), values (entry, 16 keys).  A wave's load stays
+  // within 16 keys, so its page is one scalar and its address one scalar and an offset that never
+  // changes.  Nothing branches: where a block is absent the first of the cache is read, and its weight is
+  // zero.  The table's entries are loaded a tile earlier and judged when they are used, so that no load is
+  // waited for where it is issued.
+  __device__ __forceinline__ int entry(int key) const {
     const int p = key >> a.page_shift;
-    const int32_t pg = table[p < a.c.max_pages ? p : a.c.max_pages - 1];
-    return key < s.len && static_cast<uint32_t>(pg) < static_cast<uint32_t>(a.c.pages) ? pg : -1;
-  };
-  const auto pages = [&](int t) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) kpg[i] = page_at(64 * t + (i * NT + tid) / (D / 16));
-    vpg = page_at(64 * t + 16 * (tid & 3));
-  };
-  const auto block_of = [&](int pg) {  // (pg heads + kvh) blocks, pg < 0 as 0
-    return (static_cast<uint64_t>(static_cast<uint32_t>(pg < 0 ? 0 : pg)) * static_cast<uint32_t>(a.c.heads) + kvh) * block_bytes;
-  };
-  const auto load = [&](int t) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int at = i * NT + tid, key = 64 * t + at / (D / 16), u = at % (D / 16);
-      kr[i] = *reinterpret_cast<const u32x4_t*>(a.c.k + block_of(kpg[i]) + (key & page_mask) * D + 16 * u);
-    }
-    const int8_t* v = a.c.v + block_of(vpg) + ((64 * t + 16 * (tid & 3)) & page_mask) + (tid >> 2) * a.c.page;
-#pragma unroll
-    for (int i = 0; i < NL; ++i) vr[i] = *reinterpret_cast<const u32x4_t*>(v + (i * NT / 4) * a.c.page);
-    if (tid < 4) {
-      block_scales(a, static_cast<int64_t>(vpg < 0 ? 0 : vpg) * a.c.heads + kvh, &sc[0], &sc[1], &sc[2]);
-      if (vpg < 0) {  // a block that is absent has no weight
-        sc[0] = sc[2] = 0.0f;
-        sc[1] = -__builtin_inff();
-      }
-    }
-  };
-  const auto stage = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int at = i * NT + tid, key = at / (D / 16), u = at % (D / 16);
-      lk[buf][(2 * u) * M::kKPitch + key] = codes_to_half8(kr[i][0], kr[i][1]);
-      lk[buf][(2 * u + 1) * M::kKPitch + key] = codes_to_half8(kr[i][2], kr[i][3]);
-    }
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int at = i * NT + tid, d = at >> 2, g = at & 3;
-      // keys 0-3 and 8-11 of the sixteen, then 4-7 and 12-15: as the weights lie in their registers
-      lv[buf][(2 * g) * M::kVPitch + d] = codes_to_half8(vr[i][0], vr[i][2]);
-      lv[buf][(2 * g + 1) * M::kVPitch + d] = codes_to_half8(vr[i][1], vr[i][3]);
-    }
-    if (tid < 4) {
-#pragma unroll
-      for (int i = 0; i < 3; ++i) lsc[buf][tid][i] = sc[i];
-    }
-  };
-
-  if (t0 < t1) {
-    pages(t0);
-    load(t0);
-    pages(t0 + 1);
-    stage(0);
+    return table[p < a.c.max_pages ? p : a.c.max_pages - 1];
   }
-  __syncthreads();
-  int buf = 0;
-  for (int t = t0; t < t1; ++t, buf ^= 1) {
-    if (t + 1 < t1) {
-      load(t + 1);
-      pages(t + 2);
+  __device__ __forceinline__ bool present(int pg, int key) const {
+    return key < s.len && static_cast<uint32_t>(pg) < static_cast<uint32_t>(a.c.pages);
+  }
+  __device__ __forceinline__ uint64_t slot_of(int pg, int key) const {  // pg heads + kvh, an absent block as page 0
+    return static_cast<uint64_t>(present(pg, key) ? static_cast<uint32_t>(pg) : 0u) * static_cast<uint32_t>(a.c.heads) + kvh;
+  }
+  // first of the 16 keys that hold this wave's load i of keys, and of its loads of values
+  __device__ __forceinline__ int key_of(int t, int i) const { return 64 * t + ((i * M::kWaves + wave) * (1024 / D) & ~15); }
+  __device__ __forceinline__ int val_of(int t) const { return 64 * t + 16 * (wave & 3); }
+  // entry of this thread's load i of values
+  __device__ __forceinline__ int entry_of(int i) const { return 64 * (i * (M::kWaves / 4) + (wave >> 2)) + lane; }
+  __device__ __forceinline__ void pages_k(int t) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) kpg[i] = entry(key_of(t, i));
+    if (wave == 0) spg = entry(64 * t + 16 * (lane & 3));
+  }
+  __device__ __forceinline__ void pages_v(int t) { vpg = entry(val_of(t)); }
+  __device__ __forceinline__ void load_k(int t) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int key = key_of(t, i);
+      const int8_t* p = a.c.k + slot_of(kpg[i], key) * block_bytes + (key & page_mask) * D;
+      kr[i] = *reinterpret_cast<const u32x4_t*>(p + k_off[i]);
     }
-    if (64 * t < any_hi && 64 * t + 64 > any_lo) {
-      f32x16_t st[2];
+    if (wave == 0) {
+      const int key = 64 * t + 16 * (lane & 3);
+      const uint64_t slot = slot_of(spg, key);
+      ks = a.c.ks[slot];
+      vs = a.c.vs[slot];
+      have = present(spg, key);
+    }
+  }
+  __device__ __forceinline__ void load_v(int t) {
+    const int key = val_of(t);
+    const int8_t* p = a.c.v + slot_of(vpg, key) * block_bytes + (key & page_mask);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) st[0][j] = st[1][j] = 0.0f;
+    for (int i = 0; i < NL; ++i) vr[i] = *reinterpret_cast<const u32x4_t*>(p + v_off[i]);
+  }
+  __device__ __forceinline__ void stage_k(int t) {
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const half8_t k0 = lk[buf][(2 * i + hi32) * M::kKPitch + l31], k1 = lk[buf][(2 * i + hi32) * M::kKPitch + 32 + l31];
-        st[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k0, q[i], st[0], 0, 0, 0);
-        st[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k1, q[i], st[1], 0, 0, 0);
-      }
-      // register 8 (g & 1) + 4 k + j of st[g / 2]: key 16 g + 8 k + 4 hi32 + j
-      if (64 * t < all_lo || 64 * t + 64 > all_hi) {
-        asm volatile("; masked tile");  // keeps this a branch: few tiles take it
+    for (int i = 0; i < NL; ++i) {
+      const int at = i * M::kThreads + tid, key = at / (D / 16), u = at % (D / 16);
+      lk[t & 1][(2 * u) * M::kKPitch + key] = codes_to_half8(kr[i][0], kr[i][1]);
+      lk[t & 1][(2 * u + 1) * M::kKPitch + key] = codes_to_half8(kr[i][2], kr[i][3]);
+    }
+    if (tid < 4) {
+      float c, x, y;
+      block_scales(a, ks, vs, have, &c, &x, &y);
+      lsc[t & 3][tid] = f32x4_t{c, x, y, 0.0f};
+    }
+  }
+  __device__ __forceinline__ void stage_v(int t) {
+    const int g = wave & 3;
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+    for (int i = 0; i < NL; ++i) {
+      // keys 0-3 and 8-11 of the sixteen, then 4-7 and 12-15: as the weights lie in their registers
+      lv[t & 1][(2 * g) * M::kVPitch + entry_of(i)] = codes_to_half8(vr[i][0], vr[i][2]);
+      lv[t & 1][(2 * g + 1) * M::kVPitch + entry_of(i)] = codes_to_half8(vr[i][1], vr[i][3]);
+    }
+  }
+
+  // S^T of tile t: register 8 (g & 1) + 4 k + j of st[g / 2] is key 16 g + 8 k + 4 hi32 + j
+  __device__ __forceinline__ void scores(int t, f32x16_t* st) const {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int key = 64 * t + 16 * g + 8 * (j >> 2) + 4 * hi32 + (j & 3);
-            if (key < lo || key >= hi) st[g >> 1][8 * (g & 1) + j] = -__builtin_inff();
-          }
-      }
-      // c is positive (a factor of zero is taken as the least normal number, so that a masked score stays
-      // at -infinity): a block's largest weight is its largest score's
-      float c[4], v[4], top = -__builtin_inff();
+    for (int j = 0; j < 16; ++j) st[0][j] = st[1][j] = 0.0f;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        c[g] = __builtin_fmaxf(lsc[buf][g][0] * qs, 0x1p-126f);
-        v[g] = lsc[buf][g][1];
-        float x = st[g >> 1][8 * (g & 1)];
+    for (int i = 0; i < NS; ++i) {
+      const half8_t k0 = lk[t & 1][(2 * i + hi32) * M::kKPitch + l31], k1 = lk[t & 1][(2 * i + hi32) * M::kKPitch + 32 + l31];
+      st[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k0, q[i], st[0], 0, 0, 0);
+      st[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k1, q[i], st[1], 0, 0, 0);
+    }
+  }
+  // O^T += V^T w^T of tile t
+  __device__ __forceinline__ void values(int t, const half8_t* p) {
 #pragma unroll
-        for (int j = 1; j < 8; ++j) x = __builtin_fmaxf(x, st[g >> 1][8 * (g & 1) + j]);
-        top = __builtin_fmaxf(top, __builtin_fmaf(x, c[g], v[g]));
-      }
-      top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-      if (__any(top > m + kSlack)) {
-        const float mn = __builtin_fmaxf(m, top), by = exp2_fast(m - mn);
-        m = mn;
-        l *= by;
+    for (int g = 0; g < 4; ++g)
 #pragma unroll
-        for (int i = 0; i < ND; ++i) o[i] *= by;
-      }
-      half8_t p[4];
+      for (int i = 0; i < ND; ++i)
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lv[t & 1][(2 * g + hi32) * M::kVPitch + 32 * i + l31], p[g], o[i], 0, 0, 0);
+  }
+  // a block's factor on raw scores; positive (zero is taken as the least normal number, so that a masked
+  // score stays at -infinity), so that a block's largest weight is its largest score's
+  __device__ __forceinline__ float factor(float f) const { return __builtin_fmaxf(f * qs, 0x1p-126f); }
+  // masks tile t and finds the exponent of each row's largest weight in it
+  __device__ __forceinline__ float largest(int t, f32x16_t* st, Factors* f) const {
+    if (64 * t < all_lo || 64 * t + 64 > all_hi) {
+      asm volatile("; masked tile");  // keeps this a branch: few tiles take it
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float y = v[g] - m;
-        float sum = 0.0f;
+      for (int g = 0; g < 4; ++g)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float w = exp2_fast(__builtin_fmaf(st[g >> 1][8 * (g & 1) + j], c[g], y));
-          sum += w;
-          p[g][j] = static_cast<_Float16>(w);
+          const int key = 64 * t + 16 * g + 8 * (j >> 2) + 4 * hi32 + (j & 3);
+          if (key < lo || key >= hi) st[g >> 1][8 * (g & 1) + j] = -__builtin_inff();
         }
-        l = __builtin_fmaf(sum, lsc[buf][g][2], l);
-      }
-#pragma unroll
-      for (int i = 0; i < ND; ++i)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lv[buf][(2 * g + hi32) * M::kVPitch + 32 * i + l31], p[g], o[i], 0, 0, 0);
     }
-    if (t + 1 < t1) stage(buf ^ 1);
-    __syncthreads();
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f32x4_t x4 = lsc[t & 3][g];
+      f->c[g] = factor(x4[0]);
+      f->lv[g] = x4[1];
+      f->iv[g] = x4[2];
+      float x = st[g >> 1][8 * (g & 1)];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) x = __builtin_fmaxf(x, st[g >> 1][8 * (g & 1) + j]);
+      top = __builtin_fmaxf(top, __builtin_fmaf(x, f->c[g], f->lv[g]));
+    }
+    return __builtin_fmaxf(top, __shfl_xor(top, 32));
+  }
+  __device__ __forceinline__ void raise(float top) {
+    if (__any(top > m + kSlack)) {
+      const float mn = __builtin_fmaxf(m, top), by = exp2_fast(m - mn);
+      m = mn;
+      l *= by;
+#pragma unroll
+      for (int i = 0; i < ND; ++i) o[i] *= by;
+    }
+  }
+  __device__ __forceinline__ void weights(const f32x16_t* st, const Factors& f, half8_t* p) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float y = f.lv[g] - m;
+      float sum = 0.0f;  // of the weights before their rounding: the logarithm of l is an output in 32 bits
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float w = exp2_fast(__builtin_fmaf(st[g >> 1][8 * (g & 1) + j], f.c[g], y));
+        sum += w;
+        p[g][j] = static_cast<_Float16>(w);
+      }
+      l = __builtin_fmaf(sum, f.iv[g], l);
+    }
   }
 
-  l += __shfl_xor(l, 32);
-  if (!live) return;
-  // register 4 k + j of o[i]: entry 32 i + 8 k + 4 hi32 + j
-  if (a.splits > 1) {
-    float* po = a.part_o + (row * a.splits + split) * D;
-    if (l != 0.0f) {
+  __device__ __forceinline__ void finish() {
+    l += __shfl_xor(l, 32);
+    if (!live) return;
+    // register 4 k + j of o[i]: entry 32 i + 8 k + 4 hi32 + j
+    if (a.splits > 1) {
+      float* po = a.part_o + (row * a.splits + split) * D;
+      if (l != 0.0f) {
 #pragma unroll
-      for (int i = 0; i < ND; ++i)
+        for (int i = 0; i < ND; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<f32x4_t*>(po + 32 * i + 8 * k + 4 * hi32) =
-              f32x4_t{o[i][4 * k], o[i][4 * k + 1], o[i][4 * k + 2], o[i][4 * k + 3]};
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<f32x4_t*>(po + 32 * i + 8 * k + 4 * hi32) =
+                f32x4_t{o[i][4 * k], o[i][4 * k + 1], o[i][4 * k + 2], o[i][4 * k + 3]};
+      }
+      if (hi32 == 0) {
+        float* ml = a.part_ml + (row * a.splits + split) * 2;
+        ml[0] = m;
+        ml[1] = l;
+      }
+      return;
     }
-    if (hi32 == 0) {
-      float* ml = a.part_ml + (row * a.splits + split) * 2;
-      ml[0] = m;
-      ml[1] = l;
-    }
-    return;
+    const float by = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t at = (s.row0 + tok) * a.ot + h * a.oh;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        store4(a, at + 32 * i + 8 * k + 4 * hi32,
+               f32x4_t{o[i][4 * k] * by, o[i][4 * k + 1] * by, o[i][4 * k + 2] * by, o[i][4 * k + 3] * by});
+    if (a.lse && hi32 == 0) a.lse[row] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
   }
-  const float by = l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t at = (s.row0 + tok) * a.ot + h * a.oh;
-#pragma unroll
-  for (int i = 0; i < ND; ++i)
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      store4(a, at + 32 * i + 8 * k + 4 * hi32,
-             f32x4_t{o[i][4 * k] * by, o[i][4 * k + 1] * by, o[i][4 * k + 2] * by, o[i][4 * k + 3] * by});
-  if (a.lse && hi32 == 0) a.lse[row] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+};
+
+template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 2) void k_many(const AttnArgs a, int streams) {
+  using M = Many<D>;
+  __shared__ __attribute__((aligned(16))) half8_t lk[2][M::kKPieces], lv[2][M::kVPieces];
+  __shared__ __attribute__((aligned(16))) f32x4_t lsc[4][4];
+  ManyRows<D> r(a, lk, lv, lsc);
+  if (!r.begin(streams)) return;
+  if (r.t0 < r.t1) {
+    r.pages_k(r.t0);
+    r.pages_v(r.t0);
+    r.load_k(r.t0);
+    r.load_v(r.t0);
+    r.pages_k(r.t0 + 1);
+    r.pages_v(r.t0 + 1);
+    r.stage_k(r.t0);
+    r.stage_v(r.t0);
+    r.load_k(r.t0 + 1);
+    r.load_v(r.t0 + 1);
+    r.pages_k(r.t0 + 2);
+    r.pages_v(r.t0 + 2);
+    __syncthreads();
+    for (int t = r.t0; t < r.t1; ++t) {
+      f32x16_t st[2];
+      half8_t p[4];
+      r.scores(t, st);
+      Factors f;
+      r.raise(r.largest(t, st, &f));
+      r.weights(st, f, p);
+      r.values(t, p);
+      r.stage_k(t + 1);
+      r.stage_v(t + 1);
+      r.load_k(t + 2);
+      r.load_v(t + 2);
+      r.pages_k(t + 3);
+      r.pages_v(t + 3);
+      __syncthreads();
+    }
+  }
+  r.finish();
+}
+
+// Heads of 256: a wave's rows fill the registers of a SIMD, so the overlap is made within the wave.  Step t takes
+// the weights of tile t beside the scores of tile t + 1 on the matrix cores, and finds the maximum of tile t + 1
+// and stages what comes next beside the values of tile t.
+template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 1) void k_wide(const AttnArgs a, int streams) {
+  using M = Many<D>;
+  __shared__ __attribute__((aligned(16))) half8_t lk[2][M::kKPieces], lv[2][M::kVPieces];
+  __shared__ __attribute__((aligned(16))) f32x4_t lsc[4][4];
+  ManyRows<D> r(a, lk, lv, lsc);
+  if (!r.begin(streams)) return;
+  f32x16_t st[2][2];
+  Factors fa[2];
+  if (r.t0 < r.t1) {
+    r.pages_k(r.t0);
+    r.pages_v(r.t0);
+    r.load_k(r.t0);
+    r.load_v(r.t0);
+    r.pages_k(r.t0 + 1);
+    r.pages_v(r.t0 + 1);
+    r.stage_k(r.t0);
+    r.stage_v(r.t0);
+    r.load_k(r.t0 + 1);
+    r.pages_k(r.t0 + 2);
+    r.stage_k(r.t0 + 1);
+  }
+  __syncthreads();
+  if (r.t0 < r.t1) {
+    r.scores(r.t0, st[0]);
+    r.raise(r.largest(r.t0, st[0], &fa[0]));
+  }
+  const auto step = [&](int t, f32x16_t* now, f32x16_t* next, const Factors& f, Factors* fnext) {
+    r.load_k(t + 2);
+    r.load_v(t + 1);
+    r.pages_k(t + 3);
+    r.pages_v(t + 2);
+    r.scores(t + 1, next);
+    half8_t p[4];
+    r.weights(now, f, p);
+    r.values(t, p);
+    const float top = r.largest(t + 1, next, fnext);
+    r.stage_k(t + 2);
+    r.stage_v(t + 1);
+    if (t + 1 < r.t1) r.raise(top);
+    __syncthreads();
+  };
+  int t = r.t0;
+  for (; t + 1 < r.t1; t += 2) {
+    step(t, st[0], st[1], fa[0], &fa[1]);
+    step(t + 1, st[1], st[0], fa[1], &fa[0]);
+  }
+  if (t < r.t1) step(t, st[0], st[1], fa[0], &fa[1]);
+  r.finish();
 }
 
 // ----------------------------------------------------------------------------------------- join
@@ -682,7 +817,9 @@ template <int D> int launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream
     const int streams = a.c.batch * a.c.heads * a.splits;
     const int64_t total = static_cast<int64_t>(streams) * a.row_tiles, grid = (total + 7) / 8 * 8;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((attn::k_many<D>), dim3(static_cast<uint32_t>(grid)), dim3(attn::Many<D>::kThreads), 0, stream, a, streams);
+    const dim3 g(static_cast<uint32_t>(grid)), t(attn::Many<D>::kThreads);
+    if constexpr (D <= 128) hipLaunchKernelGGL((attn::k_many<D>), g, t, 0, stream, a, streams);
+    else hipLaunchKernelGGL((attn::k_wide<D>), g, t, 0, stream, a, streams);
   } else {
     const dim3 grid(a.splits, a.c.heads * a.row_tiles, a.c.batch);
     if (p.rt == 1) hipLaunchKernelGGL((attn::k_few<D, 1>), grid, dim3(64 * attn::kFewWaves), 0, stream, a);
