@@ -12,9 +12,40 @@ P = 0x10000   # an aligned dummy device address; the host never reads it
 OK, ARG, UNSUPPORTED, ALIGN, WORKSPACE = 0, -1, -2, -3, -4
 
 
+class Structs:
+    """The C structs as include/orbq.h declares them."""
+    class _Rope(ctypes.Structure):
+        _fields_ = [("axes", ctypes.c_int32), ("dims", ctypes.c_int32 * 4), ("freqs", ctypes.c_void_p), ("layout", ctypes.c_int)]
+
+    class _Heads(ctypes.Structure):
+        _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int32)] + \
+            [(n, ctypes.c_int64) for n in ("x_token", "x_head", "y_token", "y_head")]
+
+    class _Cache(ctypes.Structure):
+        _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales")] + \
+            [(n, ctypes.c_int32) for n in ("num_pages", "kv_heads", "page_tokens", "head_dim")]
+
+    class _Table(ctypes.Structure):
+        _fields_ = [("table", ctypes.c_void_p), ("ld", ctypes.c_int64), ("max_pages", ctypes.c_int32), ("batch", ctypes.c_int32)]
+
+
 def structs():
+    return Structs
+
+
+def test_the_binding_packs_the_structs_as_declared():
     from calibration_free_w4a4_amd import attention as at
-    return at
+    for mine, theirs in ((at._ROPE, Structs._Rope), (at._HEADS, Structs._Heads), (at._CACHE, Structs._Cache),
+                         (at._TABLE, Structs._Table)):
+        assert mine.size == ctypes.sizeof(theirs)
+    r = Structs._Rope.from_buffer_copy(at._ROPE.pack(3, 44, 42, 40, 2, 1 << 40, 1))
+    assert (r.axes, list(r.dims), r.freqs, r.layout) == (3, [44, 42, 40, 2], 1 << 40, 1)
+    h = Structs._Heads.from_buffer_copy(at._HEADS.pack(1, 2, 3, -4, 5, 6, 7))
+    assert (h.x, h.y, h.heads, h.x_token, h.x_head, h.y_token, h.y_head) == (1, 2, 3, -4, 5, 6, 7)
+    c = Structs._Cache.from_buffer_copy(at._CACHE.pack(1, 2, 3, 4, 5, 6, 7, 8))
+    assert [getattr(c, f[0]) for f in c._fields_] == [1, 2, 3, 4, 5, 6, 7, 8]
+    t = Structs._Table.from_buffer_copy(at._TABLE.pack(1, 2, 3, 4))
+    assert [getattr(t, f[0]) for f in t._fields_] == [1, 2, 3, 4]
 
 
 def rope_call(dims=(44, 42, 42), axes=None, freqs=P, layout=0, pos=P, n_pos=8, n=8, d=128, x=P, y=P, heads=2, strides=None,
