@@ -206,40 +206,53 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
   }
 
   // This lane's loads of a tile: keys 16 (l15 / 4) + 4 t + l15 % 4, t = 0..3, entries 64 c + 16 g ..
-  // + 15; and for values entries 16 i + l15, keys 16 g .. + 15.  Keys past the sequence's end in a
-  // block that it holds are read and masked; blocks that it does not hold are not read.
+  // + 15; and for values entries 16 i + l15, keys 16 g .. + 15.  Nothing branches: keys past the
+  // sequence's end are read and masked, and for a block that is absent the first of the cache is read
+  // and has no weight.  The table's entries are loaded a tile earlier and judged when they are used, so that no
+  // load is waited for where it is issued.
   const int page_mask = a.c.page - 1;
+  const int64_t block_bytes = static_cast<int64_t>(D) * a.c.page;
+  const int32_t* table = a.c.table + b * a.c.ldt;
   u32x4_t kr[4][NC], vr[ND];
-  int kpg, vpg;                      // pages of the tile to load next
-  const auto pages = [&](int t, int* kp, int* vp) {
-    const int kk = 64 * t + 16 * (l15 >> 2), vk = 64 * t + 16 * g;
-    *kp = t < t1 && kk < s.len ? page_of(a.c, b, kk >> a.page_shift) : -1;
-    *vp = t < t1 && vk < s.len ? page_of(a.c, b, vk >> a.page_shift) : -1;
+  const auto entry = [&](int key) {
+    const int p = key >> a.page_shift;
+    return table[p < a.c.max_pages ? p : a.c.max_pages - 1];
   };
+  const auto present = [&](int pg, int key) { return key < s.len && static_cast<uint32_t>(pg) < static_cast<uint32_t>(a.c.pages); };
+  const auto slot_of = [&](int pg, int key) {  // pg heads + kvh, an absent block as page 0
+    return static_cast<uint64_t>(present(pg, key) ? static_cast<uint32_t>(pg) : 0u) * static_cast<uint32_t>(a.c.heads) + kvh;
+  };
+  const auto key_of = [&](int t) { return 64 * t + 16 * (l15 >> 2); };
+  const auto val_of = [&](int t) { return 64 * t + 16 * g; };
+  const int k_off = (l15 & 3) * D + 16 * g, v_off = l15 * a.c.page;
   const auto load_k = [&](int t, int pg) {
-    const int at = (64 * t + 16 * (l15 >> 2) + (l15 & 3)) & page_mask;
-    const int8_t* p = a.c.k + ((static_cast<int64_t>(pg) * a.c.heads + kvh) * a.c.page + at) * D + 16 * g;
+    const int key = key_of(t);
+    const int8_t* p = a.c.k + slot_of(pg, key) * block_bytes + (key & page_mask) * D + k_off;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-        kr[i][c] = pg >= 0 ? *reinterpret_cast<const u32x4_t*>(p + 4 * i * D + 64 * c) : u32x4_t{0, 0, 0, 0};
+      for (int c = 0; c < NC; ++c) kr[i][c] = *reinterpret_cast<const u32x4_t*>(p + 4 * i * D + 64 * c);
   };
-  const auto load_v = [&](int t, int pg) {
-    const int8_t* p = a.c.v + ((static_cast<int64_t>(pg) * a.c.heads + kvh) * D + l15) * a.c.page + ((64 * t + 16 * g) & page_mask);
+  const auto load_v = [&](int t, uint64_t slot) {
+    const int8_t* p = a.c.v + slot * block_bytes + (val_of(t) & page_mask) + v_off;
 #pragma unroll
-    for (int i = 0; i < ND; ++i)
-      vr[i] = pg >= 0 ? *reinterpret_cast<const u32x4_t*>(p + static_cast<int64_t>(16 * i) * a.c.page) : u32x4_t{0, 0, 0, 0};
+    for (int i = 0; i < ND; ++i) vr[i] = *reinterpret_cast<const u32x4_t*>(p + 16 * i * a.c.page);
   };
+
   int t = t0 + wave;
-  pages(t, &kpg, &vpg);
-  load_k(t, kpg);
+  int kpg = 0, vpg = 0;  // table entries of the tile to load next
+  if (t < t1) {
+    kpg = entry(key_of(t));
+    vpg = entry(val_of(t));
+    load_k(t, kpg);
+    kpg = entry(key_of(t + kFewWaves));
+  }
   for (; t < t1; t += kFewWaves) {
-    load_v(t, vpg);
-    const bool have = vpg >= 0;
-    const int64_t slot = static_cast<int64_t>(have ? vpg : 0) * a.c.heads + kvh;
+    const bool have = present(vpg, val_of(t));
+    const uint64_t slot = slot_of(vpg, val_of(t));
+    load_v(t, slot);
     const float ks = a.c.ks[slot], vs = a.c.vs[slot];
-    pages(t + kFewWaves, &kpg, &vpg);
+    vpg = entry(val_of(t + kFewWaves));
     // S^T: accumulator register 4 i + j of this lane is key 16 g + 4 i + j of row l15
     f32x4_t st[RT][4];
 #pragma unroll
@@ -257,24 +270,27 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
       }
     }
     load_k(t + kFewWaves, kpg);
+    kpg = entry(key_of(t + 2 * kFewWaves));
     float sc, lv, iv;
     block_scales(a, ks, vs, have, &sc, &lv, &iv);
     const bool whole = 64 * t >= lo_most && 64 * t + 64 <= hi_least;
     half8_t p[RT][2];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const float c = sc * qs[rt];
-      float x[16];
-      float top = -__builtin_inff();
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(st[rt][i >> 2][i & 3], c, lv);
+      // positive (zero is taken as the least normal number, so that a masked score stays at -infinity), so
+      // that the largest score is the largest weight's
+      const float c = __builtin_fmaxf(sc * qs[rt], 0x1p-126f);
       if (!whole) {
+        asm volatile("; masked tile");  // keeps this a branch: few tiles take it
         const int k0 = 64 * t + 16 * g;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = k0 + i >= lo[rt] && k0 + i < hi[rt] ? x[i] : -__builtin_inff();
+        for (int i = 0; i < 16; ++i)
+          if (k0 + i < lo[rt] || k0 + i >= hi[rt]) st[rt][i >> 2][i & 3] = -__builtin_inff();
       }
+      float top = st[rt][0][0];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, x[i]);
+      for (int i = 1; i < 16; ++i) top = __builtin_fmaxf(top, st[rt][i >> 2][i & 3]);
+      top = __builtin_fmaf(top, c, lv);
       top = __builtin_fmaxf(top, __shfl_xor(top, 16));
       top = __builtin_fmaxf(top, __shfl_xor(top, 32));
       if (__any(top > m[rt] + kSlack)) {
@@ -284,10 +300,11 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
 #pragma unroll
         for (int i = 0; i < ND; ++i) o[rt][i] *= by;
       }
-      float sum = 0.0f;
+      const float y = lv - m[rt];
+      float sum = 0.0f;  // of the weights before their rounding: the logarithm of l is an output in 32 bits
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float w = exp2_fast(x[i] - m[rt]);
+        const float w = exp2_fast(__builtin_fmaf(st[rt][i >> 2][i & 3], c, y));
         sum += w;
         p[rt][i >> 3][i & 7] = static_cast<_Float16>(w);
       }
