@@ -12,6 +12,7 @@ Head tensors are [tokens, heads, head_dim] with the last dimension contiguous.
 """
 from __future__ import annotations
 
+import functools
 import struct
 
 import torch
@@ -211,6 +212,12 @@ def kv_attention_workspace_bytes(cache: KVCache, batch: int, total: int, max_new
                                                         window))
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace(kv_heads, head_dim, device, *sizes) -> int:
+    # the plan goes by these sizes alone (and the device's compute units)
+    return int(load().orbq_kv_attention_workspace_bytes(_CACHE.pack(0, 0, 0, 0, 1, kv_heads, 16, head_dim), *sizes))
+
+
 def kv_attention(cache: KVCache, q, table, lens, cu=None, max_new=None, causal_block: int = 0, window: int = 0,
                  scale=None, max_len=None, out=None, lse=None, workspace=None):
     """Attention of packed queries q [total, heads, head_dim] (bf16 or f16) over the cache; query i of the n of
@@ -240,9 +247,9 @@ def kv_attention(cache: KVCache, q, table, lens, cu=None, max_new=None, causal_b
     max_len = held if max_len is None or max_len > held else max_len
     lib = load()
     if workspace is None:
-        need = lib.orbq_kv_attention_workspace_bytes(cache.packed, batch, n, max_new, h, max_len, causal_block, window)
+        need = _workspace(cache.kv_heads, d, dev, batch, n, max_new, h, max_len, causal_block, window)
         if need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty((need + 1) // 2)
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = lib.orbq_kv_attention(cache.packed, t, lens, cu, n, max_new, max_len, qp, qt, qh, h, op, ot, oh,
                                0 if lse is None else lse.data_ptr(), code, d ** -0.5 if scale is None else scale, causal_block,

@@ -86,6 +86,7 @@ constexpr int many_rows(int d) { return d == 128 ? 256 : 128; }
 struct AttnPlan {
   int32_t many;    // the form for many rows (else few)
   int32_t rt;      // few: 16-row tiles a workgroup
+  int32_t waves;   // few: waves a workgroup
   int32_t row_tiles, splits, chunk;
 };
 

@@ -22,9 +22,20 @@ AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t k
   if (window) span = std::min<int64_t>(span, static_cast<int64_t>(window) + max_new + causal_block);
   const int64_t tiles = std::max<int64_t>(1, (span + 63) / 64 + 1);
   const int64_t groups = static_cast<int64_t>(batch) * kv_heads * p.row_tiles;
-  const int64_t want = static_cast<int64_t>(cus) * (p.many ? 2 : 8), least = p.many ? 8 : 4;
   int64_t splits = 1;
-  if (groups < want) splits = std::min((want + groups - 1) / groups, (tiles + least - 1) / least);
+  p.waves = 4;
+  if (p.many) {
+    const int64_t want = static_cast<int64_t>(cus) * 2;
+    if (groups < want) splits = std::min((want + groups - 1) / groups, (tiles + 7) / 8);
+  } else if (p.rt == 1 && d <= 128 && (tiles * d <= 17 * 128 || (4 * groups >= 3 * cus && groups <= cus))) {
+    p.waves = 8;
+  } else {
+    // as many workgroups as are resident at once (two a CU), if that leaves few idle; else enough small
+    // ones that the dispatcher evens them out
+    const int64_t want = static_cast<int64_t>(cus) * 2, fit = want / groups;
+    if (groups < 2 * want) splits = fit >= 4 ? fit : (2 * want + groups - 1) / groups;
+    splits = std::min(splits, (tiles + 3) / 4);
+  }
   p.chunk = static_cast<int32_t>((tiles + splits - 1) / splits);
   p.splits = static_cast<int32_t>((tiles + p.chunk - 1) / p.chunk);
   return p;

@@ -20,8 +20,9 @@
 // the rescaling factors are one value a lane.
 //
 // Two forms:
-//   few   16 or 32 rows a workgroup (token-by-token serving): bound by the cache's bytes.  Four waves
-//         take 64-key tiles in turn straight from memory into registers, and are joined at the end.
+//   few   16 or 32 rows a workgroup (token-by-token serving): bound by the cache's bytes.  Four waves, or
+//         eight for a short cache, take 64-key tiles in turn straight from memory into registers, and are
+//         joined at the end.
 //   many  128 rows a workgroup: bound by the matrix cores and the softmax's vector work.  Codes
 //         are turned into f16 once a workgroup on their way into LDS, double buffered.
 // Either splits the keys over workgroups where there are few rows; k_join joins the parts.
@@ -135,12 +136,10 @@ __device__ __forceinline__ void store4(const AttnArgs& a, int64_t at, f32x4_t v)
 }
 
 // ------------------------------------------------------------------------------------------ few
-constexpr int kFewWaves = 4;
-
-template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few(const AttnArgs a) {
+template <int D, int RT, int NW> __global__ __launch_bounds__(64 * NW) void k_few(const AttnArgs a) {
   constexpr int NC = D / 64, ND = D / 16;
-  __shared__ __attribute__((aligned(16))) f32x4_t join_o[kFewWaves / 2][RT][ND][64];
-  __shared__ float join_m[kFewWaves][RT][16], join_l[kFewWaves][RT][16];
+  __shared__ __attribute__((aligned(16))) f32x4_t join_o[NW / 2][RT][ND][64];
+  __shared__ float join_m[NW][RT][16], join_l[NW][RT][16];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int split = blockIdx.x, kvh = blockIdx.y / a.row_tiles, tile = blockIdx.y - kvh * a.row_tiles, b = blockIdx.z;
   const Seq s = seq_of(a, b);
@@ -156,7 +155,7 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
   const int t0 = t_first + split * a.chunk;
   const int t1 = split + 1 < a.splits && t0 + a.chunk < t_end ? t0 + a.chunk : t_end;
   if (a.splits > 1 && t0 >= t1) {  // nothing here: an empty part
-    for (int i = tid; i < r1 - r0; i += 64 * kFewWaves) {
+    for (int i = tid; i < r1 - r0; i += 64 * NW) {
       const int r = r0 + i;
       const int64_t row = (s.row0 + r / a.group) * a.heads + kvh * a.group + r % a.group;
       float* ml = a.part_ml + (row * a.splits + split) * 2;
@@ -164,35 +163,6 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
       ml[1] = 0.0f;
     }
     return;
-  }
-
-  // q: lane l15 holds row l15, entries 64 c + 16 g + 0..15 as two operands
-  half8_t q[RT][NC][2];
-  float qs[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int r = r0 + 16 * rt + l15;
-    const bool live = r < r1;
-    const int rr = live ? r : r0, tok = rr / a.group, h = kvh * a.group + rr - tok * a.group;
-    const int64_t at = (s.row0 + tok) * a.qt + h * a.qh;
-    visible(a, static_cast<int64_t>(s.len) - s.rows + tok, s.len, &lo[rt], &hi[rt]);
-    if (!live) hi[rt] = 0;
-    float most = 0.0f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        q[rt][c][k] = load_q8(a, at + 64 * c + 16 * g + 8 * k);
-        most = __builtin_fmaxf(most, q_most(q[rt][c][k], a.f16));
-      }
-    most = __builtin_fmaxf(most, __shfl_xor(most, 16));
-    most = __builtin_fmaxf(most, __shfl_xor(most, 32));
-    qs[rt] = row_power(most);
-    const float by = (a.negative ? -1.0f : 1.0f) / qs[rt];
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) q[rt][c][k] = q_scaled(q[rt][c][k], a.f16, by);
   }
 
   f32x4_t o[RT][ND];
@@ -239,20 +209,55 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
     for (int i = 0; i < ND; ++i) vr[i] = *reinterpret_cast<const u32x4_t*>(p + 16 * i * a.c.page);
   };
 
+  // The first table entries, q and the first keys are on their way together.
+  // q: lane l15 holds row l15, entries 64 c + 16 g + 0..15 as two operands
   int t = t0 + wave;
   int kpg = 0, vpg = 0;  // table entries of the tile to load next
   if (t < t1) {
     kpg = entry(key_of(t));
     vpg = entry(val_of(t));
-    load_k(t, kpg);
-    kpg = entry(key_of(t + kFewWaves));
   }
-  for (; t < t1; t += kFewWaves) {
+  half8_t q[RT][NC][2];
+  float qs[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int r = r0 + 16 * rt + l15;
+    const bool live = r < r1;
+    const int rr = live ? r : r0, tok = rr / a.group, h = kvh * a.group + rr - tok * a.group;
+    const int64_t at = (s.row0 + tok) * a.qt + h * a.qh;
+    visible(a, static_cast<int64_t>(s.len) - s.rows + tok, s.len, &lo[rt], &hi[rt]);
+    if (!live) hi[rt] = 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) q[rt][c][k] = load_q8(a, at + 64 * c + 16 * g + 8 * k);
+  }
+  if (t < t1) {
+    load_k(t, kpg);
+    kpg = entry(key_of(t + NW));
+  }
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    float most = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) most = __builtin_fmaxf(most, q_most(q[rt][c][k], a.f16));
+    most = __builtin_fmaxf(most, __shfl_xor(most, 16));
+    most = __builtin_fmaxf(most, __shfl_xor(most, 32));
+    qs[rt] = row_power(most);
+    const float by = (a.negative ? -1.0f : 1.0f) / qs[rt];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) q[rt][c][k] = q_scaled(q[rt][c][k], a.f16, by);
+  }
+  for (; t < t1; t += NW) {
     const bool have = present(vpg, val_of(t));
     const uint64_t slot = slot_of(vpg, val_of(t));
     load_v(t, slot);
     const float ks = a.c.ks[slot], vs = a.c.vs[slot];
-    vpg = entry(val_of(t + kFewWaves));
+    vpg = entry(val_of(t + NW));
     // S^T: accumulator register 4 i + j of this lane is key 16 g + 4 i + j of row l15
     f32x4_t st[RT][4];
 #pragma unroll
@@ -269,8 +274,8 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
         }
       }
     }
-    load_k(t + kFewWaves, kpg);
-    kpg = entry(key_of(t + 2 * kFewWaves));
+    load_k(t + NW, kpg);
+    kpg = entry(key_of(t + 2 * NW));
     float sc, lv, iv;
     block_scales(a, ks, vs, have, &sc, &lv, &iv);
     const bool whole = 64 * t >= lo_most && 64 * t + 64 <= hi_least;
@@ -321,7 +326,7 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
     }
   }
 
-  // join the four waves
+  // join the waves
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     l[rt] += __shfl_xor(l[rt], 16);
@@ -338,15 +343,15 @@ template <int D, int RT> __global__ __launch_bounds__(64 * kFewWaves) void k_few
     mt[rt] = kNone;
     lt[rt] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) mt[rt] = __builtin_fmaxf(mt[rt], join_m[w][rt][l15]);
+    for (int w = 0; w < NW; ++w) mt[rt] = __builtin_fmaxf(mt[rt], join_m[w][rt][l15]);
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) lt[rt] += join_l[w][rt][l15] * exp2_fast(join_m[w][rt][l15] - mt[rt]);
+    for (int w = 0; w < NW; ++w) lt[rt] += join_l[w][rt][l15] * exp2_fast(join_m[w][rt][l15] - mt[rt]);
     const float by = exp2_fast(m[rt] - mt[rt]);
 #pragma unroll
     for (int i = 0; i < ND; ++i) o[rt][i] *= by;
   }
 #pragma unroll
-  for (int half = kFewWaves / 2; half >= 1; half >>= 1) {
+  for (int half = NW / 2; half >= 1; half >>= 1) {
     if (wave >= half && wave < 2 * half) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
@@ -839,8 +844,9 @@ template <int D> int launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream
     else hipLaunchKernelGGL((attn::k_wide<D>), g, t, 0, stream, a, streams);
   } else {
     const dim3 grid(a.splits, a.c.heads * a.row_tiles, a.c.batch);
-    if (p.rt == 1) hipLaunchKernelGGL((attn::k_few<D, 1>), grid, dim3(64 * attn::kFewWaves), 0, stream, a);
-    else hipLaunchKernelGGL((attn::k_few<D, 2>), grid, dim3(64 * attn::kFewWaves), 0, stream, a);
+    if (p.rt == 2) hipLaunchKernelGGL((attn::k_few<D, 2, 4>), grid, dim3(256), 0, stream, a);
+    else if (p.waves == 4) hipLaunchKernelGGL((attn::k_few<D, 1, 4>), grid, dim3(256), 0, stream, a);
+    else if constexpr (D <= 128) hipLaunchKernelGGL((attn::k_few<D, 1, 8>), grid, dim3(512), 0, stream, a);
   }
   if (a.splits > 1)
     hipLaunchKernelGGL((attn::k_join<D>), dim3(static_cast<uint32_t>(a.total * a.heads)), dim3(256), 0, stream, a);
