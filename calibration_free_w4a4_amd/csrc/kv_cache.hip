@@ -17,6 +17,8 @@
 // One workgroup for each (touched page, head, keys or values): it holds the page's new values in
 // registers between the maximum and the quantisation, so every byte crosses HBM once, and no two
 // workgroups write the same page (no atomics; the result does not depend on any order).
+#include <type_traits>
+
 #include "attention_device.h"
 
 namespace orbq {
@@ -34,6 +36,27 @@ __device__ __forceinline__ uint32_t code_of(float x, float inv) {
   return static_cast<uint32_t>(static_cast<int>(c)) & 0xffu;
 }
 
+// the codes of four finite values within 127.5 / inv: adding 1.5 2^23 rounds to the integer (ties to even) that
+// is then the low byte
+__device__ __forceinline__ uint32_t codes_of_finite(const float* x, float inv) {
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float y = x[i] * inv;
+    asm("" : "+v"(y));  // rounded by itself, as rint(x inv) asks: not one fused operation with the sum
+    c[i] = __builtin_bit_cast(uint32_t, y + 12582912.0f);
+  }
+  return __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u) | __builtin_amdgcn_perm(c[3], c[2], 0x04000c0cu);
+}
+
+template <bool FINITE> __device__ __forceinline__ uint32_t codes_of(const float* x, float inv) {
+  if constexpr (FINITE) return codes_of_finite(x, inv);
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r |= code_of(x[i], inv) << (8 * i);
+  return r;
+}
+
 // four codes of a scale that grew
 __device__ __forceinline__ uint32_t rescale4(uint32_t q, float ratio) {
   uint32_t r = 0;
@@ -49,12 +72,61 @@ __device__ __forceinline__ uint32_t below(int at, int end) {
   return n <= 0 ? 0u : (n >= 4 ? 0xffffffffu : (1u << (8 * n)) - 1u);
 }
 
+template <int DT> __device__ __forceinline__ auto half_bits() {
+  if constexpr (DT == kF32) return uint32_t{};
+  else return uint16_t{};
+}
+
+// The largest of N 16-byte words' magnitudes as an unsigned integer, two entries an instruction where they have 16
+// bits; above the largest number's it is an infinity's or a NaN's.
+template <int DT, int N> __device__ __forceinline__ uint32_t largest_bits(const u32x4_t* w) {
+  typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+  if constexpr (DT == kF32) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = max(m, w[i][j] & 0x7fffffffu);
+    return m;
+  } else {
+    u16x2_t m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, w[i][j] & 0x7fff7fffu));
+    return max(static_cast<uint32_t>(m[0]), static_cast<uint32_t>(m[1]));
+  }
+}
+
+// maximum over the workgroup
+template <int NT> __device__ __forceinline__ uint32_t wide_max(uint32_t m, uint32_t* top) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), off)));
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) m = max(m, top[w]);
+  }
+  return m;
+}
+
+// A thread's share of a page: PER columns of 8 entries, TP consecutive tokens each time, so that the codes of
+// TP tokens cross LDS as one word where values are turned.
+template <int D, int PAGE> struct Share {
+  static constexpr int NT = threads_for(D * PAGE), PER = D * PAGE / (8 * NT), TP = PER < 4 ? PER : 4;
+  static constexpr int LD = PAGE + 4;  // LDS pitch of a value row
+  static_assert(TP == 2 || TP == 4, "");
+  static __device__ __forceinline__ int token(int tid, int i) { return (i / TP * (NT / (D / 8)) + tid / (D / 8)) * TP + i % TP; }
+  static __device__ __forceinline__ int entry(int tid) { return tid % (D / 8) * 8; }
+};
+
 template <int DT, int D, int PAGE>
 __global__ __launch_bounds__(threads_for(D* PAGE)) void k_append(const KvCache c, const KvTokens x) {
-  constexpr int NT = threads_for(D * PAGE), PER = D * PAGE / (8 * NT);  // groups of 8 values a thread
-  constexpr int LD = PAGE + 4;                                          // LDS pitch of a value row
+  using S = Share<D, PAGE>;
+  constexpr int NT = S::NT, PER = S::PER, TP = S::TP, LD = S::LD;
   __shared__ __attribute__((aligned(16))) uint8_t turned[D * LD];
-  __shared__ float top[NT / 64];
+  __shared__ uint32_t top[NT / 64];
   const int tid = threadIdx.x, head = blockIdx.y >> 1, b = blockIdx.z;
   const bool values = blockIdx.y & 1;
   int64_t row0;
@@ -64,78 +136,95 @@ __global__ __launch_bounds__(threads_for(D* PAGE)) void k_append(const KvCache c
   if (start < 0 || rows == 0) return;
   const int64_t p = start / PAGE + blockIdx.x;
   const int64_t t0 = p * PAGE;                       // the page's first token
-  if (t0 >= start + rows) return;
-  const int32_t pg = page_of(c, b, p);
-  if (pg < 0) return;
+  if (t0 >= start + rows || c.max_pages == 0) return;
   const int had = static_cast<int>(start > t0 ? start - t0 : 0);                        // tokens held before
   const int end = static_cast<int>(start + rows - t0 < PAGE ? start + rows - t0 : PAGE);  // and after
-  const int64_t slot = static_cast<int64_t>(pg) * c.heads + head;
-  float* scales = (values ? c.vs : c.ks) + slot;
-  const float old = had ? *scales : 0.0f;
+  // the page, and with it the old scale, are looked up while the new values are on their way
+  const int32_t entry = c.table[b * c.ldt + (p < c.max_pages ? p : 0)];
 
   const void* src = values ? x.v : x.k;
   const int64_t st = values ? x.vt : x.kt, sh = (values ? x.vh : x.kh) * head;
-  float f[PER][8];
-  float most = 0.0f;
+  // no load depends on a branch (a token that is not new reads a neighbour's row), so that all are under way at once
+  typedef typename Elem<DT>::T T;
+  constexpr int W = sizeof(T) / 2;  // 16-byte words of 8 entries
+  u32x4_t raw[PER][W];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int at = i * NT + tid, t = at / (D / 8), e = at % (D / 8) * 8;
-    if (t >= had && t < end) {
-      const int64_t from = (row0 + t0 + t - start) * st + sh + e;
-      if constexpr (DT == kF32) {
-        Vec<DT, 4>::load(src, from, f[i]);
-        Vec<DT, 4>::load(src, from + 4, f[i] + 4);
-      } else {
-        Vec<DT, 8>::load(src, from, f[i]);
-      }
+    int t = S::token(tid, i);
+    t = t < had ? had : (t >= end ? end - 1 : t);
+    const T* from = static_cast<const T*>(src) + (row0 + t0 + t - start) * st + sh + S::entry(tid);
+#pragma unroll
+    for (int w = 0; w < W; ++w) raw[i][w] = reinterpret_cast<const u32x4_t*>(from)[w];
+  }
+  const int32_t pg = p < c.max_pages && entry >= 0 && entry < c.pages ? entry : -1;
+  if (pg < 0) return;
+  const int64_t slot = static_cast<int64_t>(pg) * c.heads + head;
+  float* scales = (values ? c.vs : c.ks) + slot;
+  const float old = had ? *scales : 0.0f;
+  // the largest magnitude, as the integer that its bits are
+  const uint32_t big = largest_bits<DT, PER * W>(&raw[0][0]);
+  uint32_t bits = wide_max<NT>(big, top);
+  constexpr uint32_t kInf = DT == kF32 ? 0x7f800000u : (DT == kBF16 ? 0x7f80u : 0x7c00u);
+  const bool odd = bits >= kInf;  // an infinity or a NaN: the largest finite one is looked for value by value
+  float f[PER][8];
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[i][j] = static_cast<float>(reinterpret_cast<const T*>(&raw[i][0])[j]);
+  if (odd) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float a = __builtin_fabsf(f[i][j]);
-        most = a < __builtin_inff() ? __builtin_fmaxf(most, a) : most;
+        const float v = __builtin_fabsf(f[i][j]);
+        m = v < __builtin_inff() ? __builtin_fmaxf(m, v) : m;
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
-    }
-  }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) most = __builtin_fmaxf(most, __shfl_xor(most, off));
-  if constexpr (NT > 64) {
-    if ((tid & 63) == 0) top[tid >> 6] = most;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < NT / 64; ++w) most = __builtin_fmaxf(most, top[w]);
+    bits = wide_max<NT>(__builtin_bit_cast(uint32_t, m), top);
   }
+  const float most = odd || DT == kF32 ? __builtin_bit_cast(float, bits)
+                                       : static_cast<float>(__builtin_bit_cast(T, static_cast<decltype(half_bits<DT>())>(bits)));
   const float need = __builtin_fmaxf(most * kInv127, kScaleFloor);
   const bool grow = !(need <= old);
   const float scale = grow ? __builtin_fmaxf(need, kScaleGrow * old) : old;
   const float inv = 1.0f / scale, ratio = old / scale;
   if (tid == 0 && grow) *scales = scale;
 
-  if (!values) {
-    uint8_t* dst = reinterpret_cast<uint8_t*>(c.k) + slot * (D * PAGE);
+  const auto write = [&](auto finite) {
+    constexpr bool F = decltype(finite)::value;
+    if (!values) {
+      uint8_t* dst = reinterpret_cast<uint8_t*>(c.k) + slot * (D * PAGE);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int at = i * NT + tid, t = at / (D / 8);
-      u32x2_t* to = reinterpret_cast<u32x2_t*>(dst + 8 * at);
-      if (t >= had && t < end) {
-        u32x2_t q = {0, 0};
+      for (int i = 0; i < PER; ++i) {
+        const int t = S::token(tid, i);
+        u32x2_t* to = reinterpret_cast<u32x2_t*>(dst + t * D + S::entry(tid));
+        if (t >= had && t < end) {
+          *to = u32x2_t{codes_of<F>(&f[i][0], inv), codes_of<F>(&f[i][4], inv)};
+        } else if (t < had && grow) {
+          const u32x2_t q = *to;
+          *to = u32x2_t{rescale4(q[0], ratio), rescale4(q[1], ratio)};
+        }
+      }
+      return;
+    }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j >> 2] |= code_of(f[i][j], inv) << (8 * (j & 3));
-        *to = q;
-      } else if (t < had && grow) {
-        const u32x2_t q = *to;
-        *to = u32x2_t{rescale4(q[0], ratio), rescale4(q[1], ratio)};
+    for (int i = 0; i < PER; i += TP) {
+      uint8_t* to = &turned[S::entry(tid) * LD + S::token(tid, i)];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < TP; ++k) x[k] = f[i + k][j];
+        const uint32_t q = codes_of<F>(x, inv);
+        if constexpr (TP == 4) *reinterpret_cast<uint32_t*>(to + j * LD) = q;
+        else *reinterpret_cast<uint16_t*>(to + j * LD) = static_cast<uint16_t>(q);
       }
     }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int at = i * NT + tid, t = at / (D / 8), e = at % (D / 8) * 8;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) turned[(e + j) * LD + t] = static_cast<uint8_t>(code_of(f[i][j], inv));
-  }
+  };
+  if (odd) write(std::false_type{});
+  else write(std::true_type{});
+  if (!values) return;
   __syncthreads();
   uint8_t* dst = reinterpret_cast<uint8_t*>(c.v) + slot * (D * PAGE);
   for (int at = tid; at < D * PAGE / 16; at += NT) {
@@ -160,8 +249,8 @@ __global__ __launch_bounds__(threads_for(D* PAGE)) void k_append(const KvCache c
 
 template <int DT, int D, int PAGE>
 __global__ __launch_bounds__(threads_for(D* PAGE)) void k_read(const KvCache c, const KvTokens x) {
-  constexpr int NT = threads_for(D * PAGE), PER = D * PAGE / (8 * NT);
-  constexpr int LD = PAGE + 4;
+  using S = Share<D, PAGE>;
+  constexpr int NT = S::NT, PER = S::PER, TP = S::TP, LD = S::LD;
   __shared__ __attribute__((aligned(16))) uint8_t turned[D * LD];
   const int tid = threadIdx.x, head = blockIdx.y >> 1, b = blockIdx.z;
   const bool values = blockIdx.y & 1;
@@ -176,44 +265,60 @@ __global__ __launch_bounds__(threads_for(D* PAGE)) void k_read(const KvCache c, 
   const int32_t pg = page_of(c, b, p);
   const int from = static_cast<int>(first > t0 ? first - t0 : 0);
   const int end = static_cast<int>(first + rows - t0 < PAGE ? first + rows - t0 : PAGE);
-  const int64_t slot = static_cast<int64_t>(pg < 0 ? 0 : pg) * c.heads + head;
+  const int64_t slot = static_cast<int64_t>(pg < 0 ? 0 : pg) * c.heads + head;  // an absent page: page 0, times zero
   const float scale = pg < 0 ? 0.0f : (values ? c.vs : c.ks)[slot];
   const uint8_t* src = reinterpret_cast<const uint8_t*>(values ? c.v : c.k) + slot * (D * PAGE);
   if (values) {
-    if (pg >= 0) {
-      for (int at = tid; at < D * PAGE / 16; at += NT) {
-        const int e = at / (PAGE / 16), t = at % (PAGE / 16) * 16;
-        const u32x4_t q = *reinterpret_cast<const u32x4_t*>(src + 16 * at);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(&turned[e * LD + t + 4 * j]) = q[j];
-      }
+    for (int i = 0; i < D * PAGE / 16 / NT; ++i) {
+      const int at = i * NT + tid, e = at / (PAGE / 16), t = at % (PAGE / 16) * 16;
+      const u32x4_t q = *reinterpret_cast<const u32x4_t*>(src + 16 * at);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(&turned[e * LD + t + 4 * j]) = q[j];
     }
     __syncthreads();
   }
   void* dst = values ? x.v : x.k;
   const int64_t st = values ? x.vt : x.kt, sh = (values ? x.vh : x.kh) * head;
+  const int e = S::entry(tid);
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int at = i * NT + tid, t = at / (D / 8), e = at % (D / 8) * 8;
-    if (t < from || t >= end) continue;
-    float f[8];
-    if (pg < 0) {
+  for (int i = 0; i < PER; i += TP) {
+    float f[TP][8];
+    if (values) {
+      const uint8_t* at = &turned[e * LD + S::token(tid, i)];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-    } else if (values) {
+      for (int j = 0; j < 8; ++j) {
+        uint32_t w;
+        if constexpr (TP == 4) w = *reinterpret_cast<const uint32_t*>(at + j * LD);
+        else w = *reinterpret_cast<const uint16_t*>(at + j * LD);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = static_cast<float>(static_cast<int8_t>(turned[(e + j) * LD + t])) * scale;
+        for (int k = 0; k < TP; ++k) f[k][j] = static_cast<float>(static_cast<int8_t>(w >> (8 * k)));
+      }
     } else {
-      const u32x2_t q = *reinterpret_cast<const u32x2_t*>(src + 8 * at);
+      u32x2_t q[TP];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = static_cast<float>(static_cast<int8_t>(q[j >> 2] >> (8 * (j & 3)))) * scale;
+      for (int k = 0; k < TP; ++k) q[k] = *reinterpret_cast<const u32x2_t*>(src + S::token(tid, i + k) * D + e);
+#pragma unroll
+      for (int k = 0; k < TP; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[k][j] = static_cast<float>(static_cast<int8_t>(q[k][j >> 2] >> (8 * (j & 3))));
     }
-    const int64_t to = (row0 + t0 + t - first) * st + sh + e;
-    if constexpr (DT == kF32) {
-      Vec<DT, 4>::store(dst, to, f);
-      Vec<DT, 4>::store(dst, to + 4, f + 4);
-    } else {
-      Vec<DT, 8>::store(dst, to, f);
+#pragma unroll
+    for (int k = 0; k < TP; ++k) {
+      const int t = S::token(tid, i + k);
+      if (t < from || t >= end) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[k][j] = pg < 0 ? 0.0f : f[k][j] * scale;
+        asm("" : "+v"(f[k][j]));  // an fp32 product, then the output type: not one rounding of both here and two there
+      }
+      const int64_t to = (row0 + t0 + t - first) * st + sh + e;
+      if constexpr (DT == kF32) {
+        Vec<DT, 4>::store(dst, to, f[k]);
+        Vec<DT, 4>::store(dst, to + 4, f[k] + 4);
+      } else {
+        Vec<DT, 8>::store(dst, to, f[k]);
+      }
     }
   }
 }
