@@ -41,6 +41,18 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// x of this lane and of the lane 32 (16) away, combined: one vector instruction, where a shuffle would go through LDS
+__device__ __forceinline__ float max_over32(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_fmaxf(__builtin_bit_cast(float, static_cast<uint32_t>(r[0])), __builtin_bit_cast(float, static_cast<uint32_t>(r[1])));
+}
+__device__ __forceinline__ float max_over16(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return __builtin_fmaxf(__builtin_bit_cast(float, static_cast<uint32_t>(r[0])), __builtin_bit_cast(float, static_cast<uint32_t>(r[1])));
+}
+
 // four signed codes -> f16: byte u = code + 128 behind 0x64 is 1024 + u, less 1152 is the code
 __device__ __forceinline__ void codes_to_f16(uint32_t q, half2_t* lo, half2_t* hi) {
   const uint32_t u = q ^ 0x80808080u;
@@ -243,8 +255,7 @@ template <int D, int RT, int NW> __global__ __launch_bounds__(64 * NW) void k_fe
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int k = 0; k < 2; ++k) most = __builtin_fmaxf(most, q_most(q[rt][c][k], a.f16));
-    most = __builtin_fmaxf(most, __shfl_xor(most, 16));
-    most = __builtin_fmaxf(most, __shfl_xor(most, 32));
+    most = max_over32(max_over16(most));
     qs[rt] = row_power(most);
     const float by = (a.negative ? -1.0f : 1.0f) / qs[rt];
 #pragma unroll
@@ -296,8 +307,7 @@ template <int D, int RT, int NW> __global__ __launch_bounds__(64 * NW) void k_fe
 #pragma unroll
       for (int i = 1; i < 16; ++i) top = __builtin_fmaxf(top, st[rt][i >> 2][i & 3]);
       top = __builtin_fmaf(top, c, lv);
-      top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-      top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+      top = max_over32(max_over16(top));
       if (__any(top > m[rt] + kSlack)) {
         const float mn = __builtin_fmaxf(m[rt], top), by = exp2_fast(m[rt] - mn);
         m[rt] = mn;
@@ -306,14 +316,14 @@ template <int D, int RT, int NW> __global__ __launch_bounds__(64 * NW) void k_fe
         for (int i = 0; i < ND; ++i) o[rt][i] *= by;
       }
       const float y = lv - m[rt];
-      float sum = 0.0f;  // of the weights before their rounding: the logarithm of l is an output in 32 bits
+      float total = 0.0f;  // of the weights before their rounding: the logarithm of l is an output in 32 bits
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float w = exp2_fast(__builtin_fmaf(st[rt][i >> 2][i & 3], c, y));
-        sum += w;
+        total += w;
         p[rt][i >> 3][i & 7] = static_cast<_Float16>(w);
       }
-      l[rt] = __builtin_fmaf(sum, iv, l[rt]);
+      l[rt] = __builtin_fmaf(total, iv, l[rt]);
     }
 #pragma unroll
     for (int i = 0; i < ND; ++i) {
@@ -497,7 +507,7 @@ template <int D> struct ManyRows {
       q[i] = load_q8(a, at + 16 * i + 8 * hi32);
       most = __builtin_fmaxf(most, q_most(q[i], a.f16));
     }
-    most = __builtin_fmaxf(most, __shfl_xor(most, 32));
+    most = max_over32(most);
     qs = row_power(most);
     const float by = (a.negative ? -1.0f : 1.0f) / qs;
 #pragma unroll
@@ -636,7 +646,7 @@ template <int D> struct ManyRows {
       for (int j = 1; j < 8; ++j) x = __builtin_fmaxf(x, st[g >> 1][8 * (g & 1) + j]);
       top = __builtin_fmaxf(top, __builtin_fmaf(x, f->c[g], f->lv[g]));
     }
-    return __builtin_fmaxf(top, __shfl_xor(top, 32));
+    return max_over32(top);
   }
   __device__ __forceinline__ void raise(float top) {
     if (__any(top > m + kSlack)) {
@@ -651,14 +661,14 @@ template <int D> struct ManyRows {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const float y = f.lv[g] - m;
-      float sum = 0.0f;  // of the weights before their rounding: the logarithm of l is an output in 32 bits
+      float total = 0.0f;  // of the weights before their rounding: the logarithm of l is an output in 32 bits
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float w = exp2_fast(__builtin_fmaf(st[g >> 1][8 * (g & 1) + j], f.c[g], y));
-        sum += w;
+        total += w;
         p[g][j] = static_cast<_Float16>(w);
       }
-      l = __builtin_fmaf(sum, f.iv[g], l);
+      l = __builtin_fmaf(total, f.iv[g], l);
     }
   }
 
