@@ -78,6 +78,9 @@ struct AttnArgs {
   int32_t row_tiles, splits, chunk;  // chunk: 64-key tiles of a split
   float* part_o;                     // [total * heads][splits][d], splits > 1
   float* part_ml;                    // [total * heads][splits][2]
+  void* turned;                      // AttnPlan::turned: f16 tiles [batch][cache heads][turned_tiles][16 d][8]
+  void* factors;                     // and their factors [batch][cache heads][turned_tiles][4][4] fp32
+  int32_t turned_tiles;
 };
 
 // rows of a workgroup in the form for many rows, 32 a wave
@@ -88,10 +91,12 @@ struct AttnPlan {
   int32_t rt;      // few: 16-row tiles a workgroup
   int32_t waves;   // few: waves a workgroup
   int32_t row_tiles, splits, chunk;
+  int32_t turned;  // many: the tiles a stream's keys are turned into f16 before (0: on the way into LDS)
 };
 
+// bound: no sequence can be longer than max_len
 AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t kv_heads, int32_t d, int64_t max_len,
-                        int32_t causal_block, int32_t window, int cus);
+                        int32_t causal_block, int32_t window, bool bound, int cus);
 int launch_kv_attention(AttnArgs a, const AttnPlan& p, hipStream_t stream);
 
 // one instantiation unit per head dimension

@@ -10,7 +10,7 @@ template <> int launch_attn<128>(const AttnArgs&, const AttnPlan&, hipStream_t);
 template <> int launch_attn<256>(const AttnArgs&, const AttnPlan&, hipStream_t);
 
 AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t kv_heads, int32_t d, int64_t max_len,
-                        int32_t causal_block, int32_t window, int cus) {
+                        int32_t causal_block, int32_t window, bool bound, int cus) {
   AttnPlan p{};
   const int64_t rows = static_cast<int64_t>(max_new) * (heads / kv_heads);
   p.many = rows > 32;
@@ -25,8 +25,19 @@ AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t k
   int64_t splits = 1;
   p.waves = 4;
   if (p.many) {
-    const int64_t want = static_cast<int64_t>(cus) * 2;
-    if (groups < want) splits = std::min((want + groups - 1) / groups, (tiles + 7) / 8);
+    // Workgroups resident at once: one a CU (LDS and registers), three with heads of 64.  A split costs its parts'
+    // way through memory, about as long as 400 keys of its rows take; it pays where it fills the last round.
+    const int64_t want = static_cast<int64_t>(cus) * (d == 64 ? 3 : 1), most = std::max<int64_t>(1, tiles / 8);
+    const auto rounds = [&](int64_t n) {
+      return static_cast<double>((groups * n + want - 1) / want) / n + (n > 1 ? n * 400.0 / span * groups / want : 0.0);
+    };
+    const auto consider = [&](int64_t n) {
+      if (n > 1 && n <= most && rounds(n) < rounds(splits)) splits = n;
+    };
+    for (int n = 2; n <= 8; ++n) consider(n);
+    for (int n = 1; n <= 3; ++n) consider(n * want / groups);
+    if (bound && d > 64 && p.row_tiles >= 4 && static_cast<int64_t>(batch) * kv_heads * tiles * d <= (int64_t{1} << 22))
+      p.turned = static_cast<int32_t>(tiles);  // at most 1 GiB of workspace
   } else if (p.rt == 1 && d <= 128 && (tiles * d <= 17 * 128 || (4 * groups >= 3 * cus && groups <= cus))) {
     p.waves = 8;
   } else {

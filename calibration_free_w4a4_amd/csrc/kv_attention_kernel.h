@@ -405,11 +405,13 @@ template <int D, int RT, int NW> __global__ __launch_bounds__(64 * NW) void k_fe
 }
 
 // ----------------------------------------------------------------------------------------- many
-template <int D> struct Many {
+// TURNED: k_turn has laid the tiles out in f16 before, and they come into LDS as they are.
+template <int D, bool TURNED = false> struct Many {
   static constexpr int kRows = many_rows(D), kWaves = kRows / 32, kThreads = 64 * kWaves;
-  // LDS of one tile in 16-byte pieces: keys [d / 8][64 + 1], values [8][d + 2] (pieces of 8 keys).
-  // A wave's operand reads are 32 consecutive pieces; the pitches spread the writers over banks.
-  static constexpr int kKPitch = 65, kVPitch = D + 2;
+  // LDS of one tile in 16-byte pieces: keys [d / 8][64], values [8][d] (pieces of 8 keys).  A wave's
+  // operand reads are 32 consecutive pieces; where threads turn codes themselves, a pitch of 1 and 2 more
+  // pieces spreads them over banks.
+  static constexpr int kKPitch = TURNED ? 64 : 65, kVPitch = TURNED ? D : D + 2;
   static constexpr int kKPieces = D / 8 * kKPitch, kVPieces = 8 * kVPitch;
   static constexpr int kLoads = 4 * D / kThreads;  // 16-byte loads a thread for a tile's keys, and for its values
 };
@@ -418,10 +420,17 @@ struct Factors {  // of each 16 keys of a tile: on raw scores, log2 of the value
   float c[4], lv[4], iv[4];
 };
 
+// the first 64-key tile that a sequence's rows see
+__device__ __forceinline__ int first_of(const AttnArgs& a, const Seq& s) {
+  int32_t lo, hi;
+  visible(a, static_cast<int64_t>(s.len) - s.rows, s.len, &lo, &hi);
+  return lo / 64;
+}
+
 // One workgroup's rows, its part of the keys, and one wave's 32 rows of them: lane l31 of either half
 // holds row l31.  Everything here is inlined; the members live in registers.
-template <int D> struct ManyRows {
-  using M = Many<D>;
+template <int D, bool TURNED = false> struct ManyRows {
+  using M = Many<D, TURNED>;
   static constexpr int NS = D / 16, ND = D / 32, NL = M::kLoads;
   const AttnArgs& a;
   half8_t (*lk)[M::kKPieces];   // [2]: tile t in t & 1
@@ -447,6 +456,9 @@ template <int D> struct ManyRows {
   int kpg[NL], vpg, spg;        // table entries of the next tiles' keys, values and scales
   float ks, vs;                 // scales of the keys to stage next, of 16 keys a lane (tid < 4)
   bool have;
+  // TURNED: this stream's tiles and their factors
+  const half8_t* turned;
+  const f32x4_t* factors;
 
   __device__ __forceinline__ ManyRows(const AttnArgs& args, half8_t (*k)[M::kKPieces], half8_t (*v)[M::kVPieces], f32x4_t (*sc4)[4])
       : a(args), lk(k), lv(v), lsc(sc4) {}
@@ -509,6 +521,13 @@ template <int D> struct ManyRows {
       for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
     m = kNone;
     l = 0.0f;
+    if constexpr (TURNED) {
+      // tile t of the stream is its (t - first_of)th
+      const int64_t first_tile = (static_cast<int64_t>(b) * a.c.heads + kvh) * a.turned_tiles - first_of(a, s);
+      turned = static_cast<const half8_t*>(a.turned) + first_tile * (16 * D);
+      factors = static_cast<const f32x4_t*>(a.factors) + first_tile * 4;
+      return true;
+    }
     table = a.c.table + b * a.c.ldt;
     block_bytes = static_cast<int64_t>(D) * a.c.page;
     page_mask = a.c.page - 1;
@@ -591,6 +610,23 @@ template <int D> struct ManyRows {
     }
   }
 
+  // TURNED: half a tile, 8 D pieces, straight into LDS by every wave's share of 64 pieces at a time.  The loads
+  // are written out because the compiler would wait for all of them before the next LDS read of any kind; they
+  // have no register results, and arrived() ends them.
+  __device__ __forceinline__ void fetch(const half8_t* from, half8_t* to) const {
+#pragma unroll
+    for (int i = 0; i < D / 8 / M::kWaves; ++i) {
+      const int j = 64 * (i * M::kWaves + wave);
+      const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) half8_t*)(to + j)));
+      asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from + j + lane),
+                   "s"(__builtin_amdgcn_readfirstlane(at))
+                   : "memory");
+    }
+  }
+  __device__ __forceinline__ void fetch_k(int t) const { fetch(turned + static_cast<int64_t>(t) * (16 * D), lk[t & 1]); }
+  __device__ __forceinline__ void fetch_v(int t) const { fetch(turned + static_cast<int64_t>(t) * (16 * D) + 8 * D, lv[t & 1]); }
+  __device__ __forceinline__ void arrived() const { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
   // S^T of tile t: register 8 (g & 1) + 4 k + j of st[g / 2] is key 16 g + 8 k + 4 hi32 + j
   __device__ __forceinline__ void scores(int t, f32x16_t* st) const {
 #pragma unroll
@@ -628,7 +664,7 @@ template <int D> struct ManyRows {
     float top = -__builtin_inff();
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const f32x4_t x4 = lsc[t & 3][g];
+      const f32x4_t x4 = TURNED ? factors[4 * t + g] : lsc[t & 3][g];
       f->c[g] = factor(x4[0]);
       f->lv[g] = x4[1];
       f->iv[g] = x4[2];
@@ -736,6 +772,85 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 2) void k_many(
   r.finish();
 }
 
+// The same with tiles that k_turn has laid out.
+template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 2) void k_many_turned(const AttnArgs a, int streams) {
+  using M = Many<D, true>;
+  __shared__ __attribute__((aligned(16))) half8_t lk[2][M::kKPieces], lv[2][M::kVPieces];
+  ManyRows<D, true> r(a, lk, lv, nullptr);
+  if (!r.begin(streams)) return;
+  if (r.t0 < r.t1) {
+    r.fetch_k(r.t0);
+    r.fetch_v(r.t0);
+    r.arrived();
+    __syncthreads();
+    for (int t = r.t0; t < r.t1; ++t) {
+      if (t + 1 < r.t1) {
+        r.fetch_k(t + 1);
+        r.fetch_v(t + 1);
+      }
+      f32x16_t st[2];
+      half8_t p[4];
+      r.scores(t, st);
+      Factors f;
+      r.raise(r.largest(t, st, &f));
+      r.weights(st, f, p);
+      r.values(t, p);
+      r.arrived();
+      __syncthreads();
+    }
+  }
+  r.finish();
+}
+
+// Lays out the tiles that a call's rows will read, in f16 and in the order of LDS: for tile t of a stream (sequence,
+// cache head) 8 d pieces of keys [d / 8][64] and 8 d of values [8][d], and the factors of its four blocks of
+// 16 keys.  One workgroup a tile; lanes follow the pieces, so that writes are whole lines.
+template <int D> __global__ __launch_bounds__(256) void k_turn(const AttnArgs a) {
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, kvh = blockIdx.y, b = blockIdx.z;
+  const Seq s = seq_of(a, b);
+  if (s.rows == 0) return;
+  int32_t last, x;
+  visible(a, static_cast<int64_t>(s.len) - 1, s.len, &x, &last);
+  const int t = first_of(a, s) + blockIdx.x;  // as many workgroups as a stream has room for tiles
+  if (t >= (last + 63) / 64) return;
+  const int64_t tile = (static_cast<int64_t>(b) * a.c.heads + kvh) * a.turned_tiles + blockIdx.x;
+  half8_t* out = static_cast<half8_t*>(a.turned) + tile * (16 * D);
+  const int page_mask = a.c.page - 1;
+  const auto page = [&](int key) { return key < s.len ? page_of(a.c, b, key >> a.page_shift) : -1; };
+  {
+    const int key = 64 * t + lane, pg = page(key & ~15);
+    const int8_t* p = a.c.k + ((static_cast<int64_t>(pg < 0 ? 0 : pg) * a.c.heads + kvh) * a.c.page + (key & page_mask)) * D;
+    u32x4_t q[D / 64];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) q[i] = *reinterpret_cast<const u32x4_t*>(p + 16 * (4 * i + wave));
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const int u = 4 * i + wave;
+      out[2 * u * 64 + lane] = codes_to_half8(q[i][0], q[i][1]);
+      out[(2 * u + 1) * 64 + lane] = codes_to_half8(q[i][2], q[i][3]);
+    }
+  }
+  {
+    const int key = 64 * t + 16 * wave, pg = page(key);
+    const int8_t* p = a.c.v + ((static_cast<int64_t>(pg < 0 ? 0 : pg) * a.c.heads + kvh) * D + lane) * a.c.page + (key & page_mask);
+    u32x4_t q[D / 64];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) q[i] = *reinterpret_cast<const u32x4_t*>(p + 64 * i * a.c.page);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      // keys 0-3 and 8-11 of the sixteen, then 4-7 and 12-15: as the weights lie in their registers
+      out[8 * D + 2 * wave * D + 64 * i + lane] = codes_to_half8(q[i][0], q[i][2]);
+      out[8 * D + (2 * wave + 1) * D + 64 * i + lane] = codes_to_half8(q[i][1], q[i][3]);
+    }
+    if (lane == 0) {
+      const int64_t slot = static_cast<int64_t>(pg < 0 ? 0 : pg) * a.c.heads + kvh;
+      float c, y, z;
+      block_scales(a, a.c.ks[slot], a.c.vs[slot], pg >= 0, &c, &y, &z);
+      static_cast<f32x4_t*>(a.factors)[4 * tile + wave] = f32x4_t{c, y, z, 0.0f};
+    }
+  }
+}
+
 // Heads of 256: a wave's rows fill the registers of a SIMD, so the overlap is made within the wave.  Step t takes
 // the weights of tile t beside the scores of tile t + 1 on the matrix cores, and finds the maximum of tile t + 1
 // and stages what comes next beside the values of tile t.
@@ -789,42 +904,91 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 1) void k_wide(
   r.finish();
 }
 
+template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 1) void k_wide_turned(const AttnArgs a, int streams) {
+  using M = Many<D, true>;
+  __shared__ __attribute__((aligned(16))) half8_t lk[2][M::kKPieces], lv[2][M::kVPieces];
+  ManyRows<D, true> r(a, lk, lv, nullptr);
+  if (!r.begin(streams)) return;
+  f32x16_t st[2][2];
+  Factors fa[2];
+  if (r.t0 < r.t1) {
+    r.fetch_k(r.t0);
+    r.fetch_v(r.t0);
+    if (r.t0 + 1 < r.t1) r.fetch_k(r.t0 + 1);
+    r.arrived();
+  }
+  __syncthreads();
+  if (r.t0 < r.t1) {
+    r.scores(r.t0, st[0]);
+    r.raise(r.largest(r.t0, st[0], &fa[0]));
+  }
+  __syncthreads();  // keys t0 are read before keys t0 + 2 come
+  // the last step's scores are of a tile that was never fetched: finite or not, they are not used
+  const auto step = [&](int t, f32x16_t* now, f32x16_t* next, const Factors& f, Factors* fnext) {
+    const bool more = t + 1 < r.t1;
+    if (t + 2 < r.t1) r.fetch_k(t + 2);
+    if (more) r.fetch_v(t + 1);
+    r.scores(t + 1, next);
+    half8_t p[4];
+    r.weights(now, f, p);
+    r.values(t, p);
+    if (more) r.raise(r.largest(t + 1, next, fnext));
+    r.arrived();
+    __syncthreads();
+  };
+  int t = r.t0;
+  for (; t + 1 < r.t1; t += 2) {
+    step(t, st[0], st[1], fa[0], &fa[1]);
+    step(t + 1, st[1], st[0], fa[1], &fa[0]);
+  }
+  if (t < r.t1) step(t, st[0], st[1], fa[0], &fa[1]);
+  r.finish();
+}
+
 // ----------------------------------------------------------------------------------------- join
-// One workgroup a row: D / 4 threads a part, the parts dealt to 1024 / D teams.
-template <int D> __global__ __launch_bounds__(256) void k_join(const AttnArgs a) {
+// D / 4 threads a part.  Many parts of a row are dealt to the 1024 / D teams of a workgroup; with few, each
+// team takes a row (FEW).
+template <int D, bool FEW> __global__ __launch_bounds__(256) void k_join(const AttnArgs a) {
   constexpr int TEAM = D / 4, TEAMS = 256 / TEAM;
-  __shared__ __attribute__((aligned(16))) f32x4_t lo[TEAMS][TEAM];
+  __shared__ __attribute__((aligned(16))) f32x4_t lo[FEW ? 1 : TEAMS][TEAM];
   __shared__ float red[256];
-  const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, team = tid / TEAM, e = tid % TEAM;
+  const int64_t row = FEW ? static_cast<int64_t>(blockIdx.x) * TEAMS + team : blockIdx.x;
+  if (FEW && row >= a.total * a.heads) return;
   const float* ml = a.part_ml + row * a.splits * 2;
   float m = kNone;
-  for (int i = tid; i < a.splits; i += 256) m = ml[2 * i + 1] != 0.0f ? __builtin_fmaxf(m, ml[2 * i]) : m;
-  red[tid] = m;
-  __syncthreads();
-#pragma unroll
-  for (int off = 128; off >= 1; off >>= 1) {
-    if (tid < off) red[tid] = __builtin_fmaxf(red[tid], red[tid + off]);
+  if constexpr (FEW) {
+    for (int i = 0; i < a.splits; ++i) m = ml[2 * i + 1] != 0.0f ? __builtin_fmaxf(m, ml[2 * i]) : m;
+  } else {
+    for (int i = tid; i < a.splits; i += 256) m = ml[2 * i + 1] != 0.0f ? __builtin_fmaxf(m, ml[2 * i]) : m;
+    red[tid] = m;
     __syncthreads();
+#pragma unroll
+    for (int off = 128; off >= 1; off >>= 1) {
+      if (tid < off) red[tid] = __builtin_fmaxf(red[tid], red[tid + off]);
+      __syncthreads();
+    }
+    m = red[0];
   }
-  m = red[0];
   f32x4_t o = {0, 0, 0, 0};
   float l = 0.0f;
-  for (int i = team; i < a.splits; i += TEAMS) {
+  for (int i = FEW ? 0 : team; i < a.splits; i += FEW ? 1 : TEAMS) {
     const float li = ml[2 * i + 1];
     if (li == 0.0f) continue;  // nothing visible in that part: its values were not written
     const float by = exp2_fast(ml[2 * i] - m);
     l = __builtin_fmaf(li, by, l);
     o += *reinterpret_cast<const f32x4_t*>(a.part_o + (row * a.splits + i) * D + 4 * e) * by;
   }
-  __syncthreads();
-  lo[team][e] = o;
-  red[tid] = l;
-  __syncthreads();
-  if (team) return;
-  for (int i = 1; i < TEAMS; ++i) {
-    o += lo[i][e];
-    l += red[i * TEAM];
+  if constexpr (!FEW) {
+    __syncthreads();
+    lo[team][e] = o;
+    red[tid] = l;
+    __syncthreads();
+    if (team) return;
+    for (int i = 1; i < TEAMS; ++i) {
+      o += lo[i][e];
+      l += red[i * TEAM];
+    }
   }
   const int64_t tok = row / a.heads;
   const int h = static_cast<int>(row - tok * a.heads);
@@ -841,16 +1005,29 @@ template <int D> int launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream
     const int64_t grid = static_cast<int64_t>(streams) * a.row_tiles;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     const dim3 g(static_cast<uint32_t>(grid)), t(attn::Many<D>::kThreads);
-    if constexpr (D <= 128) hipLaunchKernelGGL((attn::k_many<D>), g, t, 0, stream, a, streams);
-    else hipLaunchKernelGGL((attn::k_wide<D>), g, t, 0, stream, a, streams);
+    if constexpr (D > 64) {
+      if (p.turned) {
+        hipLaunchKernelGGL((attn::k_turn<D>), dim3(p.turned, a.c.heads, a.c.batch), dim3(256), 0, stream, a);
+        if constexpr (D <= 128) hipLaunchKernelGGL((attn::k_many_turned<D>), g, t, 0, stream, a, streams);
+        else hipLaunchKernelGGL((attn::k_wide_turned<D>), g, t, 0, stream, a, streams);
+      }
+    }
+    if (!p.turned) {
+      if constexpr (D <= 128) hipLaunchKernelGGL((attn::k_many<D>), g, t, 0, stream, a, streams);
+      else hipLaunchKernelGGL((attn::k_wide<D>), g, t, 0, stream, a, streams);
+    }
   } else {
     const dim3 grid(a.splits, a.c.heads * a.row_tiles, a.c.batch);
     if (p.rt == 2) hipLaunchKernelGGL((attn::k_few<D, 2, 4>), grid, dim3(256), 0, stream, a);
     else if (p.waves == 4) hipLaunchKernelGGL((attn::k_few<D, 1, 4>), grid, dim3(256), 0, stream, a);
     else if constexpr (D <= 128) hipLaunchKernelGGL((attn::k_few<D, 1, 8>), grid, dim3(512), 0, stream, a);
   }
-  if (a.splits > 1)
-    hipLaunchKernelGGL((attn::k_join<D>), dim3(static_cast<uint32_t>(a.total * a.heads)), dim3(256), 0, stream, a);
+  if (a.splits > 1) {
+    const int64_t rows = a.total * a.heads;
+    if (a.splits <= 8)
+      hipLaunchKernelGGL((attn::k_join<D, true>), dim3(static_cast<uint32_t>((rows + 1024 / D - 1) / (1024 / D))), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((attn::k_join<D, false>), dim3(static_cast<uint32_t>(rows)), dim3(256), 0, stream, a);
+  }
   return static_cast<int>(hipGetLastError());
 }
 
