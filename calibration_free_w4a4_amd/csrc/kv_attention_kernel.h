@@ -772,36 +772,6 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 2) void k_many(
   r.finish();
 }
 
-// The same with tiles that k_turn has laid out.
-template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 2) void k_many_turned(const AttnArgs a, int streams) {
-  using M = Many<D, true>;
-  __shared__ __attribute__((aligned(16))) half8_t lk[2][M::kKPieces], lv[2][M::kVPieces];
-  ManyRows<D, true> r(a, lk, lv, nullptr);
-  if (!r.begin(streams)) return;
-  if (r.t0 < r.t1) {
-    r.fetch_k(r.t0);
-    r.fetch_v(r.t0);
-    r.arrived();
-    __syncthreads();
-    for (int t = r.t0; t < r.t1; ++t) {
-      if (t + 1 < r.t1) {
-        r.fetch_k(t + 1);
-        r.fetch_v(t + 1);
-      }
-      f32x16_t st[2];
-      half8_t p[4];
-      r.scores(t, st);
-      Factors f;
-      r.raise(r.largest(t, st, &f));
-      r.weights(st, f, p);
-      r.values(t, p);
-      r.arrived();
-      __syncthreads();
-    }
-  }
-  r.finish();
-}
-
 // Lays out the tiles that a call's rows will read, in f16 and in the order of LDS: for tile t of a stream (sequence,
 // cache head) 8 d pieces of keys [d / 8][64] and 8 d of values [8][d], and the factors of its four blocks of
 // 16 keys.  One workgroup a tile; lanes follow the pieces, so that writes are whole lines.
@@ -904,7 +874,7 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 1) void k_wide(
   r.finish();
 }
 
-template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 1) void k_wide_turned(const AttnArgs a, int streams) {
+template <int D> __global__ __launch_bounds__(Many<D>::kThreads, D <= 128 ? 2 : 1) void k_turned(const AttnArgs a, int streams) {
   using M = Many<D, true>;
   __shared__ __attribute__((aligned(16))) half8_t lk[2][M::kKPieces], lv[2][M::kVPieces];
   ManyRows<D, true> r(a, lk, lv, nullptr);
@@ -1008,8 +978,7 @@ template <int D> int launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream
     if constexpr (D > 64) {
       if (p.turned) {
         hipLaunchKernelGGL((attn::k_turn<D>), dim3(p.turned, a.c.heads, a.c.batch), dim3(256), 0, stream, a);
-        if constexpr (D <= 128) hipLaunchKernelGGL((attn::k_many_turned<D>), g, t, 0, stream, a, streams);
-        else hipLaunchKernelGGL((attn::k_wide_turned<D>), g, t, 0, stream, a, streams);
+        hipLaunchKernelGGL((attn::k_turned<D>), g, t, 0, stream, a, streams);
       }
     }
     if (!p.turned) {
