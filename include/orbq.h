@@ -378,9 +378,12 @@ int orbq_kv_read(const orbq_kv_cache* cache, const orbq_page_table* table, const
  *         and strides.  Products on the codes in f16 with fp32 accumulation, softmax in fp32.
  *   lse   [device] float[total][heads] or NULL: natural log of the sum of exponentials
  *   max_new  bound of the queries of a sequence;  max_len  expected bound of lens (0: the page table's);
- *         it only chooses how the work is split, any value gives the same result up to rounding
- *   workspace [device] >= orbq_kv_attention_workspace_bytes of the same arguments (max_len given as used:
- *         the page table's bound if 0), 256-byte aligned, where that is not 0: parts of split sequences
+ *         it only chooses how the work is done, any value gives the same result up to rounding
+ *   workspace [device] >= orbq_kv_attention_workspace_bytes of the same arguments (max_len as used: the page
+ *         table's bound max_pages * page_tokens if 0 or above it), 256-byte aligned, where that is not 0.  It holds
+ *         the parts of sequences that are split over workgroups and, for many rows of heads of 128 or 256 and a
+ *         max_len of the page table's bound, the codes once in f16 (4 head_dim bytes a token and cache head,
+ *         at most 1 GiB, else not taken).  Nothing is kept in it between calls.
  * Few queries take a form bound by the cache's bytes, many one bound by the matrix cores. */
 size_t orbq_kv_attention_workspace_bytes(const orbq_kv_cache* cache, int32_t batch, int64_t total, int32_t max_new,
                                          int32_t heads, int64_t max_len, int32_t causal_block, int32_t window);

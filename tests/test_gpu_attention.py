@@ -519,3 +519,25 @@ def test_refusals_of_the_binding(orbq):
     assert e.value.status == -4
     o = orbq.kv_attention(big, q, t, ints([0]), workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
     assert not o.any()
+
+
+@pytest.mark.parametrize("d,heads,kv_heads,lens,new,kw", [
+    (128, 4, 4, [1500, 1100], [1030, 1100], dict(block=1)),
+    (128, 6, 2, [700, 900], [400, 900], dict(block=37, window=130, absent=((0, 3), (1, 0), (1, 9)))),
+    (256, 2, 1, [800, 5], [300, 600], dict(block=0, absent=((0, 12),))),
+    (256, 1, 1, [9000], [700], dict(block=1)),
+    (128, 2, 2, [9000], [1200], dict(block=300, window=2000))])
+def test_many_rows_with_tiles_turned_before_or_on_the_way(orbq, d, heads, kv_heads, lens, new, kw):
+    """Enough rows that the tiles are laid out in the workspace first; a guess at the lengths below what the
+    table holds forbids that, and gives the same up to rounding."""
+    log(f"turned d={d} lens={lens} new={new} {kw}")
+    kw = dict(kw)
+    block, window = kw.get("block", 0), kw.get("window", 0)
+    c, q, table, o = run_attention(orbq, "bf16", d, 64, heads, kv_heads, lens, new, **kw)
+    cu = ints(np.concatenate([[0], np.cumsum(new)]))
+    args = dict(cu=cu, max_new=max(new), causal_block=block, window=window)
+    full = table.shape[1] * 64
+    assert orbq.kv_attention_workspace_bytes(c, len(lens), sum(new), max(new), heads, full, block, window) >= \
+        len(lens) * kv_heads * 64 * 4 * d                       # the f16 tiles are there
+    o2 = orbq.kv_attention(c, q, ints(table), ints(lens), max_len=max(lens) // 2, **args)
+    assert (o2.float() - o.float()).abs().max().item() <= 2.0 ** -7 * o.float().abs().max().item()
