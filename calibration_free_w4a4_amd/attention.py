@@ -89,6 +89,13 @@ def _like(x):
     return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
+def _written(x, y, func: str):
+    """Token and head strides of the output y given for x."""
+    if y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
+        raise _bad(func, "out must have the inputs' shapes, types and device")
+    return _lay(y, func, "out")[3:5]
+
+
 def _turn(func, rope, positions, q, k, inverse, out):
     n, h, d, xt, xh, x, code = _lay(q, func, "q")
     dev = rope.device
@@ -97,21 +104,18 @@ def _turn(func, rope, positions, q, k, inverse, out):
     if positions.dtype != torch.float32 or positions.get_device() != dev or positions.dim() != 2 or \
             positions.shape[1] != len(rope.dims) or not positions.is_contiguous():
         raise _bad(func, f"positions must be contiguous float32 [tokens, {len(rope.dims)}] on cuda:{dev}")
-    if out is None:
-        yq, yk = _like(q), None if k is None else _like(k)
-    else:
+    if out is not None:
         yq, yk = (out, None) if k is None else out
-        for a, b in ((q, yq), (k, yk)):
-            if a is not None and (b.shape != a.shape or b.dtype != a.dtype or b.device != a.device):
-                raise _bad(func, "out must have the inputs' shapes, types and device")
-    _, _, _, yt, yh, y, _ = _lay(yq, func, "out")
-    heads = _HEADS.pack(x, y, h, xt, xh, yt, yh)
+    else:
+        yq = _like(q)
+    heads = _HEADS.pack(x, yq.data_ptr(), h, xt, xh, *((h * d, d) if out is None else _written(q, yq, func)))
     if k is not None:
         n2, h, d2, xt, xh, x, code2 = _lay(k, func, "k")
-        _, _, _, yt, yh, y, _ = _lay(yk, func, "out")
         if n2 != n or d2 != d or code2 != code or k.get_device() != dev:
             raise _bad(func, "q and k must agree in tokens, head_dim, type and device")
-        heads += _HEADS.pack(x, y, h, xt, xh, yt, yh)
+        if out is None:
+            yk = _like(k)
+        heads += _HEADS.pack(x, yk.data_ptr(), h, xt, xh, *((h * d, d) if out is None else _written(k, yk, func)))
     st = load().orbq_rope_apply(rope.packed, positions.data_ptr(), positions.shape[0], n, d, heads, 1 if k is None else 2,
                                 code, inverse, _stream(dev))
     if st:
@@ -197,7 +201,7 @@ def kv_append(cache: KVCache, k, v, table, start, cu=None, max_new=None) -> None
 def kv_read(cache: KVCache, table, first, cu, total: int, max_tokens=None, dtype=torch.bfloat16, out=None):
     """(k, v) [total, kv_heads, head_dim] of tokens first[b] .. of each sequence, cu as in kv_append."""
     if out is None:
-        k = torch.empty((total, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.k_codes.device)
+        k = cache.k_scales.new_empty((total, cache.kv_heads, cache.head_dim), dtype=dtype)
         out = (k, torch.empty_like(k))
     elif out[0].shape[0] != total:
         raise _bad("kv_read", f"out must have {total} tokens")
@@ -236,10 +240,9 @@ def kv_attention(cache: KVCache, q, table, lens, cu=None, max_new=None, causal_b
     if max_new is None:
         max_new = n if cu else n // max(1, batch)
     if out is None:
-        out = _like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device:
-        raise _bad(func, "out must have q's shape, type and device")
-    _, _, _, ot, oh, op, _ = _lay(out, func, "out")
+        out, ot, oh = _like(q), h * d, d
+    else:
+        ot, oh = _written(q, out, func)
     if lse is not None and (lse.shape != (n, h) or lse.dtype != torch.float32 or lse.get_device() != dev or
                             not lse.is_contiguous()):
         raise _bad(func, f"lse must be contiguous float32 [{n}, {h}] on cuda:{dev}")
@@ -251,7 +254,7 @@ def kv_attention(cache: KVCache, q, table, lens, cu=None, max_new=None, causal_b
         if need:
             workspace = q.new_empty((need + 1) // 2)
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = lib.orbq_kv_attention(cache.packed, t, lens, cu, n, max_new, max_len, qp, qt, qh, h, op, ot, oh,
+    st = lib.orbq_kv_attention(cache.packed, t, lens, cu, n, max_new, max_len, qp, qt, qh, h, out.data_ptr(), ot, oh,
                                0 if lse is None else lse.data_ptr(), code, d ** -0.5 if scale is None else scale, causal_block,
                                window, ws, ws_bytes, _stream(dev))
     if st:

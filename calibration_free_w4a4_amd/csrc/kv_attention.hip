@@ -20,23 +20,31 @@ AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t k
   // the keys that one row tile can see, in 64-key tiles
   int64_t span = max_len;
   if (window) span = std::min<int64_t>(span, static_cast<int64_t>(window) + max_new + causal_block);
-  const int64_t tiles = std::max<int64_t>(1, (span + 63) / 64 + 1);
+  const int64_t tiles = std::max<int64_t>(1, (span + 63) / 64 + (window ? 1 : 0));
   const int64_t groups = static_cast<int64_t>(batch) * kv_heads * p.row_tiles;
   int64_t splits = 1;
   p.waves = 4;
   if (p.many) {
-    // Workgroups resident at once: one a CU (LDS and registers), three with heads of 64.  A split costs its parts'
-    // way through memory, about as long as 400 keys of its rows take; it pays where it fills the last round.
-    const int64_t want = static_cast<int64_t>(cus) * (d == 64 ? 3 : 1), most = std::max<int64_t>(1, tiles / 8);
-    const auto rounds = [&](int64_t n) {
-      return static_cast<double>((groups * n + want - 1) / want) / n + (n > 1 ? n * 400.0 / span * groups / want : 0.0);
+    // Workgroups resident at once: one a CU (LDS and registers), three with heads of 64.  In tiles of one
+    // workgroup: the rounds of splits, the joining launch (3) and the parts' way through memory, which takes a
+    // full card about as long as 400 keys of the same rows.
+    const int64_t want = static_cast<int64_t>(cus) * (d == 64 ? 3 : 1);
+    const auto cost = [&](int64_t n) {
+      return static_cast<double>((groups * n + want - 1) / want * ((tiles + n - 1) / n)) +
+             (n > 1 ? 3.0 + 400.0 / 64 * n * groups / want : 0.0);
     };
     const auto consider = [&](int64_t n) {
-      if (n > 1 && n <= most && rounds(n) < rounds(splits)) splits = n;
+      if (n > 1 && 2 * n <= tiles && cost(n) < cost(splits)) splits = n;
     };
-    for (int n = 2; n <= 8; ++n) consider(n);
+    for (int n = 2; n <= 16; ++n) consider(n);
     for (int n = 1; n <= 3; ++n) consider(n * want / groups);
-    if (bound && d > 64 && p.row_tiles >= 4 && static_cast<int64_t>(batch) * kv_heads * tiles * d <= (int64_t{1} << 22))
+    // Turning the codes once a call instead of once a row tile pays where some eight row tiles read each of
+    // them (4680 queries over 32760 tokens, 12 heads of 128: 1165 us without, 1005 with; 327 queries with a
+    // window of 19: 28 without, 36 with); with heads of 64 staging is too small a share (82 without, 89 with).
+    const int64_t tile_tokens = std::max<int64_t>(1, many_rows(d) / (heads / kv_heads));
+    int64_t readers = p.row_tiles;
+    if (window) readers = std::min<int64_t>(readers, (static_cast<int64_t>(window) + causal_block + 63) / tile_tokens + 1);
+    if (bound && d > 64 && readers >= 8 && static_cast<int64_t>(batch) * kv_heads * tiles * d <= (int64_t{1} << 22))
       p.turned = static_cast<int32_t>(tiles);  // at most 1 GiB of workspace
   } else if (p.rt == 1 && d <= 128 && (tiles * d <= 17 * 128 || (4 * groups >= 3 * cus && groups <= cus))) {
     p.waves = 8;

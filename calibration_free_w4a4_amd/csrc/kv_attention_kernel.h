@@ -842,26 +842,31 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 1) void k_wide(
     r.stage_k(r.t0);
     r.stage_v(r.t0);
     r.load_k(r.t0 + 1);
+    r.load_v(r.t0 + 1);
     r.pages_k(r.t0 + 2);
+    r.pages_v(r.t0 + 2);
     r.stage_k(r.t0 + 1);
+    r.load_k(r.t0 + 2);
+    r.pages_k(r.t0 + 3);
   }
   __syncthreads();
   if (r.t0 < r.t1) {
     r.scores(r.t0, st[0]);
     r.raise(r.largest(r.t0, st[0], &fa[0]));
   }
+  __syncthreads();  // keys t0 are read before keys t0 + 2 are staged
   const auto step = [&](int t, f32x16_t* now, f32x16_t* next, const Factors& f, Factors* fnext) {
-    r.load_k(t + 2);
-    r.load_v(t + 1);
-    r.pages_k(t + 3);
-    r.pages_v(t + 2);
+    r.stage_k(t + 2);
+    r.stage_v(t + 1);
+    r.load_k(t + 3);
+    r.load_v(t + 2);
+    r.pages_k(t + 4);
+    r.pages_v(t + 3);
     r.scores(t + 1, next);
     half8_t p[4];
     r.weights(now, f, p);
     r.values(t, p);
     const float top = r.largest(t + 1, next, fnext);
-    r.stage_k(t + 2);
-    r.stage_v(t + 1);
     if (t + 1 < r.t1) r.raise(top);
     __syncthreads();
   };

@@ -161,6 +161,17 @@ __global__ __launch_bounds__(threads_for(D* PAGE)) void k_append(const KvCache c
   const int64_t slot = static_cast<int64_t>(pg) * c.heads + head;
   float* scales = (values ? c.vs : c.ks) + slot;
   const float old = had ? *scales : 0.0f;
+  // values: old codes that share a 16-byte piece with new ones are fetched meanwhile
+  constexpr int PIECES = D * PAGE / 16 / NT;
+  uint8_t* const block = reinterpret_cast<uint8_t*>(values ? c.v : c.k) + slot * (D * PAGE);
+  u32x4_t kept[PIECES];
+  if (values && had % 16) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const int at = i * NT + tid, t = at % (PAGE / 16) * 16;
+      if (t < had && t + 16 > had) kept[i] = *reinterpret_cast<const u32x4_t*>(block + 16 * at);
+    }
+  }
   // the largest magnitude, as the integer that its bits are
   const uint32_t big = largest_bits<DT, PER * W>(&raw[0][0]);
   uint32_t bits = wide_max<NT>(big, top);
@@ -194,11 +205,10 @@ __global__ __launch_bounds__(threads_for(D* PAGE)) void k_append(const KvCache c
   const auto write = [&](auto finite) {
     constexpr bool F = decltype(finite)::value;
     if (!values) {
-      uint8_t* dst = reinterpret_cast<uint8_t*>(c.k) + slot * (D * PAGE);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int t = S::token(tid, i);
-        u32x2_t* to = reinterpret_cast<u32x2_t*>(dst + t * D + S::entry(tid));
+        u32x2_t* to = reinterpret_cast<u32x2_t*>(block + t * D + S::entry(tid));
         if (t >= had && t < end) {
           *to = u32x2_t{codes_of<F>(&f[i][0], inv), codes_of<F>(&f[i][4], inv)};
         } else if (t < had && grow) {
@@ -226,16 +236,16 @@ __global__ __launch_bounds__(threads_for(D* PAGE)) void k_append(const KvCache c
   else write(std::true_type{});
   if (!values) return;
   __syncthreads();
-  uint8_t* dst = reinterpret_cast<uint8_t*>(c.v) + slot * (D * PAGE);
-  for (int at = tid; at < D * PAGE / 16; at += NT) {
-    const int e = at / (PAGE / 16), t = at % (PAGE / 16) * 16;
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int at = i * NT + tid, e = at / (PAGE / 16), t = at % (PAGE / 16) * 16;
     if (t >= end || (t + 16 <= had && !grow)) continue;  // nothing to write here
-    u32x4_t* to = reinterpret_cast<u32x4_t*>(dst + 16 * at);
+    u32x4_t* to = reinterpret_cast<u32x4_t*>(block + 16 * at);
     u32x4_t q;
 #pragma unroll
     for (int j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const uint32_t*>(&turned[e * LD + t + 4 * j]);
     if (t < had) {
-      u32x4_t o = *to;
+      u32x4_t o = t + 16 > had ? kept[i] : *to;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t mask = below(t + 4 * j, had);
