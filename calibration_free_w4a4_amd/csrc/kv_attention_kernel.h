@@ -150,7 +150,7 @@ __device__ __forceinline__ void store4(const AttnArgs& a, int64_t at, f32x4_t v)
 // ------------------------------------------------------------------------------------------ few
 template <int D, int RT, int NW> __global__ __launch_bounds__(64 * NW) void k_few(const AttnArgs a) {
   constexpr int NC = D / 64, ND = D / 16;
-  __shared__ __attribute__((aligned(16))) f32x4_t join_o[NW / 2][RT][ND][64];
+  __shared__ __attribute__((aligned(16))) f32x4_t join_o[NW][RT][ND][64];
   __shared__ float join_m[NW][RT][16], join_l[NW][RT][16];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l15 = lane & 15, g = lane >> 4;
   const int split = blockIdx.x, kvh = blockIdx.y / a.row_tiles, tile = blockIdx.y - kvh * a.row_tiles, b = blockIdx.z;
@@ -361,45 +361,34 @@ template <int D, int RT, int NW> __global__ __launch_bounds__(64 * NW) void k_fe
     for (int i = 0; i < ND; ++i) o[rt][i] *= by;
   }
 #pragma unroll
-  for (int half = NW / 2; half >= 1; half >>= 1) {
-    if (wave >= half && wave < 2 * half) {
+  for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int i = 0; i < ND; ++i) join_o[wave - half][rt][i][lane] = o[rt][i];
-    }
-    __syncthreads();
-    if (wave < half) {
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int i = 0; i < ND; ++i) o[rt][i] += join_o[wave][rt][i][lane];
-    }
-    __syncthreads();
-  }
-  if (wave) return;
+    for (int i = 0; i < ND; ++i) join_o[wave][rt][i][lane] = o[rt][i];
+  __syncthreads();
+  // each wave sums and writes its share of the entries
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int r = r0 + 16 * rt + l15;
-    if (r >= r1) continue;
-    const int tok = r / a.group, h = kvh * a.group + r - tok * a.group;
-    const int64_t row = (s.row0 + tok) * a.heads + h;
+    const bool live = r < r1;
+    const int rr = live ? r : r0, tok = rr / a.group, h = kvh * a.group + rr - tok * a.group;
+    const int64_t row = (s.row0 + tok) * a.heads + h, at = (s.row0 + tok) * a.ot + h * a.oh;
+    float* po = a.part_o + (row * a.splits + split) * D;
+    const float by = lt[rt] == 0.0f ? 0.0f : 1.0f / lt[rt];
+    for (int i = wave; i < ND; i += NW) {
+      f32x4_t x = join_o[0][rt][i][lane];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) x += join_o[w][rt][i][lane];
+      if (!live) continue;
+      if (a.splits > 1) *reinterpret_cast<f32x4_t*>(po + 16 * i + 4 * g) = x;
+      else store4(a, at + 16 * i + 4 * g, x * by);
+    }
+    if (wave || g || !live) continue;
     if (a.splits > 1) {
-      float* po = a.part_o + (row * a.splits + split) * D;
-#pragma unroll
-      for (int i = 0; i < ND; ++i) *reinterpret_cast<f32x4_t*>(po + 16 * i + 4 * g) = o[rt][i];
-      if (g == 0) {
-        float* ml = a.part_ml + (row * a.splits + split) * 2;
-        ml[0] = mt[rt];
-        ml[1] = lt[rt];
-      }
-    } else {
-      const float by = lt[rt] == 0.0f ? 0.0f : 1.0f / lt[rt];
-      const int64_t at = (s.row0 + tok) * a.ot + h * a.oh;
-#pragma unroll
-      for (int i = 0; i < ND; ++i) store4(a, at + 16 * i + 4 * g, o[rt][i] * by);
-      if (a.lse && g == 0)
-        a.lse[row] = lt[rt] == 0.0f ? -__builtin_inff() : (mt[rt] + __builtin_log2f(lt[rt])) * kLn2;
+      float* ml = a.part_ml + (row * a.splits + split) * 2;
+      ml[0] = mt[rt];
+      ml[1] = lt[rt];
+    } else if (a.lse) {
+      a.lse[row] = lt[rt] == 0.0f ? -__builtin_inff() : (mt[rt] + __builtin_log2f(lt[rt])) * kLn2;
     }
   }
 }
