@@ -20,11 +20,12 @@
 // the rescaling factors are one value a lane.
 //
 // Two forms:
-//   few   16 or 32 rows a workgroup (token-by-token serving): bound by the cache's bytes.  Four waves, or
+//   few   up to 64 rows, 16 or 32 a workgroup (token-by-token serving): bound by the cache's bytes.  Four waves, or
 //         eight for a short cache, take 64-key tiles in turn straight from memory into registers, and are
 //         joined at the end.
-//   many  128 rows a workgroup: bound by the matrix cores and the softmax's vector work.  Codes
-//         are turned into f16 once a workgroup on their way into LDS, double buffered.
+//   many  128 or 256 rows a workgroup: bound by the matrix cores, the softmax's vector work and the LDS reads
+//         between them.  Codes are turned into f16 once a workgroup on their way into LDS, double
+//         buffered, or once a call by k_turn, and then fetched into LDS as they are.
 // Either splits the keys over workgroups where there are few rows; k_join joins the parts.
 #pragma once
 
@@ -981,9 +982,11 @@ template <int D> int launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream
     }
   } else {
     const dim3 grid(a.splits, a.c.heads * a.row_tiles, a.c.batch);
-    if (p.rt == 2) hipLaunchKernelGGL((attn::k_few<D, 2, 4>), grid, dim3(256), 0, stream, a);
-    else if (p.waves == 4) hipLaunchKernelGGL((attn::k_few<D, 1, 4>), grid, dim3(256), 0, stream, a);
-    else if constexpr (D <= 128) hipLaunchKernelGGL((attn::k_few<D, 1, 8>), grid, dim3(512), 0, stream, a);
+    if constexpr (D <= 128) {
+      if (p.rt == 2) hipLaunchKernelGGL((attn::k_few<D, 2, 4>), grid, dim3(256), 0, stream, a);
+      else if (p.waves == 8) hipLaunchKernelGGL((attn::k_few<D, 1, 8>), grid, dim3(512), 0, stream, a);
+    }
+    if (p.rt == 1 && p.waves == 4) hipLaunchKernelGGL((attn::k_few<D, 1, 4>), grid, dim3(256), 0, stream, a);
   }
   if (a.splits > 1) {
     const int64_t rows = a.total * a.heads;
