@@ -29,6 +29,8 @@ int check_type(orbq_dtype t, bool f32, const char* what) {
 
 constexpr int64_t kMaxTokens = int64_t{1} << 30;  // of a sequence: positions are 32-bit in the kernels
 
+constexpr int64_t kMaxRows = int64_t{1} << 36;    // queries times query heads of one cache head: row tiles are 32-bit
+
 int check_cache(const orbq_kv_cache* c, const orbq_page_table* t, orbq::KvCache* out, const char* what) {
   if (!c || !t) return set_error(ORBQ_ERR_INVALID_ARG, "%s: cache or page table is NULL", what);
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
@@ -194,7 +196,8 @@ ORBQ_API size_t orbq_kv_attention_workspace_bytes(const orbq_kv_cache* cache, in
                                                   int32_t max_new, int32_t heads, int64_t max_len, int32_t causal_block,
                                                   int32_t window) {
   if (!cache || batch < 1 || total < 1 || max_new < 1 || heads < 1 || cache->kv_heads < 1 || heads % cache->kv_heads ||
-      max_len < 0 || max_len > kMaxTokens || causal_block < 0 || window < 0)
+      max_len < 0 || max_len > kMaxTokens || causal_block < 0 || window < 0 ||
+      static_cast<int64_t>(max_new) * (heads / cache->kv_heads) > kMaxRows)
     return 0;
   const orbq::AttnPlan p = orbq::plan_attention(batch, max_new, heads, cache->kv_heads, cache->head_dim, max_len, causal_block,
                                                 window, true, orbq::device_cus());
@@ -216,6 +219,8 @@ ORBQ_API int orbq_kv_attention(const orbq_kv_cache* cache, const orbq_page_table
   if (heads < 1 || heads % a.c.heads)
     return set_error(ORBQ_ERR_INVALID_ARG, "%s: %d query heads for %d cache heads", what, heads, a.c.heads);
   if (heads > 16384) return set_error(ORBQ_ERR_UNSUPPORTED, "%s: heads above 16384", what);
+  if (static_cast<int64_t>(max_new) * (heads / a.c.heads) > kMaxRows)
+    return set_error(ORBQ_ERR_UNSUPPORTED, "%s: more than 2^36 rows a cache head", what);
   if (max_len < 0) return set_error(ORBQ_ERR_INVALID_ARG, "%s: max_len negative", what);
   if (causal_block < 0 || window < 0) return set_error(ORBQ_ERR_INVALID_ARG, "%s: causal_block or window negative", what);
   if (!std::isfinite(scale)) return set_error(ORBQ_ERR_INVALID_ARG, "%s: scale is not finite", what);

@@ -19,9 +19,9 @@ AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t k
   // 60).  Above 32 rows double tiles win (64 rows over 60000 tokens: 53 against 55, heads of 64 31 against 35) and
   // beat the many-row form up to 64 rows (82); with heads of 256 a double tile's registers spill, and the many-row
   // form takes over at 33 rows.
-  const int64_t cached = 2 * max_len * batch * kv_heads * d;
+  const double cached = 2.0 * max_len * batch * kv_heads * d;
   p.many = rows > (d == 256 ? 32 : 64);
-  p.rt = d < 256 && (rows > 32 || (rows > 16 && cached > (int64_t{128} << 20))) ? 2 : 1;
+  p.rt = d < 256 && (rows > 32 || (rows > 16 && cached > 0x1p27)) ? 2 : 1;
   const int tile_rows = p.many ? many_rows(d) : 16 * p.rt;
   p.row_tiles = static_cast<int32_t>((rows + tile_rows - 1) / tile_rows);
   // the keys that one row tile can see, in 64-key tiles

@@ -135,7 +135,7 @@ def test_attention():
                      (dict(dtype=0), UNSUPPORTED), (dict(dtype=5), ARG), (dict(q=None), ARG), (dict(o=None), ARG),
                      (dict(q=P + 8), ALIGN), (dict(qh=132), ALIGN), (dict(o=P + 4), ALIGN), (dict(ot=510), ALIGN),
                      (dict(ot=64), ARG), (dict(oh=64), ARG), (dict(lse=P + 2), ALIGN), (dict(cu=None, total=5), ARG),
-                     (dict(t=long), WORKSPACE), (dict(t=long, ws=P, ws_bytes=100), WORKSPACE),
+                     (dict(most=1 << 30, heads=256), UNSUPPORTED), (dict(t=long), WORKSPACE), (dict(t=long, ws=P, ws_bytes=100), WORKSPACE),
                      (dict(t=long, ws=P + 16, ws_bytes=1 << 40), ALIGN),
                      (dict(total=0, q=None, o=None, lens=None), OK), (dict(most=0, q=None), OK)):
         assert attend(**kw) == want, (kw, orbq.load().orbq_last_error())
