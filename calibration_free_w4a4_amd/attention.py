@@ -253,6 +253,8 @@ def kv_attention(cache: KVCache, q, table, lens, cu=None, max_new=None, causal_b
         need = _workspace(cache.kv_heads, d, dev, batch, n, max_new, h, max_len, causal_block, window)
         if need:
             workspace = q.new_empty((need + 1) // 2)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise _bad(func, f"workspace must be contiguous on cuda:{dev}")
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = lib.orbq_kv_attention(cache.packed, t, lens, cu, n, max_new, max_len, qp, qt, qh, h, out.data_ptr(), ot, oh,
                                0 if lse is None else lse.data_ptr(), code, d ** -0.5 if scale is None else scale, causal_block,

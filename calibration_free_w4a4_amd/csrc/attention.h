@@ -32,6 +32,7 @@ int launch_rope(const RopeArgs& a, int dtype, hipStream_t stream);
 
 // ------------------------------------------------------------------------------------ the cache
 constexpr float kScaleFloor = 0x1p-64f;  // the least scale of a block
+constexpr float kScaleMost = 0x1p+126f;  // and the largest that attention takes (its reciprocal is a normal number)
 constexpr float kScaleGrow = 1.25f;      // a scale that has to grow grows at least by this factor
 
 struct KvCache {

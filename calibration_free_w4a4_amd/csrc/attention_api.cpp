@@ -52,7 +52,7 @@ int check_cache(const orbq_kv_cache* c, const orbq_page_table* t, orbq::KvCache*
 
 // pointers that a call with work to do dereferences
 int check_cache_buffers(const orbq::KvCache& c, const char* what) {
-  if (!c.k || !c.v || !c.ks || !c.vs || !c.table) return set_error(ORBQ_ERR_INVALID_ARG, "%s: NULL cache buffer or page table", what);
+  if (!c.k || !c.v || !c.ks || !c.vs || (!c.table && c.max_pages)) return set_error(ORBQ_ERR_INVALID_ARG, "%s: NULL cache buffer or page table", what);
   if (!aligned(c.k, 16) || !aligned(c.v, 16)) return set_error(ORBQ_ERR_ALIGNMENT, "%s: codes must be 16-byte aligned", what);
   if (!aligned(c.ks, 4) || !aligned(c.vs, 4) || !aligned(c.table, 4))
     return set_error(ORBQ_ERR_ALIGNMENT, "%s: scales and page table must be 4-byte aligned", what);

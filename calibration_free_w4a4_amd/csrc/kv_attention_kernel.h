@@ -13,6 +13,10 @@
 // so no element is multiplied by a scale and the rounding of w to f16 is relative to the row's largest
 // weight whatever the scales are.  m, l and O are fp32.  m may lag behind the true maximum by up
 // to 2^kSlack (w stays below the f16 limit), which saves most of the rescaling of O.
+// The exponent is one fused operation on the raw score and log2(vs_j) - m, both rounded apart: a relative error of
+// 2^-24 of the score each, which the row's sum shares.  With scores to 2^25 it adds 4 to the 8 of kSlack at most, and
+// w stays within f16 (2^16); subtracting rounded scores instead would need no such limit and one more
+// instruction for each weight.
 //
 // The products are taken transposed: S^T = K Q^T has one query row a lane and its keys down the
 // accumulator registers, which is, up to an order of the keys that the values follow, the layout in
@@ -140,9 +144,10 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
 }
 
 // one value a lane that covers a block's keys: c = ks |scale| log2(e), log2(vs), 1/vs; a block that is absent
-// has no weight
+// has no weight.  The value scale is kept finite: a block before the window may hold anything, and an infinite
+// logarithm would turn the -infinity of its masked scores into a NaN.
 __device__ __forceinline__ void block_scales(const AttnArgs& a, float ks, float vs, bool have, float* c, float* lv, float* iv) {
-  const float v = __builtin_fmaxf(vs, kScaleFloor);
+  const float v = __builtin_fminf(__builtin_fmaxf(vs, kScaleFloor), kScaleMost);
   *c = have ? ks * a.scale_log2e : 0.0f;
   *lv = have ? __builtin_amdgcn_logf(v) : -__builtin_inff();  // log2, exact to a unit of its last place for a normal number
   *iv = have ? __builtin_amdgcn_rcpf(v) : 0.0f;

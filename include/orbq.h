@@ -336,7 +336,8 @@ typedef struct {
 } orbq_kv_cache;
 
 /* table [device] int32[batch][ld]: page of tokens i * page_tokens .. of each sequence, i < max_pages <= ld.
- * max_pages * page_tokens at most 2^30, batch at most 65535.  Sequences may share pages that are only
+ * max_pages * page_tokens at most 2^30, batch at most 65535; without pages (max_pages 0: nothing is held) table
+ * may be NULL.  Sequences may share pages that are only
  * read; a page that orbq_kv_append writes belongs to one sequence. */
 typedef struct {
   const int32_t* table;
@@ -376,6 +377,7 @@ int orbq_kv_read(const orbq_kv_cache* cache, const orbq_page_table* table, const
  *   q, o  [device] head tensors of `total` packed rows and `heads` heads, bf16 or f16; heads a multiple of
  *         kv_heads, query head h reads cache head h / (heads / kv_heads).  q 16-byte, o 8-byte addresses
  *         and strides.  Products on the codes in f16 with fp32 accumulation, softmax in fp32.
+ *         Scores scale q . k are taken up to 2^25 in magnitude; a row with larger ones may be not finite.
  *   lse   [device] float[total][heads] or NULL: natural log of the sum of exponentials
  *   max_new  bound of the queries of a sequence;  max_len  expected bound of lens (0: the page table's);
  *         it only chooses how the work is done, any value gives the same result up to rounding

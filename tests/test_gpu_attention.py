@@ -541,3 +541,81 @@ def test_many_rows_with_tiles_turned_before_or_on_the_way(orbq, d, heads, kv_hea
         len(lens) * kv_heads * 64 * 4 * d                       # the f16 tiles are there
     o2 = orbq.kv_attention(c, q, ints(table), ints(lens), max_len=max(lens) // 2, **args)
     assert (o2.float() - o.float()).abs().max().item() <= 2.0 ** -7 * o.float().abs().max().item()
+
+
+@pytest.mark.parametrize("d,heads,kv_heads,lens,new,window,turned", [
+    (64, 8, 2, [777], [1], 35, False), (128, 4, 4, [777], [1], 35, False), (256, 4, 2, [777], [1], 35, False),
+    (128, 48, 4, [900], [3], 35, False), (64, 4, 2, [900], [90], 90, False), (128, 4, 2, [900], [90], 90, False),
+    (256, 4, 2, [900], [90], 90, False), (128, 2, 2, [4600], [2100], 1900, True), (256, 1, 1, [2600], [1500], 1000, True)])
+def test_blocks_before_the_window_may_hold_anything(orbq, d, heads, kv_heads, lens, new, window, turned):
+    """Pages that no query of the call sees, in the tile where the first window begins among them, hold scales that are
+    no numbers."""
+    torch = torch_mod()
+    log(f"before the window d={d} new={new}")
+    page = 16
+    first = lens[0] - new[0] + 1 - window            # the first visible token
+    assert first > 16 and first % 64 >= 16           # and there is a block before it in its tile
+    c, q, table, o = run_attention(orbq, "bf16", d, page, heads, kv_heads, lens, new, block=1, window=window)
+    tiles = orbq.kv_attention_workspace_bytes(c, 1, new[0], new[0], heads, table.shape[1] * page, 1, window)
+    assert (tiles >= kv_heads * (window + new[0]) * 4 * d) == turned
+    hidden = torch.from_numpy(table[0, :first // page].astype(np.int64)).cuda()
+    for k, v in (("inf", "inf"), ("-inf", "nan"), ("nan", "-inf")):
+        c.k_scales[hidden] = float(k)
+        c.v_scales[hidden] = float(v)
+        assert torch.equal(orbq.kv_attention(c, q, ints(table), ints(lens), causal_block=1, window=window), o), (k, v)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 70])
+def test_scores_of_the_largest_magnitude(orbq, d, new):
+    """Scores down to -2^25: the largest takes all the weight, as with small ones."""
+    torch = torch_mod()
+    page, heads, n = 64, 2, 300
+    c = orbq.KVCache.create(8, heads, d, page)
+    rng = np.random.default_rng(d + new)
+    table = ints(np.arange(5)[None])
+    k = np.zeros((n, heads, d), np.float32)
+    k[:, :, 0] = -rng.uniform(90, 127, (n, 1))
+    v = rng.standard_normal((n, heads, d)).astype(np.float32)
+    orbq.kv_append(c, dev(k)[0], dev(v)[0], table, ints([0]))
+    rk, rv = orbq.kv_read(c, table, ints([0]), None, n, dtype=torch.float32)
+    q = torch.zeros((new, heads, d), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 2.0 ** 18                                    # times 127: just below 2^25
+    lse = torch.empty((new, heads), device="cuda")
+    o = orbq.kv_attention(c, q, table, ints([n]), lse=lse, scale=1.0)
+    for h in range(heads):
+        top = rk[:, h, 0].max()
+        assert bool((rk[rk[:, h, 0] != top, h, 0] < top * 1.00001).all())   # the next is far behind
+        mean = rv[rk[:, h, 0] == top, h].double().mean(0)     # equal keys share the weight
+        err = (o[:, h].double() - mean).abs()
+        assert bool((err <= 2.0 ** -8 * mean.abs() + 2.0 ** -10 * rv.abs().max()).all())
+        want = top.double() * 2.0 ** 18
+        assert -2.0 ** 25 < rk[:, h, 0].min().item() * 2.0 ** 18 < -2.0 ** 24.9 and bool(((lse[:, h].double() - want) / want).abs().max() <= 1e-6)
+
+
+def test_a_table_without_pages(orbq):
+    """Nothing is held: appending writes nothing, reading gives zeros, attention sees nothing."""
+    torch = torch_mod()
+    c = orbq.KVCache.create(2, 2, 64, 16)
+    for t in (c.k_codes, c.v_codes, c.k_scales, c.v_scales):
+        t.fill_(3)
+    table = torch.empty((2, 0), dtype=torch.int32, device="cuda")
+    for each in (1, 70):
+        x = torch.ones((2 * each, 2, 64), dtype=torch.bfloat16, device="cuda")
+        orbq.kv_append(c, x, x, table, ints([0, 5]))
+        assert all(bool((t == 3).all()) for t in (c.k_codes, c.v_codes, c.k_scales, c.v_scales))
+        k, v = orbq.kv_read(c, table, ints([0, 5]), None, 2 * each)
+        assert not k.any() and not v.any()
+        lse = torch.zeros((2 * each, 2), device="cuda")
+        assert not orbq.kv_attention(c, x, table, ints([0, 9]), lse=lse).any()
+        assert bool(torch.isneginf(lse).all())
+
+
+def test_a_workspace_elsewhere_is_refused(orbq):
+    torch = torch_mod()
+    c = orbq.KVCache.create(600, 1, 64, 128)
+    q = torch.zeros((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(orbq.OrbqError) as e:
+            orbq.kv_attention(c, q, ints(np.arange(600)[None]), ints([0]), workspace=ws)
+        assert e.value.status == -1
