@@ -52,16 +52,20 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// the larger one, or a NaN where either is: one instruction takes two of them, and unlike fmax it needs none that
+// quiet its operands first
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // x of this lane and of the lane 32 (16) away, combined: one vector instruction, where a shuffle would go through LDS
 __device__ __forceinline__ float max_over32(float x) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x);
   const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return __builtin_fmaxf(__builtin_bit_cast(float, static_cast<uint32_t>(r[0])), __builtin_bit_cast(float, static_cast<uint32_t>(r[1])));
+  return larger(__builtin_bit_cast(float, static_cast<uint32_t>(r[0])), __builtin_bit_cast(float, static_cast<uint32_t>(r[1])));
 }
 __device__ __forceinline__ float max_over16(float x) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x);
   const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  return __builtin_fmaxf(__builtin_bit_cast(float, static_cast<uint32_t>(r[0])), __builtin_bit_cast(float, static_cast<uint32_t>(r[1])));
+  return larger(__builtin_bit_cast(float, static_cast<uint32_t>(r[0])), __builtin_bit_cast(float, static_cast<uint32_t>(r[1])));
 }
 
 // four signed codes -> f16: byte u = code + 128 behind 0x64 is 1024 + u, less 1152 is the code
@@ -414,6 +418,7 @@ template <int D, bool TURNED = false> struct Many {
   // pieces spreads them over banks.
   static constexpr int kKPitch = TURNED ? 64 : 65, kVPitch = TURNED ? D : D + 2;
   static constexpr int kKPieces = D / 8 * kKPitch, kVPieces = 8 * kVPitch;
+  static constexpr int kFactors = TURNED ? 16 : 4;  // 16 bytes each; four are used, the rest is a wave's fetch
   static constexpr int kLoads = 4 * D / kThreads;  // 16-byte loads a thread for a tile's keys, and for its values
 };
 
@@ -436,7 +441,7 @@ template <int D, bool TURNED = false> struct ManyRows {
   const AttnArgs& a;
   half8_t (*lk)[M::kKPieces];   // [2]: tile t in t & 1
   half8_t (*lv)[M::kVPieces];   // [2]
-  f32x4_t (*lsc)[4];            // [4]: tile t in t & 3; for each 16 keys ks |scale| log2(e), log2(vs), 1 / vs
+  f32x4_t (*lsc)[M::kFactors];  // [4]: tile t in t & 3; for each 16 keys ks |scale| log2(e), log2(vs), 1 / vs
   int tid, wave, lane, l31, hi32;
   int b, kvh, split, h;
   Seq s;
@@ -461,7 +466,7 @@ template <int D, bool TURNED = false> struct ManyRows {
   const half8_t* turned;
   const f32x4_t* factors;
 
-  __device__ __forceinline__ ManyRows(const AttnArgs& args, half8_t (*k)[M::kKPieces], half8_t (*v)[M::kVPieces], f32x4_t (*sc4)[4])
+  __device__ __forceinline__ ManyRows(const AttnArgs& args, half8_t (*k)[M::kKPieces], half8_t (*v)[M::kVPieces], f32x4_t (*sc4)[M::kFactors])
       : a(args), lk(k), lv(v), lsc(sc4) {}
 
   // false: this workgroup has no rows
@@ -624,7 +629,17 @@ template <int D, bool TURNED = false> struct ManyRows {
                    : "memory", "m0");
     }
   }
-  __device__ __forceinline__ void fetch_k(int t) const { fetch(turned + static_cast<int64_t>(t) * (16 * D), lk[t & 1]); }
+  // keys, and the tile's factors: 16 words (the other lanes fetch them again, into the room behind)
+  __device__ __forceinline__ void fetch_k(int t) const {
+    fetch(turned + static_cast<int64_t>(t) * (16 * D), lk[t & 1]);
+    if (wave == 0) {
+      const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) f32x4_t*)(lsc[t & 3])));
+      asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(
+                       reinterpret_cast<const float*>(factors + 4 * t) + (lane & 15)),
+                   "s"(__builtin_amdgcn_readfirstlane(at))
+                   : "memory", "m0");
+    }
+  }
   __device__ __forceinline__ void fetch_v(int t) const { fetch(turned + static_cast<int64_t>(t) * (16 * D) + 8 * D, lv[t & 1]); }
   __device__ __forceinline__ void arrived() const { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
@@ -665,14 +680,14 @@ template <int D, bool TURNED = false> struct ManyRows {
     float top = -__builtin_inff();
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const f32x4_t x4 = TURNED ? factors[4 * t + g] : lsc[t & 3][g];
+      const f32x4_t x4 = lsc[t & 3][g];
       f->c[g] = factor(x4[0]);
       f->lv[g] = x4[1];
       f->iv[g] = x4[2];
       float x = st[g >> 1][8 * (g & 1)];
 #pragma unroll
-      for (int j = 1; j < 8; ++j) x = __builtin_fmaxf(x, st[g >> 1][8 * (g & 1) + j]);
-      top = __builtin_fmaxf(top, __builtin_fmaf(x, f->c[g], f->lv[g]));
+      for (int j = 1; j < 8; ++j) x = larger(x, st[g >> 1][8 * (g & 1) + j]);
+      top = larger(top, __builtin_fmaf(x, f->c[g], f->lv[g]));
     }
     return max_over32(top);
   }
@@ -884,7 +899,8 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 1) void k_wide(
 template <int D> __global__ __launch_bounds__(Many<D>::kThreads, D <= 128 ? 2 : 1) void k_turned(const AttnArgs a, int streams) {
   using M = Many<D, true>;
   __shared__ __attribute__((aligned(16))) half8_t lk[2][M::kKPieces], lv[2][M::kVPieces];
-  ManyRows<D, true> r(a, lk, lv, nullptr);
+  __shared__ __attribute__((aligned(16))) f32x4_t lsc[4][M::kFactors];
+  ManyRows<D, true> r(a, lk, lv, lsc);
   if (!r.begin(streams)) return;
   f32x16_t st[2][2];
   Factors fa[2];
