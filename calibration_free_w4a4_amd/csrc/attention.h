@@ -77,8 +77,9 @@ struct AttnArgs {
   int32_t causal_block, window;
   // the launch
   int32_t row_tiles, splits, chunk;  // chunk: 64-key tiles of a split
-  float* part_o;                     // [total * heads][splits][d], splits > 1
-  float* part_ml;                    // [total * heads][splits][2]
+  int32_t whole;                     // many: the first row tiles in turn, which are not split
+  float* part_o;                     // [rows][splits][d], splits > 1; rows as AttnPlan::part_rows counts them
+  float* part_ml;                    // [rows][splits][2]
   void* turned;                      // AttnPlan::turned: f16 tiles [batch][cache heads][turned_tiles][16 d][8]
   void* factors;                     // and their factors [batch][cache heads][turned_tiles][4][4] fp32
   int32_t turned_tiles;
@@ -92,11 +93,13 @@ struct AttnPlan {
   int32_t rt;      // few: 16-row tiles a workgroup
   int32_t waves;   // few: waves a workgroup
   int32_t row_tiles, splits, chunk;
+  int32_t whole;   // many: this many row tiles of all streams, in the order of the launch, are not split
+  int64_t part_rows;  // rows with parts.  many: those of the split row tiles in turn; few: all, [total][heads]
   int32_t turned;  // many: the tiles a stream's keys are turned into f16 before (0: on the way into LDS)
 };
 
 // bound: no sequence can be longer than max_len
-AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t kv_heads, int32_t d, int64_t max_len,
+AttnPlan plan_attention(int32_t batch, int64_t total, int32_t max_new, int32_t heads, int32_t kv_heads, int32_t d, int64_t max_len,
                         int32_t causal_block, int32_t window, bool bound, int cus);
 int launch_kv_attention(AttnArgs a, const AttnPlan& p, hipStream_t stream);
 

@@ -116,8 +116,8 @@ size_t turned_bytes(const orbq::AttnPlan& p, int32_t batch, int32_t kv_heads, in
 size_t factor_bytes(const orbq::AttnPlan& p, int32_t batch, int32_t kv_heads) {
   return static_cast<size_t>(batch) * kv_heads * p.turned * 64;
 }
-size_t part_bytes(const orbq::AttnPlan& p, int64_t rows, int32_t d) {
-  return p.splits > 1 ? static_cast<size_t>(rows) * p.splits * (d + 2) * sizeof(float) : 0;
+size_t part_bytes(const orbq::AttnPlan& p, int32_t d) {
+  return p.splits > 1 ? static_cast<size_t>(p.part_rows) * p.splits * (d + 2) * sizeof(float) : 0;
 }
 
 }  // namespace
@@ -199,10 +199,10 @@ ORBQ_API size_t orbq_kv_attention_workspace_bytes(const orbq_kv_cache* cache, in
       max_len < 0 || max_len > kMaxTokens || causal_block < 0 || window < 0 ||
       static_cast<int64_t>(max_new) * (heads / cache->kv_heads) > kMaxRows)
     return 0;
-  const orbq::AttnPlan p = orbq::plan_attention(batch, max_new, heads, cache->kv_heads, cache->head_dim, max_len, causal_block,
+  const orbq::AttnPlan p = orbq::plan_attention(batch, total, max_new, heads, cache->kv_heads, cache->head_dim, max_len, causal_block,
                                                 window, true, orbq::device_cus());
   return turned_bytes(p, batch, cache->kv_heads, cache->head_dim) + factor_bytes(p, batch, cache->kv_heads) +
-         part_bytes(p, total * heads, cache->head_dim);
+         part_bytes(p, cache->head_dim);
 }
 
 ORBQ_API int orbq_kv_attention(const orbq_kv_cache* cache, const orbq_page_table* table, const int32_t* lens,
@@ -234,21 +234,21 @@ ORBQ_API int orbq_kv_attention(const orbq_kv_cache* cache, const orbq_page_table
   const int64_t most = static_cast<int64_t>(a.c.max_pages) * a.c.page;
   const int64_t len = max_len && max_len < most ? max_len : most;
   // tiles are turned into the workspace only where it is known how many there can be
-  const orbq::AttnPlan p = orbq::plan_attention(a.c.batch, max_new, heads, a.c.heads, a.c.d, len, causal_block, window,
+  const orbq::AttnPlan p = orbq::plan_attention(a.c.batch, total, max_new, heads, a.c.heads, a.c.d, len, causal_block, window,
                                                 len == most, orbq::device_cus());
   const size_t turned = turned_bytes(p, a.c.batch, a.c.heads, a.c.d), factors = factor_bytes(p, a.c.batch, a.c.heads);
-  const size_t need = turned + factors + part_bytes(p, total * heads, a.c.d);
+  const size_t need = turned + factors + part_bytes(p, a.c.d);
   if (need) {
     if (!workspace || ws_bytes < need)
       return set_error(ORBQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, workspace ? ws_bytes : 0, need);
     if (!aligned(workspace, 256)) return set_error(ORBQ_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", what);
-    if (p.splits > 1 && total * heads > 0x7fffffff)
+    if (p.splits > 1 && (p.part_rows > 0x7fffffff || static_cast<int64_t>(a.c.batch) * max_new * heads > 0x7fffffff))
       return set_error(ORBQ_ERR_UNSUPPORTED, "%s: more than 2^31 rows over split keys", what);
     a.turned = workspace;
     a.factors = static_cast<char*>(workspace) + turned;
     a.turned_tiles = p.turned;
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + turned + factors);
-    a.part_ml = a.part_o + total * heads * p.splits * a.c.d;
+    a.part_ml = a.part_o + p.part_rows * p.splits * a.c.d;
   }
   a.page_shift = __builtin_ctz(a.c.page);
   a.lens = lens;

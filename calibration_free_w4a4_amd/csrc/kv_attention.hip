@@ -9,7 +9,7 @@ template <> int launch_attn<64>(const AttnArgs&, const AttnPlan&, hipStream_t);
 template <> int launch_attn<128>(const AttnArgs&, const AttnPlan&, hipStream_t);
 template <> int launch_attn<256>(const AttnArgs&, const AttnPlan&, hipStream_t);
 
-AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t kv_heads, int32_t d, int64_t max_len,
+AttnPlan plan_attention(int32_t batch, int64_t total, int32_t max_new, int32_t heads, int32_t kv_heads, int32_t d, int64_t max_len,
                         int32_t causal_block, int32_t window, bool bound, int cus) {
   AttnPlan p{};
   const int64_t rows = static_cast<int64_t>(max_new) * (heads / kv_heads);
@@ -29,22 +29,36 @@ AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t k
   if (window) span = std::min<int64_t>(span, static_cast<int64_t>(window) + max_new + causal_block);
   const int64_t tiles = std::max<int64_t>(1, (span + 63) / 64 + (window ? 1 : 0));
   const int64_t groups = static_cast<int64_t>(batch) * kv_heads * p.row_tiles;
-  int64_t splits = 1;
+  int64_t splits = 1, whole = groups, part_tiles = tiles;
   p.waves = 4;
   if (p.many) {
-    // Workgroups resident at once: one a CU (LDS and registers), three with heads of 64.  In tiles of one
+    // Workgroups resident at once: one a CU (LDS and registers), three with heads of 64.  Row tiles that fill whole
+    // rounds are not split, those of the last round are, so that it is full too (2 x 4605 queries of 8 heads of 256,
+    // 576 row tiles: all in three parts 528 us, the last 64 in four 435).  Sequences of unequal rows leave row
+    // tiles empty, so rounds are not told apart there (ragged prompts: 82 us without, 93 with).  In tiles of one
     // workgroup: the rounds of splits, the joining launch (3) and the parts' way through memory, which takes a
     // full card about as long as 400 keys of the same rows.
     const int64_t want = static_cast<int64_t>(cus) * (d == 64 ? 3 : 1);
-    const auto cost = [&](int64_t n) {
-      return static_cast<double>((groups * n + want - 1) / want * ((tiles + n - 1) / n)) +
-             (n > 1 ? 3.0 + 400.0 / 64 * n * groups / want : 0.0);
-    };
+    const int64_t full = total == static_cast<int64_t>(batch) * max_new ? groups / want * want : 0, rest = groups - full;
+    // the last round's row tiles are a sequence's first rows, which see less under a causal mask
+    if (full && causal_block) span = std::min(span, std::max<int64_t>(0, max_len - max_new) + max_new * rest / groups + causal_block);
+    part_tiles = std::min(tiles, (span + 63) / 64 + 1);
+    const int64_t before = full / want * tiles;
+    double least = static_cast<double>(before + (rest + want - 1) / want * part_tiles);
     const auto consider = [&](int64_t n) {
-      if (n > 1 && 2 * n <= tiles && cost(n) < cost(splits)) splits = n;
+      if (n < 2 || 2 * n > part_tiles) return;
+      const double cost = static_cast<double>(before + (rest * n + want - 1) / want * ((part_tiles + n - 1) / n)) + 3.0 +
+                          400.0 / 64 * n * rest / want;
+      if (cost < least) {
+        least = cost;
+        splits = n;
+        whole = full;
+      }
     };
-    for (int n = 2; n <= 16; ++n) consider(n);
-    for (int n = 1; n <= 3; ++n) consider(n * want / groups);
+    if (rest) {
+      for (int n = 2; n <= 16; ++n) consider(n);
+      for (int n = 1; n <= 3; ++n) consider(n * want / rest);
+    }
     // Turning the codes once a call instead of once a row tile pays where some eight row tiles read each of
     // them (4680 queries over 32760 tokens, 12 heads of 128: 1165 us without, 1005 with; 327 queries with a
     // window of 19: 28 without, 36 with); with heads of 64 staging is too small a share (82 without, 89 with).
@@ -62,8 +76,10 @@ AttnPlan plan_attention(int32_t batch, int32_t max_new, int32_t heads, int32_t k
     if (groups < 2 * want) splits = fit >= 4 ? fit : (2 * want + groups - 1) / groups;
     splits = std::min(splits, (tiles + 3) / 4);
   }
-  p.chunk = static_cast<int32_t>((tiles + splits - 1) / splits);
-  p.splits = static_cast<int32_t>((tiles + p.chunk - 1) / p.chunk);
+  p.chunk = static_cast<int32_t>((part_tiles + splits - 1) / splits);
+  p.splits = static_cast<int32_t>((part_tiles + p.chunk - 1) / p.chunk);
+  p.whole = static_cast<int32_t>(std::min<int64_t>(whole, 0x7fffffff));
+  p.part_rows = p.many ? (groups - whole) * tile_rows : total * heads;
   return p;
 }
 
@@ -71,6 +87,7 @@ int launch_kv_attention(AttnArgs a, const AttnPlan& p, hipStream_t stream) {
   a.row_tiles = p.row_tiles;
   a.splits = p.splits;
   a.chunk = p.chunk;
+  a.whole = p.whole;
   switch (a.c.d) {
     case 64: return launch_attn<64>(a, p, stream);
     case 128: return launch_attn<128>(a, p, stream);

@@ -433,6 +433,14 @@ __device__ __forceinline__ int first_of(const AttnArgs& a, const Seq& s) {
   return lo / 64;
 }
 
+// the n-th row tile in the order of the launch
+__device__ __forceinline__ int tile_of(const AttnArgs& a, int n, int* b, int* kvh) {
+  const int streams = a.c.batch * a.c.heads, turn = n / streams, stream = n - turn * streams;
+  *b = stream / a.c.heads;
+  *kvh = stream - *b * a.c.heads;
+  return a.row_tiles - 1 - turn;
+}
+
 // One workgroup's rows, its part of the keys, and one wave's 32 rows of them: lane l31 of either half
 // holds row l31.  Everything here is inlined; the members live in registers.
 template <int D, bool TURNED = false> struct ManyRows {
@@ -443,10 +451,10 @@ template <int D, bool TURNED = false> struct ManyRows {
   half8_t (*lv)[M::kVPieces];   // [2]
   f32x4_t (*lsc)[M::kFactors];  // [4]: tile t in t & 3; for each 16 keys ks |scale| log2(e), log2(vs), 1 / vs
   int tid, wave, lane, l31, hi32;
-  int b, kvh, split, h;
+  int b, kvh, parts, split, h;  // parts that this row tile's keys are split into
   Seq s;
   bool live;
-  int64_t tok, row;
+  int64_t tok, row, part_row;
   int t0, t1;                   // 64-key tiles of this workgroup
   int32_t lo, hi;               // this lane's visible keys
   int32_t all_lo, all_hi;       // keys from all_lo to all_hi are visible to all rows of this wave
@@ -470,22 +478,25 @@ template <int D, bool TURNED = false> struct ManyRows {
       : a(args), lk(k), lv(v), lsc(sc4) {}
 
   // false: this workgroup has no rows
-  __device__ __forceinline__ bool begin(int streams) {
+  __device__ __forceinline__ bool begin() {
     tid = threadIdx.x;
     wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     lane = tid & 63;
     l31 = tid & 31;
     hi32 = (tid >> 5) & 1;
-    // Row tiles of all streams (sequence, head, split) in turn, the last rows, which see most under a causal mask,
-    // first.  Keeping a stream on one die instead leaves the dies unevenly loaded where sequences
+    // Row tiles of all streams (sequence, head) in turn, the last rows, which see most under a causal mask, first;
+    // from a.whole on each in a.splits parts.  Keeping a stream on one die instead leaves the dies unevenly loaded where sequences
     // differ (the ragged prompts: 142 us, 82 in this order) and gains nothing where they do not.
-    const int n = blockIdx.x;
-    int tile = n / streams;
-    const int stream = n - tile * streams;
-    tile = a.row_tiles - 1 - tile;
-    split = stream % a.splits;
-    kvh = stream / a.splits % a.c.heads;
-    b = stream / a.splits / a.c.heads;
+    int n = blockIdx.x;
+    parts = 1;
+    split = 0;
+    if (n >= a.whole) {
+      parts = a.splits;
+      split = (n - a.whole) % parts;
+      n = a.whole + (n - a.whole) / parts;
+    }
+    part_row = static_cast<int64_t>(n - a.whole) * M::kRows;
+    const int tile = tile_of(a, n, &b, &kvh);
     s = seq_of(a, b);
     const int64_t all = static_cast<int64_t>(s.rows) * a.group, r0 = static_cast<int64_t>(tile) * M::kRows;
     if (r0 >= all) return false;
@@ -496,8 +507,9 @@ template <int D, bool TURNED = false> struct ManyRows {
     visible(a, base + (r1 - 1) / a.group, s.len, &x, &last);
     const int t_end = (last + 63) / 64;
     t0 = first / 64 + split * a.chunk;
-    t1 = split + 1 < a.splits && t0 + a.chunk < t_end ? t0 + a.chunk : t_end;
+    t1 = split + 1 < parts && t0 + a.chunk < t_end ? t0 + a.chunk : t_end;
     const int64_t mine = r0 + 32 * wave + l31;
+    part_row += 32 * wave + l31;
     live = mine < r1;
     const int64_t rr = live ? mine : r0;
     tok = rr / a.group;
@@ -719,8 +731,8 @@ template <int D, bool TURNED = false> struct ManyRows {
     l += __shfl_xor(l, 32);
     if (!live) return;
     // register 4 k + j of o[i]: entry 32 i + 8 k + 4 hi32 + j
-    if (a.splits > 1) {
-      float* po = a.part_o + (row * a.splits + split) * D;
+    if (parts > 1) {
+      float* po = a.part_o + (part_row * parts + split) * D;
       if (l != 0.0f) {
 #pragma unroll
         for (int i = 0; i < ND; ++i)
@@ -730,7 +742,7 @@ template <int D, bool TURNED = false> struct ManyRows {
                 f32x4_t{o[i][4 * k], o[i][4 * k + 1], o[i][4 * k + 2], o[i][4 * k + 3]};
       }
       if (hi32 == 0) {
-        float* ml = a.part_ml + (row * a.splits + split) * 2;
+        float* ml = a.part_ml + (part_row * parts + split) * 2;
         ml[0] = m;
         ml[1] = l;
       }
@@ -748,12 +760,12 @@ template <int D, bool TURNED = false> struct ManyRows {
   }
 };
 
-template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 2) void k_many(const AttnArgs a, int streams) {
+template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 2) void k_many(const AttnArgs a) {
   using M = Many<D>;
   __shared__ __attribute__((aligned(16))) half8_t lk[2][M::kKPieces], lv[2][M::kVPieces];
   __shared__ __attribute__((aligned(16))) f32x4_t lsc[4][4];
   ManyRows<D> r(a, lk, lv, lsc);
-  if (!r.begin(streams)) return;
+  if (!r.begin()) return;
   if (r.t0 < r.t1) {
     r.pages_k(r.t0);
     r.pages_v(r.t0);
@@ -841,12 +853,12 @@ template <int D> __global__ __launch_bounds__(256) void k_turn(const AttnArgs a)
 // queries: 925 us without, 800 with; heads of 128, two waves a SIMD: 1157 us without, 1188 with).  Step t takes
 // the weights of tile t beside the scores of tile t + 1 on the matrix cores, and finds the maximum of tile t + 1
 // and stages what comes next beside the values of tile t.
-template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 1) void k_wide(const AttnArgs a, int streams) {
+template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 1) void k_wide(const AttnArgs a) {
   using M = Many<D>;
   __shared__ __attribute__((aligned(16))) half8_t lk[2][M::kKPieces], lv[2][M::kVPieces];
   __shared__ __attribute__((aligned(16))) f32x4_t lsc[4][4];
   ManyRows<D> r(a, lk, lv, lsc);
-  if (!r.begin(streams)) return;
+  if (!r.begin()) return;
   f32x16_t st[2][2];
   Factors fa[2];
   if (r.t0 < r.t1) {
@@ -896,12 +908,12 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, 1) void k_wide(
   r.finish();
 }
 
-template <int D> __global__ __launch_bounds__(Many<D>::kThreads, D <= 128 ? 2 : 1) void k_turned(const AttnArgs a, int streams) {
+template <int D> __global__ __launch_bounds__(Many<D>::kThreads, D <= 128 ? 2 : 1) void k_turned(const AttnArgs a) {
   using M = Many<D, true>;
   __shared__ __attribute__((aligned(16))) half8_t lk[2][M::kKPieces], lv[2][M::kVPieces];
   __shared__ __attribute__((aligned(16))) f32x4_t lsc[4][M::kFactors];
   ManyRows<D, true> r(a, lk, lv, lsc);
-  if (!r.begin(streams)) return;
+  if (!r.begin()) return;
   f32x16_t st[2][2];
   Factors fa[2];
   if (r.t0 < r.t1) {
@@ -940,15 +952,36 @@ template <int D> __global__ __launch_bounds__(Many<D>::kThreads, D <= 128 ? 2 : 
 
 // ----------------------------------------------------------------------------------------- join
 // D / 4 threads a part.  Many parts of a row are dealt to the 1024 / D teams of a workgroup; with few, each
-// team takes a row (FEW).
-template <int D, bool FEW> __global__ __launch_bounds__(256) void k_join(const AttnArgs a) {
+// team takes a row (FEW).  `rows` rows: of the few-row form [batch][max_new][heads], of the many-row form those
+// of the split row tiles in turn.
+template <int D, bool FEW> __global__ __launch_bounds__(256) void k_join(const AttnArgs a, int64_t rows, int many) {
   constexpr int TEAM = D / 4, TEAMS = 256 / TEAM;
   __shared__ __attribute__((aligned(16))) f32x4_t lo[FEW ? 1 : TEAMS][TEAM];
   __shared__ float red[256];
   const int tid = threadIdx.x, team = tid / TEAM, e = tid % TEAM;
-  const int64_t row = FEW ? static_cast<int64_t>(blockIdx.x) * TEAMS + team : blockIdx.x;
-  if (FEW && row >= a.total * a.heads) return;
-  const float* ml = a.part_ml + row * a.splits * 2;
+  const int64_t at = FEW ? static_cast<int64_t>(blockIdx.x) * TEAMS + team : blockIdx.x;
+  if (at >= rows) return;
+  int64_t tok, part_row;
+  int h;
+  if (many) {
+    int b, kvh;
+    const int n = static_cast<int>(at / many_rows(D));
+    const int64_t r = static_cast<int64_t>(tile_of(a, a.whole + n, &b, &kvh)) * many_rows(D) + at % many_rows(D);
+    const Seq s = seq_of(a, b);
+    if (r >= static_cast<int64_t>(s.rows) * a.group) return;
+    tok = s.row0 + r / a.group;
+    h = kvh * a.group + static_cast<int>(r % a.group);
+    part_row = at;
+  } else {
+    const int64_t query = at / a.heads;
+    h = static_cast<int>(at - query * a.heads);
+    const int b = static_cast<int>(query / a.max_new), i = static_cast<int>(query - static_cast<int64_t>(b) * a.max_new);
+    const Seq s = seq_of(a, b);
+    if (i >= s.rows) return;
+    tok = s.row0 + i;
+    part_row = tok * a.heads + h;
+  }
+  const float* ml = a.part_ml + part_row * a.splits * 2;
   float m = kNone;
   if constexpr (FEW) {
     for (int i = 0; i < a.splits; ++i) m = ml[2 * i + 1] != 0.0f ? __builtin_fmaxf(m, ml[2 * i]) : m;
@@ -970,7 +1003,7 @@ template <int D, bool FEW> __global__ __launch_bounds__(256) void k_join(const A
     if (li == 0.0f) continue;  // nothing visible in that part: its values were not written
     const float by = exp2_fast(ml[2 * i] - m);
     l = __builtin_fmaf(li, by, l);
-    o += *reinterpret_cast<const f32x4_t*>(a.part_o + (row * a.splits + i) * D + 4 * e) * by;
+    o += *reinterpret_cast<const f32x4_t*>(a.part_o + (part_row * a.splits + i) * D + 4 * e) * by;
   }
   if constexpr (!FEW) {
     __syncthreads();
@@ -983,30 +1016,27 @@ template <int D, bool FEW> __global__ __launch_bounds__(256) void k_join(const A
       l += red[i * TEAM];
     }
   }
-  const int64_t tok = row / a.heads;
-  const int h = static_cast<int>(row - tok * a.heads);
   const float by = l == 0.0f ? 0.0f : 1.0f / l;
   store4(a, tok * a.ot + h * a.oh + 4 * e, o * by);
-  if (a.lse && e == 0) a.lse[row] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+  if (a.lse && e == 0) a.lse[tok * a.heads + h] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
 }
 
 }  // namespace attn
 
 template <int D> int launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   if (p.many) {
-    const int streams = a.c.batch * a.c.heads * a.splits;
-    const int64_t grid = static_cast<int64_t>(streams) * a.row_tiles;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    const int64_t tiles = static_cast<int64_t>(a.c.batch) * a.c.heads * a.row_tiles, grid = a.whole + (tiles - a.whole) * a.splits;
+    if (tiles > 0x7fffffff || grid > 0x7fffffff) return hipErrorInvalidValue;
     const dim3 g(static_cast<uint32_t>(grid)), t(attn::Many<D>::kThreads);
     if constexpr (D > 64) {
       if (p.turned) {
         hipLaunchKernelGGL((attn::k_turn<D>), dim3(p.turned, a.c.heads, a.c.batch), dim3(256), 0, stream, a);
-        hipLaunchKernelGGL((attn::k_turned<D>), g, t, 0, stream, a, streams);
+        hipLaunchKernelGGL((attn::k_turned<D>), g, t, 0, stream, a);
       }
     }
     if (!p.turned) {
-      if constexpr (D <= 128) hipLaunchKernelGGL((attn::k_many<D>), g, t, 0, stream, a, streams);
-      else hipLaunchKernelGGL((attn::k_wide<D>), g, t, 0, stream, a, streams);
+      if constexpr (D <= 128) hipLaunchKernelGGL((attn::k_many<D>), g, t, 0, stream, a);
+      else hipLaunchKernelGGL((attn::k_wide<D>), g, t, 0, stream, a);
     }
   } else {
     const dim3 grid(a.splits, a.c.heads * a.row_tiles, a.c.batch);
@@ -1017,10 +1047,11 @@ template <int D> int launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream
     if (p.rt == 1 && p.waves == 4) hipLaunchKernelGGL((attn::k_few<D, 1, 4>), grid, dim3(256), 0, stream, a);
   }
   if (a.splits > 1) {
-    const int64_t rows = a.total * a.heads;
+    const int64_t rows = p.many ? p.part_rows : static_cast<int64_t>(a.c.batch) * a.max_new * a.heads;
     if (a.splits <= 8)
-      hipLaunchKernelGGL((attn::k_join<D, true>), dim3(static_cast<uint32_t>((rows + 1024 / D - 1) / (1024 / D))), dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((attn::k_join<D, false>), dim3(static_cast<uint32_t>(rows)), dim3(256), 0, stream, a);
+      hipLaunchKernelGGL((attn::k_join<D, true>), dim3(static_cast<uint32_t>((rows + 1024 / D - 1) / (1024 / D))), dim3(256), 0, stream, a,
+                         rows, p.many);
+    else hipLaunchKernelGGL((attn::k_join<D, false>), dim3(static_cast<uint32_t>(rows)), dim3(256), 0, stream, a, rows, p.many);
   }
   return static_cast<int>(hipGetLastError());
 }

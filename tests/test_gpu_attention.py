@@ -619,3 +619,30 @@ def test_a_workspace_elsewhere_is_refused(orbq):
         with pytest.raises(orbq.OrbqError) as e:
             orbq.kv_attention(c, q, ints(np.arange(600)[None]), ints([0]), workspace=ws)
         assert e.value.status == -1
+
+
+@pytest.mark.parametrize("d,heads,kv_heads,lens,new,block,window", [
+    (128, 53, 53, [1500, 3, 800, 0, 1333], 100, 0, 0), (128, 53, 53, [1500, 3, 800, 100, 1333], 100, 1, 0),
+    (256, 262, 131, [700], 100, 30, 0), (256, 262, 131, [700], 100, 0, 400), (64, 390, 390, [600, 511], 70, 1, 0)])
+def test_only_the_last_round_of_row_tiles_is_split(orbq, d, heads, kv_heads, lens, new, block, window):
+    """Some row tiles more than fill the card once: those alone are split and joined."""
+    log(f"last round d={d} heads {heads}/{kv_heads} {lens} {block} {window}")
+    c, q, table, o = run_attention(orbq, "bf16", d, 64, heads, kv_heads, lens, [new] * len(lens), block, window)
+    n = orbq.kv_attention_workspace_bytes(c, len(lens), len(lens) * new, new, heads, table.shape[1] * 64, block, window)
+    assert 0 < n < len(lens) * new * heads * 2 * (d + 2) * 4       # less than two parts of every row
+    assert torch_mod().equal(orbq.kv_attention(c, q, ints(table), ints(lens), causal_block=block, window=window), o)
+
+
+@pytest.mark.parametrize("d,most", [(64, 2), (128, 2), (256, 2), (128, 80)])
+def test_rows_beyond_the_bound_are_left_alone(orbq, d, most):
+    """Rows of a sequence past max_new, and rows of no sequence, are not written, split keys or not."""
+    torch = torch_mod()
+    rng = np.random.default_rng(d)
+    for n in (200, 30000):
+        pages = -(-n // 128)
+        c = cache_of(orbq, rng, pages, 2, d, 128)
+        q, _ = dev(rng.standard_normal((most + 9, 2, d)), "bf16")
+        out, lse = torch.full_like(q, 7.0), torch.full((most + 9, 2), 7.0, device="cuda")
+        orbq.kv_attention(c, q, ints(np.arange(pages)[None]), ints([n]), cu=ints([0, most + 5]), max_new=most, out=out, lse=lse)
+        assert bool((out[most:] == 7.0).all()) and bool((lse[most:] == 7.0).all())
+        assert bool((out[:most] != 7.0).any(-1).all()) and bool((lse[:most] != 7.0).all())
