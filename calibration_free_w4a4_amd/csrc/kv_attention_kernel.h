@@ -30,12 +30,13 @@
 //   many  128 or 256 rows a workgroup: bound by the matrix cores, the softmax's vector work and the LDS reads
 //         between them.  Codes are turned into f16 once a workgroup on their way into LDS, double
 //         buffered, or once a call by k_turn, and then fetched into LDS as they are.
-// Either splits the keys over workgroups where there are few rows; k_join joins the parts.
+// Either splits the keys over workgroups, few where there are few rows, many where the last round of workgroups
+// would leave CUs idle; k_join joins the parts.
 //
 // Measured: few, one token of 48 sequences to 16384 long, 32 / 8 heads of 128: 170 us, 5.0 TB/s of cache; 4 tokens
-// over 262157, 64 / 8 heads of 64: 52 us, 5.2 TB/s, and 5 us of joining.  many, 4680 queries over 32760 tokens, 12
-// heads of 128: 0.97 ms, 0.93 PFLOP/s (a library f16 product of 8192^3 on the same card: 1.20); heads of 256,
-// 2 x 4605 queries that all see all: 545 us, 0.64 PFLOP/s; heads of 64, ragged prompts with a window of 1024: 83 us,
+// over 262157, 64 / 8 heads of 64: 52 us, 5.2 TB/s, and 6 us of joining.  many, 4680 queries over 32760 tokens, 12
+// heads of 128: 0.96 ms, 0.94 PFLOP/s (a library f16 product of 8192^3 on the same card: 1.20); heads of 256,
+// 2 x 4605 queries that all see all: 437 us, 0.79 PFLOP/s; heads of 64, ragged prompts with a window of 1024: 83 us,
 // 0.43 PFLOP/s.
 #pragma once
 
@@ -485,8 +486,8 @@ template <int D, bool TURNED = false> struct ManyRows {
     l31 = tid & 31;
     hi32 = (tid >> 5) & 1;
     // Row tiles of all streams (sequence, head) in turn, the last rows, which see most under a causal mask, first;
-    // from a.whole on each in a.splits parts.  Keeping a stream on one die instead leaves the dies unevenly loaded where sequences
-    // differ (the ragged prompts: 142 us, 82 in this order) and gains nothing where they do not.
+    // from a.whole on each in a.splits parts.  Keeping a stream on one die instead leaves the dies unevenly loaded
+    // where sequences differ (the ragged prompts: 142 us, 82 in this order) and gains nothing where they do not.
     int n = blockIdx.x;
     parts = 1;
     split = 0;
@@ -641,7 +642,8 @@ template <int D, bool TURNED = false> struct ManyRows {
                    : "memory", "m0");
     }
   }
-  // keys, and the tile's factors: 16 words (the other lanes fetch them again, into the room behind)
+  // keys, and the tile's factors: 16 words (the other lanes fetch them again, into the room behind).  Loaded where they
+  // are used instead, each step would wait for them and for its fetches (frames of 12 heads of 128: 972 us, 958 so).
   __device__ __forceinline__ void fetch_k(int t) const {
     fetch(turned + static_cast<int64_t>(t) * (16 * D), lk[t & 1]);
     if (wave == 0) {
