@@ -44,9 +44,10 @@ template <int DT, int E> struct Vec {
   }
 };
 
-// The rows of sequence b in the packed arrays, kept inside [0, total) whatever cu holds.
+// The rows of sequence b in the packed arrays, kept inside [0, total) whatever cu holds: the first of them, how many a
+// call processes, and how many there are (total is at most 2^30).
 __device__ __forceinline__ void rows_of(const int32_t* cu, int64_t total, int32_t batch, int32_t max_rows, int32_t b,
-                                        int64_t* row0, int32_t* rows) {
+                                        int64_t* row0, int32_t* rows, int32_t* all) {
   int64_t r0, r1;
   if (cu) {
     r0 = cu[b];
@@ -59,7 +60,8 @@ __device__ __forceinline__ void rows_of(const int32_t* cu, int64_t total, int32_
     r1 = r0 + each;
   }
   *row0 = r0;
-  *rows = static_cast<int32_t>(r1 - r0 < max_rows ? r1 - r0 : max_rows);
+  *all = static_cast<int32_t>(r1 - r0);
+  *rows = *all < max_rows ? *all : max_rows;
 }
 
 // Page of block p of sequence b, or -1 where the table has none (entries outside the cache are

@@ -135,13 +135,14 @@ __device__ __forceinline__ void visible(const AttnArgs& a, int64_t pos, int32_t 
 
 struct Seq {
   int64_t row0;   // first packed query
-  int32_t rows;   // queries
+  int32_t rows;   // queries that are processed
+  int32_t all;    // queries, max_new or not: the first stands at len - all
   int32_t len;    // cached tokens, within the table
 };
 
 __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
   Seq s;
-  rows_of(a.cu, a.total, a.c.batch, a.max_new, b, &s.row0, &s.rows);
+  rows_of(a.cu, a.total, a.c.batch, a.max_new, b, &s.row0, &s.rows, &s.all);
   const int64_t most = static_cast<int64_t>(a.c.max_pages) << a.page_shift;
   const int32_t n = a.lens[b];
   s.len = n < 0 ? 0 : (n > most ? static_cast<int32_t>(most) : n);
@@ -178,8 +179,8 @@ template <int D, int RT, int NW> __global__ __launch_bounds__(64 * NW) void k_fe
 
   // the rows' keys
   int32_t lo[RT], hi[RT], lo_most, hi_least, first, last;
-  visible(a, static_cast<int64_t>(s.len) - s.rows + r0 / a.group, s.len, &first, &hi_least);
-  visible(a, static_cast<int64_t>(s.len) - s.rows + (r1 - 1) / a.group, s.len, &lo_most, &last);
+  visible(a, static_cast<int64_t>(s.len) - s.all + r0 / a.group, s.len, &first, &hi_least);
+  visible(a, static_cast<int64_t>(s.len) - s.all + (r1 - 1) / a.group, s.len, &lo_most, &last);
   const int t_first = first / 64, t_end = (last + 63) / 64;
   const int t0 = t_first + split * a.chunk;
   const int t1 = split + 1 < a.splits && t0 + a.chunk < t_end ? t0 + a.chunk : t_end;
@@ -254,7 +255,7 @@ template <int D, int RT, int NW> __global__ __launch_bounds__(64 * NW) void k_fe
     const bool live = r < r1;
     const int rr = live ? r : r0, tok = rr / a.group, h = kvh * a.group + rr - tok * a.group;
     const int64_t at = (s.row0 + tok) * a.qt + h * a.qh;
-    visible(a, static_cast<int64_t>(s.len) - s.rows + tok, s.len, &lo[rt], &hi[rt]);
+    visible(a, static_cast<int64_t>(s.len) - s.all + tok, s.len, &lo[rt], &hi[rt]);
     if (!live) hi[rt] = 0;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -430,7 +431,7 @@ struct Factors {  // of each 16 keys of a tile: on raw scores, log2 of the value
 // the first 64-key tile that a sequence's rows see
 __device__ __forceinline__ int first_of(const AttnArgs& a, const Seq& s) {
   int32_t lo, hi;
-  visible(a, static_cast<int64_t>(s.len) - s.rows, s.len, &lo, &hi);
+  visible(a, static_cast<int64_t>(s.len) - s.all, s.len, &lo, &hi);
   return lo / 64;
 }
 
@@ -502,7 +503,7 @@ template <int D, bool TURNED = false> struct ManyRows {
     const int64_t all = static_cast<int64_t>(s.rows) * a.group, r0 = static_cast<int64_t>(tile) * M::kRows;
     if (r0 >= all) return false;
     const int64_t r1 = r0 + M::kRows < all ? r0 + M::kRows : all;
-    const int64_t base = static_cast<int64_t>(s.len) - s.rows;
+    const int64_t base = static_cast<int64_t>(s.len) - s.all;
     int32_t first, last, x;
     visible(a, base + r0 / a.group, s.len, &first, &x);
     visible(a, base + (r1 - 1) / a.group, s.len, &x, &last);
@@ -810,7 +811,7 @@ template <int D> __global__ __launch_bounds__(256) void k_turn(const AttnArgs a)
   const Seq s = seq_of(a, b);
   if (s.rows == 0) return;
   int32_t last, x;
-  visible(a, static_cast<int64_t>(s.len) - 1, s.len, &x, &last);
+  visible(a, static_cast<int64_t>(s.len) - s.all + s.rows - 1, s.len, &x, &last);
   const int t = first_of(a, s) + blockIdx.x;  // as many workgroups as a stream has room for tiles
   if (t >= (last + 63) / 64) return;
   const int64_t tile = (static_cast<int64_t>(b) * a.c.heads + kvh) * a.turned_tiles + blockIdx.x;

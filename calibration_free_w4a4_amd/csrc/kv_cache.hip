@@ -133,8 +133,8 @@ __global__ __launch_bounds__(threads_for(D* PAGE)) void k_append(const KvCache c
   const int tid = threadIdx.x, head = blockIdx.y >> 1, b = blockIdx.z;
   const bool values = blockIdx.y & 1;
   int64_t row0;
-  int32_t rows;
-  rows_of(x.cu, x.total, c.batch, x.max_rows, b, &row0, &rows);
+  int32_t rows, all;
+  rows_of(x.cu, x.total, c.batch, x.max_rows, b, &row0, &rows, &all);
   const int64_t start = x.first[b];
   if (start < 0 || rows == 0) return;
   const int64_t p = start / PAGE + blockIdx.x;
@@ -268,8 +268,8 @@ __global__ __launch_bounds__(threads_for(D* PAGE)) void k_read(const KvCache c, 
   const int tid = threadIdx.x, head = blockIdx.y >> 1, b = blockIdx.z;
   const bool values = blockIdx.y & 1;
   int64_t row0;
-  int32_t rows;
-  rows_of(x.cu, x.total, c.batch, x.max_rows, b, &row0, &rows);
+  int32_t rows, all;
+  rows_of(x.cu, x.total, c.batch, x.max_rows, b, &row0, &rows, &all);
   const int64_t first = x.first[b];
   if (first < 0 || rows == 0) return;
   const int64_t p = first / PAGE + blockIdx.x;

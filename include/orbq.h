@@ -366,8 +366,9 @@ int orbq_kv_read(const orbq_kv_cache* cache, const orbq_page_table* table, const
                  int64_t v_head, orbq_dtype type, void* stream);
 
 /* Attention of packed queries over the cache: O = softmax(scale q K^T) V over each query's visible
- * tokens.  Query i of the n of sequence b stands at position lens[b] - n + i, so the cache holds
- * the queries' own tokens already (orbq_kv_append first).  Visible are tokens lo <= j < hi:
+ * tokens.  Query i of the n that cu gives sequence b (max_new may leave the last ones out, and changes no
+ * position) stands at position lens[b] - n + i, so the cache holds the queries' own tokens already
+ * (orbq_kv_append first).  Visible are tokens lo <= j < hi:
  *   hi = lens[b] with causal_block = 0; else min(lens[b], (position / causal_block + 1) * causal_block), and 0 at
  *        a negative position (1: causal; tokens a frame: each frame sees itself and earlier ones)
  *   lo = max(0, hi - window), or 0 with window = 0

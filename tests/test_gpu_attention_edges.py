@@ -1,0 +1,39 @@
+"""Calls at the edges of what the attention-side operators take: bounds below the counts, positions outside the
+sequence, bounds far above the work."""
+import numpy as np
+import pytest
+
+from oracle import attention as oa
+from tests.gpu_common import log, torch_mod
+from tests.test_gpu_attention import cache_of, check_attention, dev, host, ints, orbq, table_of  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d,heads,kv_heads,lens,new,most,block,window", [
+    (64, 2, 2, [200, 90], [7, 3], 2, 1, 0), (128, 4, 2, [200, 90], [9, 3], 4, 1, 37), (256, 2, 1, [200, 5], [7, 9], 3, 16, 0),
+    (128, 4, 4, [30000], [7], 2, 1, 0), (64, 4, 2, [700, 300], [400, 299], 90, 1, 0), (64, 2, 2, [700], [400], 90, 0, 70),
+    (128, 4, 2, [700, 300], [400, 310], 90, 50, 130), (256, 2, 2, [700], [333], 70, 1, 33),
+    (128, 2, 1, [1500], [1400], 1100, 1, 0), (128, 2, 1, [1900], [1600], 1100, 37, 900), (256, 2, 1, [900, 500], [700, 600], 500, 1, 450)])
+def test_a_bound_below_the_counts_moves_no_position(orbq, d, heads, kv_heads, lens, new, most, block, window):  # noqa: F811
+    """Query i of a sequence's n stands at len - n + i, whether or not max_new leaves the last ones out."""
+    torch = torch_mod()
+    log(f"bound {most} of {new} d={d} heads {heads}/{kv_heads} {lens} block {block} window {window}")
+    rng = np.random.default_rng(d + most)
+    page = 64
+    pages = sum(-(-n // page) for n in lens) + 2
+    table = table_of(rng, pages, lens, page)
+    c = cache_of(orbq, rng, pages, kv_heads, d, page)
+    c.k_scales.copy_(torch.from_numpy((np.exp(rng.standard_normal((pages, kv_heads))) / 40).astype(np.float32)))
+    total, cu = sum(new), np.concatenate([[0], np.cumsum(new)])
+    q, q64 = dev(rng.standard_normal((total, heads, d)), "bf16")
+    out, lse = torch.full_like(q, 7.0), torch.full((total, heads), 7.0, device="cuda")
+    orbq.kv_attention(c, q, ints(table), ints(lens), cu=ints(cu), max_new=most, causal_block=block, window=window, out=out,
+                      lse=lse)
+    kc, vc, ks, vs = host(c)
+    for b, n in enumerate(lens):
+        k, v = oa.kv_tokens(kc, ks, table[b], n, False), oa.kv_tokens(vc, vs, table[b], n, True)
+        want = oa.attention(q64[cu[b]:cu[b + 1]], k, v, block, window, d ** -0.5)
+        m = min(most, new[b])
+        check_attention(out[cu[b]:cu[b] + m], lse[cu[b]:cu[b] + m], tuple(x[:m] for x in want), d, "bf16", n)
+        assert bool((out[cu[b] + m:cu[b + 1]] == 7.0).all()) and bool((lse[cu[b] + m:cu[b + 1]] == 7.0).all())
