@@ -271,8 +271,8 @@ __global__ __launch_bounds__(threads_for(D* PAGE)) void k_read(const KvCache c, 
   int32_t rows, all;
   rows_of(x.cu, x.total, c.batch, x.max_rows, b, &row0, &rows, &all);
   const int64_t first = x.first[b];
-  if (first < 0 || rows == 0) return;
-  const int64_t p = first / PAGE + blockIdx.x;
+  if (rows == 0) return;
+  const int64_t p = (first - (first & (PAGE - 1))) / PAGE + blockIdx.x;  // rounded down: pages before token 0 are absent
   const int64_t t0 = p * PAGE;
   if (t0 >= first + rows) return;
   const int32_t pg = page_of(c, b, p);

@@ -351,7 +351,8 @@ typedef struct {
  * one if need <= old, else max(need, 1.25 old), and then the page's earlier codes become
  * rint(code * (old / scale)) (over any number of such steps at most 2.5 steps of the last scale are lost).
  * code = rint(x * (1 / scale)) clamped to +-127 (ties to even, fp32); a NaN is written as code 0, an
- * infinity as +-127.  The result does not depend on how the work is scheduled.
+ * infinity as +-127.  The result does not depend on how the work is scheduled.  A sequence with a negative start
+ * is not written.
  *   k, v  [device] head tensors of `total` packed rows, type f32, bf16 or f16, addresses and strides
  *         multiples of 16 bytes
  *   max_new  no sequence has more new tokens */
@@ -359,7 +360,8 @@ int orbq_kv_append(const orbq_kv_cache* cache, const orbq_page_table* table, con
                    int64_t total, int32_t max_new, const void* k, int64_t k_token, int64_t k_head, const void* v,
                    int64_t v_token, int64_t v_head, orbq_dtype type, void* stream);
 
-/* Reads tokens first[b] .. of each sequence (cu gives how many) back as code * scale, rounded to `type`.
+/* Reads tokens first[b] .. of each sequence (cu gives how many) back as code * scale, rounded to `type`; tokens at
+ * negative positions and of absent pages read as zero.
  *   k, v  [device] head tensors of `total` packed rows, written; addresses and strides multiples of 16 bytes */
 int orbq_kv_read(const orbq_kv_cache* cache, const orbq_page_table* table, const int32_t* first, const int32_t* cu,
                  int64_t total, int32_t max_tokens, void* k, int64_t k_token, int64_t k_head, void* v, int64_t v_token,

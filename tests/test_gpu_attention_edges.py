@@ -37,3 +37,27 @@ def test_a_bound_below_the_counts_moves_no_position(orbq, d, heads, kv_heads, le
         m = min(most, new[b])
         check_attention(out[cu[b]:cu[b] + m], lse[cu[b]:cu[b] + m], tuple(x[:m] for x in want), d, "bf16", n)
         assert bool((out[cu[b] + m:cu[b + 1]] == 7.0).all()) and bool((lse[cu[b] + m:cu[b + 1]] == 7.0).all())
+
+
+@pytest.mark.parametrize("name", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (256, 128)])
+def test_tokens_before_the_first_read_as_zero(orbq, name, d, page):  # noqa: F811
+    """Every row of the output is written: zero at negative positions, the tokens behind them as they are held."""
+    torch = torch_mod()
+    log(f"read before token 0 {name} d={d} page={page}")
+    rng = np.random.default_rng(page)
+    heads, n = 3, 2 * page + 9
+    first = [-5, -page, -3 * page - 1, -2 ** 31, 0]
+    pages = 5 * 3
+    table = np.arange(pages, dtype=np.int32).reshape(5, 3)
+    c = cache_of(orbq, rng, pages, heads, d, page)
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[name]
+    out = [torch.full((5 * n, heads, d), float("nan"), dtype=dt, device="cuda") for _ in range(2)]
+    orbq.kv_read(c, ints(table), ints(first), None, 5 * n, out=out)
+    kc, vc, ks, vs = host(c)
+    for o, codes, scales, turned in ((out[0], kc, ks, False), (out[1], vc, vs, True)):
+        for b, f in enumerate(first):
+            zeros = min(n, -f)
+            held = oa.kv_tokens(codes, scales, table[b], n, turned)[:n - zeros].astype(np.float32)
+            want = np.concatenate([np.zeros((zeros, heads, d), np.float32), held])
+            assert torch.equal(o[b * n:(b + 1) * n].cpu(), torch.from_numpy(want).to(dt)), b
