@@ -68,6 +68,10 @@ int check_packed(int64_t total, int32_t max_rows, int32_t batch, const int32_t* 
   return ORBQ_OK;
 }
 
+// A caller's bound may be far above the work (one for all the calls of a captured graph): grids and plans go by what
+// there can be.
+int32_t bound_rows(int32_t max_rows, int64_t total) { return total < max_rows ? static_cast<int32_t>(total) : max_rows; }
+
 // [rows][heads][width] with strides; rows of a head are contiguous
 int check_strided(const void* p, int64_t token, int64_t head, int32_t width, int size, size_t align, const char* what) {
   if (!p) return set_error(ORBQ_ERR_INVALID_ARG, "%s: NULL buffer", what);
@@ -104,7 +108,8 @@ int kv_move(bool read, const orbq_kv_cache* cache, const orbq_page_table* table,
     if ((s = check_written(kt, kh, total, c.heads, c.d, what))) return s;
     if ((s = check_written(vt, vh, total, c.heads, c.d, what))) return s;
   }
-  const orbq::KvTokens x{cu, first, total, max_rows, k, v, kt, kh, vt, vh};
+  if (!read && c.max_pages == 0) return set_ok();  // nowhere to write
+  const orbq::KvTokens x{cu, first, total, bound_rows(max_rows, total), k, v, kt, kh, vt, vh};
   const hipStream_t st = static_cast<hipStream_t>(stream);
   return hip_status(read ? orbq::launch_kv_read(c, x, type, st) : orbq::launch_kv_append(c, x, type, st), what);
 }
@@ -199,8 +204,8 @@ ORBQ_API size_t orbq_kv_attention_workspace_bytes(const orbq_kv_cache* cache, in
       max_len < 0 || max_len > kMaxTokens || causal_block < 0 || window < 0 ||
       static_cast<int64_t>(max_new) * (heads / cache->kv_heads) > kMaxRows)
     return 0;
-  const orbq::AttnPlan p = orbq::plan_attention(batch, total, max_new, heads, cache->kv_heads, cache->head_dim, max_len, causal_block,
-                                                window, true, orbq::device_cus());
+  const orbq::AttnPlan p = orbq::plan_attention(batch, total, bound_rows(max_new, total), heads, cache->kv_heads, cache->head_dim,
+                                                max_len, causal_block, window, true, orbq::device_cus());
   return turned_bytes(p, batch, cache->kv_heads, cache->head_dim) + factor_bytes(p, batch, cache->kv_heads) +
          part_bytes(p, cache->head_dim);
 }
@@ -231,6 +236,7 @@ ORBQ_API int orbq_kv_attention(const orbq_kv_cache* cache, const orbq_page_table
   if ((s = check_strided(q, q_token, q_head, a.c.d, 2, 16, what))) return s;
   if ((s = check_strided(o, o_token, o_head, a.c.d, 2, 8, what))) return s;
   if ((s = check_written(o_token, o_head, total, heads, a.c.d, what))) return s;
+  max_new = bound_rows(max_new, total);
   const int64_t most = static_cast<int64_t>(a.c.max_pages) * a.c.page;
   const int64_t len = max_len && max_len < most ? max_len : most;
   // tiles are turned into the workspace only where it is known how many there can be

@@ -139,7 +139,7 @@ __global__ __launch_bounds__(threads_for(D* PAGE)) void k_append(const KvCache c
   if (start < 0 || rows == 0) return;
   const int64_t p = start / PAGE + blockIdx.x;
   const int64_t t0 = p * PAGE;                       // the page's first token
-  if (t0 >= start + rows || c.max_pages == 0) return;
+  if (t0 >= start + rows) return;
   const int had = static_cast<int>(start > t0 ? start - t0 : 0);                        // tokens held before
   const int end = static_cast<int>(start + rows - t0 < PAGE ? start + rows - t0 : PAGE);  // and after
   // the page, and with it the old scale, are looked up while the new values are on their way
@@ -338,7 +338,8 @@ __global__ __launch_bounds__(threads_for(D* PAGE)) void k_read(const KvCache c, 
 
 template <bool READ, int DT, int D, int PAGE> int launch(const KvCache& c, const KvTokens& x, hipStream_t stream) {
   // pages that max_rows tokens in a row can touch
-  const int64_t pages = (static_cast<int64_t>(x.max_rows) + PAGE - 2) / PAGE + 1;
+  int64_t pages = (static_cast<int64_t>(x.max_rows) + PAGE - 2) / PAGE + 1;
+  if (!READ && pages > c.max_pages) pages = c.max_pages;  // nothing is written behind the table (which has pages)
   const dim3 grid(static_cast<uint32_t>(pages), 2 * c.heads, c.batch), block(threads_for(D * PAGE));
   if constexpr (READ) hipLaunchKernelGGL((k_read<DT, D, PAGE>), grid, block, 0, stream, c, x);
   else hipLaunchKernelGGL((k_append<DT, D, PAGE>), grid, block, 0, stream, c, x);

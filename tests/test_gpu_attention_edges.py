@@ -61,3 +61,27 @@ def test_tokens_before_the_first_read_as_zero(orbq, name, d, page):  # noqa: F81
             held = oa.kv_tokens(codes, scales, table[b], n, turned)[:n - zeros].astype(np.float32)
             want = np.concatenate([np.zeros((zeros, heads, d), np.float32), held])
             assert torch.equal(o[b * n:(b + 1) * n].cpu(), torch.from_numpy(want).to(dt)), b
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (256, 128)])
+def test_a_bound_far_above_the_work(orbq, d, page):  # noqa: F811
+    """The largest bound a caller may give for a call of few tokens: the same bits as with their number."""
+    torch = torch_mod()
+    log(f"bound 2^30 d={d} page={page}")
+    rng = np.random.default_rng(d)
+    heads, held, new = 2, [0, 3, 700], [3, 0, 2]
+    total, lens = sum(new), [a + b for a, b in zip(held, new)]
+    table = table_of(rng, 100, lens, page, extra=1)
+    a, b = (cache_of(orbq, np.random.default_rng(1), 100, heads, d, page) for _ in range(2))
+    x, _ = dev(rng.standard_normal((total, heads, d)), "bf16")
+    args = dict(cu=ints(np.concatenate([[0], np.cumsum(new)])))
+    most = 2 ** 30
+    orbq.kv_append(a, x, x, ints(table), ints(held), max_new=max(new), **args)
+    orbq.kv_append(b, x, x, ints(table), ints(held), max_new=most, **args)
+    for g, w in zip(host(b), host(a)):
+        assert np.array_equal(g, w)
+    want = orbq.kv_read(a, ints(table), ints(held), args["cu"], total, max_tokens=max(new))
+    got = orbq.kv_read(a, ints(table), ints(held), args["cu"], total, max_tokens=most)
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    want = orbq.kv_attention(a, x, ints(table), ints(lens), max_new=total, causal_block=1, **args)
+    assert torch.equal(orbq.kv_attention(a, x, ints(table), ints(lens), max_new=most, causal_block=1, **args), want)
