@@ -228,7 +228,7 @@ def kv_attention(cache: KVCache, q, table, lens, cu=None, max_new=None, causal_b
     sequence b stands at position lens[b] - n + i.  causal_block: 0 none, 1 causal, tokens a frame: each frame
     sees itself and earlier ones.  window: at most that many of the latest visible tokens (0: all).  scale:
     1 / sqrt(head_dim) if None.  lse: float32 [total, heads] to receive the logarithms of the sums.
-    max_len: expected bound of lens (None: what the table holds); it only guides how the work is split."""
+    max_len: expected bound of lens (None or 0: what the table holds); it only guides how the work is split."""
     func = "kv_attention"
     t, batch, pages = _table(table, cache, func)
     n, h, d, qt, qh, qp, code = _lay(q, func, "q")
@@ -247,7 +247,7 @@ def kv_attention(cache: KVCache, q, table, lens, cu=None, max_new=None, causal_b
                             not lse.is_contiguous()):
         raise _bad(func, f"lse must be contiguous float32 [{n}, {h}] on cuda:{dev}")
     held = pages * cache.page_tokens
-    max_len = held if max_len is None or max_len > held else max_len
+    max_len = held if not max_len or max_len > held else max_len
     lib = load()
     if workspace is None:
         need = _workspace(cache.kv_heads, d, dev, batch, n, max_new, h, max_len, causal_block, window)

@@ -85,3 +85,14 @@ def test_a_bound_far_above_the_work(orbq, d, page):  # noqa: F811
     assert all(torch.equal(g, w) for g, w in zip(got, want))
     want = orbq.kv_attention(a, x, ints(table), ints(lens), max_new=total, causal_block=1, **args)
     assert torch.equal(orbq.kv_attention(a, x, ints(table), ints(lens), max_new=most, causal_block=1, **args), want)
+
+
+@pytest.mark.parametrize("new", [1, 70])
+def test_no_expected_length(orbq, new):  # noqa: F811
+    """max_len 0 says nothing, as in C: the call is split as the table asks for, and finds its workspace."""
+    torch = torch_mod()
+    rng = np.random.default_rng(new)
+    c = cache_of(orbq, rng, 300, 1, 128, 128)
+    table, lens = ints(np.arange(300)[None]), ints([38001])
+    q, _ = dev(rng.standard_normal((new, 1, 128)), "bf16")
+    assert torch.equal(orbq.kv_attention(c, q, table, lens, max_len=0), orbq.kv_attention(c, q, table, lens))
