@@ -131,6 +131,25 @@ def _stream(torch, dev) -> int:
     return torch.cuda.current_stream(dev).cuda_stream
 
 
+def _on_its_device(call):
+    """`call` with the device of its first argument, a tensor, current: the raw handle of a stream (0 for every device's
+    default one) means a stream of the current device."""
+    first = call.__code__.co_varnames[0]
+
+    @functools.wraps(call)
+    def on(*args, **kw):
+        x = args[0] if args else kw.get(first)
+        device = x.get_device() if hasattr(x, "get_device") else -1
+        if device < 0:
+            return call(*args, **kw)      # which refuses it
+        import torch
+        if torch._C._cuda_getDevice() == device:
+            return call(*args, **kw)
+        with torch.cuda.device(device):
+            return call(*args, **kw)
+    return on
+
+
 def _dev_tensor(t, dtype, name):
     if not t.is_cuda:
         raise OrbqError(-1, name, "tensor must be on the GPU")
@@ -219,6 +238,7 @@ def linear_workspace_bytes(n: int, d: int, bits_a: int) -> int:
 
 
 # ------------------------------------------------------------------ the calls
+@_on_its_device
 def fold_weights(W, rot: Rotation, cb: Codebook, eps: float = 1e-8, out_codes=None, out_norms=None):
     """Offline fold + quantize of bf16 weights [m, d] -> (codes uint8 [m, d*b/8], r' bf16 [m])."""
     torch = _torch()
@@ -233,6 +253,7 @@ def fold_weights(W, rot: Rotation, cb: Codebook, eps: float = 1e-8, out_codes=No
     return codes, norms
 
 
+@_on_its_device
 def rpbh_quantize(X, rot: Rotation, cb: Codebook, eps: float = 1e-8, out_codes=None, out_norms=None):
     """Online activation quantization of bf16 tokens [n, d] -> (codes uint8 [n, d*b/8], s fp32 [n])."""
     torch = _torch()
@@ -257,6 +278,7 @@ def _act(act: str) -> int:
     return ACTIVATIONS[act]
 
 
+@_on_its_device
 def lut_gemm(x_codes, x_norms, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook, d: int, out_dtype=None, out=None,
              act: str = "none"):
     """Y [n, m] = act(diag(s) C_a[x_codes] C_w[w_codes]^T diag(r')); act "none" calls
@@ -279,6 +301,7 @@ def lut_gemm(x_codes, x_norms, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook,
     return Y
 
 
+@_on_its_device
 def linear(X, rot: Rotation, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook, eps: float = 1e-8, out_dtype=None,
            workspace=None, out=None, act: str = "none"):
     """The online layer: Y [n, m] from bf16 tokens X [n, d] and folded weights (act as in
@@ -311,6 +334,7 @@ def linear(X, rot: Rotation, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook, e
 NOALLOC_SCRATCH_BYTES = 16 << 20   # ORBQ_NOALLOC_SCRATCH_BYTES
 
 
+@_on_its_device
 def linear_noalloc(X, rot: Rotation, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook, eps: float = 1e-8,
                    out_dtype=None, out=None, act: str = "none"):
     """The online layer without a caller workspace (orbq_linear_noalloc): the token codes go to
@@ -336,6 +360,7 @@ def linear_a16_workspace_bytes(n: int, d: int, m: int) -> int:
     return int(load().orbq_linear_a16_workspace_bytes(n, d, m))
 
 
+@_on_its_device
 def linear_a16(X, rot: Rotation, w_codes, w_norms, cb_w: Codebook, out_dtype=None, workspace=None, out=None):
     """Weight-only product: Y [n, m] from bf16 tokens X [n, d] (rotated, not quantized) and
     folded weight codes (orbq_linear_a16)."""
@@ -357,6 +382,7 @@ def linear_a16(X, rot: Rotation, w_codes, w_norms, cb_w: Codebook, out_dtype=Non
     return Y
 
 
+@_on_its_device
 def flatness(X):
     """(rho3, rhoinf) fp32 [n] of bf16 rows X [n, d]: sqrt(d) ||x||_3^3 / ||x||_2^3 and
     sqrt(d) ||x||_inf / ||x||_2 (orbq_rpbh_flatness)."""
@@ -378,6 +404,7 @@ def rht_passes(rho3: float, rhoinf: float, d: int, vector_quantization: bool = F
     return r
 
 
+@_on_its_device
 def test_rotate(X, rot: Rotation):
     """Test-only: x' = Pi x (fp32 [n, d]) and s (fp32 [n]) as the quantize kernel computes them."""
     torch = _torch()
@@ -391,6 +418,7 @@ def test_rotate(X, rot: Rotation):
     return xr, s
 
 
+@_on_its_device
 def test_quantize_t(t, cb: Codebook):
     """Test-only: the kernels' decision on given normalised values t (fp32) -> sign-magnitude codes."""
     torch = _torch()
@@ -410,8 +438,9 @@ def test_mfma_rate(workgroups: int, iters: int, sink=None, device=None) -> float
     if sink is None:
         sink = torch.empty((workgroups * 512,), dtype=torch.float32, device=dev)
     flops = ctypes.c_double(0.0)
-    _check(load().orbq_test_mfma_rate(workgroups, iters, sink.data_ptr(), ctypes.byref(flops), _stream(torch, dev)),
-           "orbq_test_mfma_rate")
+    with torch.cuda.device(dev):
+        _check(load().orbq_test_mfma_rate(workgroups, iters, sink.data_ptr(), ctypes.byref(flops), _stream(torch, dev)),
+               "orbq_test_mfma_rate")
     return flops.value
 
 

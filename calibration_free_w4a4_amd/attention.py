@@ -41,6 +41,12 @@ def _stream(device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device)  # torch.cuda.current_stream(device).cuda_stream, 2 us less
 
 
+def _current() -> int:
+    """The current device.  A stream's raw handle (0 for every device's default one) means a stream of that device, so each
+    call below makes the tensors' device current first."""
+    return torch._C._cuda_getDevice()
+
+
 def _lay(t, func: str, name: str):
     """(tokens, heads, head_dim, token stride, head stride, address, type) of a head tensor: on the GPU, [tokens,
     heads, head_dim] with contiguous heads.  A dimension of one entry has no stride of its own: 0."""
@@ -97,6 +103,9 @@ def _written(x, y, func: str):
 
 
 def _turn(func, rope, positions, q, k, inverse, out):
+    if _current() != rope.device:
+        with torch.cuda.device(rope.device):
+            return _turn(func, rope, positions, q, k, inverse, out)
     n, h, d, xt, xh, x, code = _lay(q, func, "q")
     dev = rope.device
     if q.get_device() != dev:
@@ -175,6 +184,9 @@ def _table(table, cache, func: str):
 
 
 def _move(func, entry, cache, k, v, table, first, cu, most):
+    if _current() != cache.device:
+        with torch.cuda.device(cache.device):
+            return _move(func, entry, cache, k, v, table, first, cu, most)
     t, batch, _ = _table(table, cache, func)
     n, h, d, kt, kh, kp, code = _lay(k, func, "k")
     nv, hv, dv, vt, vh, vp, code_v = _lay(v, func, "v")
@@ -212,8 +224,9 @@ def kv_read(cache: KVCache, table, first, cu, total: int, max_tokens=None, dtype
 # ---------------------------------------------------------------------------------------- attention
 def kv_attention_workspace_bytes(cache: KVCache, batch: int, total: int, max_new: int, heads: int, max_len: int,
                                  causal_block: int = 0, window: int = 0) -> int:
-    return int(load().orbq_kv_attention_workspace_bytes(cache.packed, batch, total, max_new, heads, max_len, causal_block,
-                                                        window))
+    with torch.cuda.device(cache.device):
+        return int(load().orbq_kv_attention_workspace_bytes(cache.packed, batch, total, max_new, heads, max_len, causal_block,
+                                                            window))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -230,6 +243,9 @@ def kv_attention(cache: KVCache, q, table, lens, cu=None, max_new=None, causal_b
     1 / sqrt(head_dim) if None.  lse: float32 [total, heads] to receive the logarithms of the sums.
     max_len: expected bound of lens (None or 0: what the table holds); it only guides how the work is split."""
     func = "kv_attention"
+    if _current() != cache.device:
+        with torch.cuda.device(cache.device):
+            return kv_attention(cache, q, table, lens, cu, max_new, causal_block, window, scale, max_len, out, lse, workspace)
     t, batch, pages = _table(table, cache, func)
     n, h, d, qt, qh, qp, code = _lay(q, func, "q")
     dev = cache.device

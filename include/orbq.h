@@ -42,7 +42,8 @@
  * Memory: every buffer is owned by the caller.  Pointers marked [device] are HIP device
  * pointers, [host] are host pointers.  The library allocates no device memory: the
  * workspaces of orbq_linear, orbq_linear_act and orbq_linear_a16 come from the caller.
- * Calls are asynchronous on `stream` (a hipStream_t; NULL = the default stream) and
+ * Calls are asynchronous on `stream` (a hipStream_t; NULL = the default stream) of the current device,
+ * which has to be the one that holds the buffers (a size helper's answer holds for the current device too), and
  * re-entrant (calls that share a workspace must not overlap); argument errors are
  * detected on the host before anything is launched and are returned synchronously.
  * Device faults surface at the caller's next synchronisation.  Device arrays (perm,

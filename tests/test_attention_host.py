@@ -18,3 +18,100 @@ def test_a_bound_above_the_work_changes_no_plan(batch, total, max_len, d):
     assert size(total) > 0
     for most in (total + 1, 1000 * total, 2 ** 30):
         assert size(most) == size(total)
+
+
+class Elsewhere:
+    """A CPU tensor that says it is on cuda:1."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def get_device(self):
+        return 1
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.fixture
+def two_devices(monkeypatch):
+    """cuda:0 is current; the library's entry points note which device is when they are called."""
+    torch = pytest.importorskip("torch")
+    from calibration_free_w4a4_amd import attention as at
+    current, seen = [0], []
+
+    class on:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.device
+
+        def __exit__(self, *args):
+            current[0] = self.before
+
+    class Library:
+        def __getattr__(self, name):
+            def entry(*args):
+                seen.append((name, current[0]))
+                return 0
+            return entry
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", on)
+    for m in (orbq, at):
+        monkeypatch.setattr(m, "load", lambda: Library())
+    monkeypatch.setattr(at, "_stream", lambda device: 0)
+    monkeypatch.setattr(orbq, "_stream", lambda torch, device: 0)
+    monkeypatch.setattr(orbq, "_torch", lambda: torch)
+    at._workspace.cache_clear()
+    yield seen
+    at._workspace.cache_clear()
+    assert current[0] == 0
+
+
+def launches(seen):
+    sizes = ("workspace_bytes", "row_bytes")      # the second goes by no device
+    return [(n, d) for n, d in seen if not n.endswith(sizes[1])]
+
+
+def test_attention_calls_run_on_the_tensors_device(two_devices):
+    import torch
+    from calibration_free_w4a4_amd import attention as at
+    x = lambda *s, dtype=torch.bfloat16: Elsewhere(torch.zeros(s, dtype=dtype))  # noqa: E731
+    r = at.Rope((32,), x(16, dtype=torch.float32))
+    q, pos = x(4, 2, 64), x(4, 1, dtype=torch.float32)
+    at.rope(r, pos, q, out=x(4, 2, 64))
+    at.rope_backward(r, pos, q, q, out=(x(4, 2, 64), x(4, 2, 64)))
+    c = at.KVCache(x(3, 2, 16, 64, dtype=torch.int8), x(3, 2, 64, 16, dtype=torch.int8), x(3, 2, dtype=torch.float32),
+                   x(3, 2, dtype=torch.float32))
+    table, lens = x(1, 3, dtype=torch.int32), x(1, dtype=torch.int32)
+    at.kv_append(c, q, q, table, lens)
+    at.kv_read(c, table, lens, None, 4, out=(x(4, 2, 64), x(4, 2, 64)))
+    at.kv_attention(c, q, table, lens, out=x(4, 2, 64))
+    at.kv_attention_workspace_bytes(c, 1, 4, 4, 2, 48)
+    assert [n for n, _ in two_devices] == ["orbq_rope_apply"] * 2 + ["orbq_kv_append", "orbq_kv_read"] + \
+        ["orbq_kv_attention_workspace_bytes", "orbq_kv_attention", "orbq_kv_attention_workspace_bytes"]
+    assert all(device == 1 for _, device in two_devices)
+
+
+def test_layer_calls_run_on_the_tensors_device(two_devices):
+    import numpy as np
+    import torch
+    x = lambda *s, dtype=torch.bfloat16: Elsewhere(torch.zeros(s, dtype=dtype))  # noqa: E731
+    rot = orbq.Rotation(64, 64, None, torch.zeros(64, dtype=torch.int8))
+    cb = orbq.Codebook.from_centroids(64, 4, np.arange(16) - 7.5)
+    X, codes, norms, y = x(2, 64), x(2, 32, dtype=torch.uint8), x(2, dtype=torch.float32), x(2, 2, dtype=torch.float32)
+    both = dict(out_codes=codes, out_norms=norms)
+    orbq.fold_weights(X, rot, cb, **both)
+    orbq.rpbh_quantize(X=X, rot=rot, cb=cb, **both)
+    orbq.lut_gemm(codes, norms, cb, codes, norms, cb, 64, out=y)
+    orbq.linear(X, rot, cb, codes, norms, cb, workspace=x(512, dtype=torch.uint8), out=y)
+    orbq.linear_noalloc(X, rot, cb, codes, norms, cb, out=y)
+    orbq.linear_a16(X, rot, codes, norms, cb, workspace=x(512, dtype=torch.uint8), out=y)
+    orbq.flatness(X)
+    orbq.test_rotate(X, rot)
+    orbq.test_quantize_t(norms, cb)
+    got = launches(two_devices)
+    assert len(got) == 11 and all(device == 1 for _, device in got), got      # nine launches, two sizes
