@@ -13,6 +13,7 @@ Head tensors are [tokens, heads, head_dim] with the last dimension contiguous.
 from __future__ import annotations
 
 import functools
+import operator
 import struct
 
 import torch
@@ -68,12 +69,21 @@ def _ints(t, device: int, count: int, func: str, name: str) -> int:
     return t.data_ptr()
 
 
+def _fixed(cls):
+    """Gives the private slots of `cls` public names that cannot be set: the packed C struct holds their values and
+    addresses, and would go on holding those of a tensor that is gone."""
+    for name in cls.__slots__:
+        setattr(cls, name[1:], property(operator.attrgetter(name)))
+    return cls
+
+
 # ------------------------------------------------------------------------------------ rotary positions
+@_fixed
 class Rope:
     """dims: entries of a head that each axis turns (even; in order from entry 0; the rest of the head
     passes through).  freqs: float32 [sum(dims) / 2] on the GPU, radians per unit of position for each
-    pair.  layout: "pairs" (2 i, 2 i + 1) or "halves" (i, i + sum(dims) / 2)."""
-    __slots__ = ("dims", "freqs", "layout", "packed", "device")
+    pair.  layout: "pairs" (2 i, 2 i + 1) or "halves" (i, i + sum(dims) / 2).  Attributes are read only."""
+    __slots__ = ("_dims", "_freqs", "_layout", "_packed", "_device")
 
     def __init__(self, dims, freqs, layout: str = "pairs"):
         dims = tuple(dims)
@@ -81,8 +91,8 @@ class Rope:
             raise _bad("Rope", f"{len(dims)} axes (1 to 4), layout {layout!r} (one of {sorted(LAYOUTS)})")
         if freqs.dtype != torch.float32 or not freqs.is_cuda or freqs.shape != (sum(dims) // 2,) or not freqs.is_contiguous():
             raise _bad("Rope", f"freqs must be contiguous float32 [{sum(dims) // 2}] on the GPU")
-        self.dims, self.freqs, self.layout, self.device = dims, freqs, layout, freqs.get_device()
-        self.packed = _ROPE.pack(len(dims), *dims, *(0,) * (4 - len(dims)), freqs.data_ptr(), LAYOUTS[layout])
+        self._dims, self._freqs, self._layout, self._device = dims, freqs, layout, freqs.get_device()
+        self._packed = _ROPE.pack(len(dims), *dims, *(0,) * (4 - len(dims)), freqs.data_ptr(), LAYOUTS[layout])
 
     @classmethod
     def create(cls, dims, theta: float = 10000.0, layout: str = "pairs", device=None) -> "Rope":
@@ -103,16 +113,16 @@ def _written(x, y, func: str):
 
 
 def _turn(func, rope, positions, q, k, inverse, out):
-    if _current() != rope.device:
-        with torch.cuda.device(rope.device):
+    if _current() != rope._device:
+        with torch.cuda.device(rope._device):
             return _turn(func, rope, positions, q, k, inverse, out)
     n, h, d, xt, xh, x, code = _lay(q, func, "q")
-    dev = rope.device
+    dev = rope._device
     if q.get_device() != dev:
         raise _bad(func, f"q must be on cuda:{dev}, where the frequencies are")
     if positions.dtype != torch.float32 or positions.get_device() != dev or positions.dim() != 2 or \
-            positions.shape[1] != len(rope.dims) or not positions.is_contiguous():
-        raise _bad(func, f"positions must be contiguous float32 [tokens, {len(rope.dims)}] on cuda:{dev}")
+            positions.shape[1] != len(rope._dims) or not positions.is_contiguous():
+        raise _bad(func, f"positions must be contiguous float32 [tokens, {len(rope._dims)}] on cuda:{dev}")
     if out is not None:
         yq, yk = (out, None) if k is None else out
     else:
@@ -125,7 +135,7 @@ def _turn(func, rope, positions, q, k, inverse, out):
         if out is None:
             yk = _like(k)
         heads += _HEADS.pack(x, yk.data_ptr(), h, xt, xh, *((h * d, d) if out is None else _written(k, yk, func)))
-    st = load().orbq_rope_apply(rope.packed, positions.data_ptr(), positions.shape[0], n, d, heads, 1 if k is None else 2,
+    st = load().orbq_rope_apply(rope._packed, positions.data_ptr(), positions.shape[0], n, d, heads, 1 if k is None else 2,
                                 code, inverse, _stream(dev))
     if st:
         _check(st, "orbq_rope_apply")
@@ -145,10 +155,12 @@ def rope_backward(rope: Rope, positions, dq, dk=None, out=None):
 
 
 # ------------------------------------------------------------------------------------------ the cache
+@_fixed
 class KVCache:
     """k_codes int8 [pages, kv_heads, page_tokens, head_dim], v_codes int8 [pages, kv_heads, head_dim,
-    page_tokens], k_scales and v_scales float32 [pages, kv_heads], all contiguous on one GPU."""
-    __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "kv_heads", "page_tokens", "head_dim", "packed", "device")
+    page_tokens], k_scales and v_scales float32 [pages, kv_heads], all contiguous on one GPU.  Attributes are read
+    only; what the tensors hold may be written."""
+    __slots__ = ("_k_codes", "_v_codes", "_k_scales", "_v_scales", "_kv_heads", "_page_tokens", "_head_dim", "_packed", "_device")
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
         if k_codes.dim() != 4:
@@ -159,9 +171,9 @@ class KVCache:
                                (k_scales, (n, h), torch.float32), (v_scales, (n, h), torch.float32)):
             if x.shape != shape or x.dtype != kind or x.get_device() != dev or dev < 0 or not x.is_contiguous():
                 raise _bad("KVCache", f"expected contiguous {kind} {shape} on one GPU, got {x.dtype} {tuple(x.shape)} on {x.device}")
-        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
-        self.kv_heads, self.page_tokens, self.head_dim, self.device = h, t, d, dev
-        self.packed = _CACHE.pack(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), n, h, t, d)
+        self._k_codes, self._v_codes, self._k_scales, self._v_scales = k_codes, v_codes, k_scales, v_scales
+        self._kv_heads, self._page_tokens, self._head_dim, self._device = h, t, d, dev
+        self._packed = _CACHE.pack(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), n, h, t, d)
 
     @classmethod
     def create(cls, num_pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device=None) -> "KVCache":
@@ -174,8 +186,8 @@ class KVCache:
 
 def _table(table, cache, func: str):
     """(packed page table, batch, pages a row)"""
-    if table.dtype != torch.int32 or table.get_device() != cache.device or table.dim() != 2:
-        raise _bad(func, f"table must be int32 [batch, pages] on cuda:{cache.device}")
+    if table.dtype != torch.int32 or table.get_device() != cache._device or table.dim() != 2:
+        raise _bad(func, f"table must be int32 [batch, pages] on cuda:{cache._device}")
     b, p = table.shape
     ld, one = table.stride()
     if one != 1 and p > 1:
@@ -184,21 +196,21 @@ def _table(table, cache, func: str):
 
 
 def _move(func, entry, cache, k, v, table, first, cu, most):
-    if _current() != cache.device:
-        with torch.cuda.device(cache.device):
+    if _current() != cache._device:
+        with torch.cuda.device(cache._device):
             return _move(func, entry, cache, k, v, table, first, cu, most)
     t, batch, _ = _table(table, cache, func)
     n, h, d, kt, kh, kp, code = _lay(k, func, "k")
     nv, hv, dv, vt, vh, vp, code_v = _lay(v, func, "v")
-    dev = cache.device
-    if h != cache.kv_heads or d != cache.head_dim or (nv, hv, dv, code_v) != (n, h, d, code) or k.get_device() != dev or \
+    dev = cache._device
+    if h != cache._kv_heads or d != cache._head_dim or (nv, hv, dv, code_v) != (n, h, d, code) or k.get_device() != dev or \
             v.get_device() != dev:
-        raise _bad(func, f"k and v must be [tokens, {cache.kv_heads}, {cache.head_dim}] of one type on cuda:{dev}")
+        raise _bad(func, f"k and v must be [tokens, {cache._kv_heads}, {cache._head_dim}] of one type on cuda:{dev}")
     first = _ints(first, dev, batch, func, "positions")
     cu = 0 if cu is None else _ints(cu, dev, batch + 1, func, "cu")
     if most is None:
         most = n if cu else n // max(1, batch)
-    st = entry(cache.packed, t, first, cu, n, most, kp, kt, kh, vp, vt, vh, code, _stream(dev))
+    st = entry(cache._packed, t, first, cu, n, most, kp, kt, kh, vp, vt, vh, code, _stream(dev))
     if st:
         _check(st, "orbq_" + func)
 
@@ -213,7 +225,7 @@ def kv_append(cache: KVCache, k, v, table, start, cu=None, max_new=None) -> None
 def kv_read(cache: KVCache, table, first, cu, total: int, max_tokens=None, dtype=torch.bfloat16, out=None):
     """(k, v) [total, kv_heads, head_dim] of tokens first[b] .. of each sequence, cu as in kv_append."""
     if out is None:
-        k = cache.k_scales.new_empty((total, cache.kv_heads, cache.head_dim), dtype=dtype)
+        k = cache._k_scales.new_empty((total, cache._kv_heads, cache._head_dim), dtype=dtype)
         out = (k, torch.empty_like(k))
     elif out[0].shape[0] != total:
         raise _bad("kv_read", f"out must have {total} tokens")
@@ -224,8 +236,8 @@ def kv_read(cache: KVCache, table, first, cu, total: int, max_tokens=None, dtype
 # ---------------------------------------------------------------------------------------- attention
 def kv_attention_workspace_bytes(cache: KVCache, batch: int, total: int, max_new: int, heads: int, max_len: int,
                                  causal_block: int = 0, window: int = 0) -> int:
-    with torch.cuda.device(cache.device):
-        return int(load().orbq_kv_attention_workspace_bytes(cache.packed, batch, total, max_new, heads, max_len, causal_block,
+    with torch.cuda.device(cache._device):
+        return int(load().orbq_kv_attention_workspace_bytes(cache._packed, batch, total, max_new, heads, max_len, causal_block,
                                                             window))
 
 
@@ -243,14 +255,14 @@ def kv_attention(cache: KVCache, q, table, lens, cu=None, max_new=None, causal_b
     1 / sqrt(head_dim) if None.  lse: float32 [total, heads] to receive the logarithms of the sums.
     max_len: expected bound of lens (None or 0: what the table holds); it only guides how the work is split."""
     func = "kv_attention"
-    if _current() != cache.device:
-        with torch.cuda.device(cache.device):
+    if _current() != cache._device:
+        with torch.cuda.device(cache._device):
             return kv_attention(cache, q, table, lens, cu, max_new, causal_block, window, scale, max_len, out, lse, workspace)
     t, batch, pages = _table(table, cache, func)
     n, h, d, qt, qh, qp, code = _lay(q, func, "q")
-    dev = cache.device
-    if d != cache.head_dim or q.get_device() != dev:
-        raise _bad(func, f"q must be [tokens, heads, {cache.head_dim}] on cuda:{dev}")
+    dev = cache._device
+    if d != cache._head_dim or q.get_device() != dev:
+        raise _bad(func, f"q must be [tokens, heads, {cache._head_dim}] on cuda:{dev}")
     lens = _ints(lens, dev, batch, func, "lens")
     cu = 0 if cu is None else _ints(cu, dev, batch + 1, func, "cu")
     if max_new is None:
@@ -262,17 +274,17 @@ def kv_attention(cache: KVCache, q, table, lens, cu=None, max_new=None, causal_b
     if lse is not None and (lse.shape != (n, h) or lse.dtype != torch.float32 or lse.get_device() != dev or
                             not lse.is_contiguous()):
         raise _bad(func, f"lse must be contiguous float32 [{n}, {h}] on cuda:{dev}")
-    held = pages * cache.page_tokens
+    held = pages * cache._page_tokens
     max_len = held if not max_len or max_len > held else max_len
     lib = load()
     if workspace is None:
-        need = _workspace(cache.kv_heads, d, dev, batch, n, max_new, h, max_len, causal_block, window)
+        need = _workspace(cache._kv_heads, d, dev, batch, n, max_new, h, max_len, causal_block, window)
         if need:
             workspace = q.new_empty((need + 1) // 2)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise _bad(func, f"workspace must be contiguous on cuda:{dev}")
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = lib.orbq_kv_attention(cache.packed, t, lens, cu, n, max_new, max_len, qp, qt, qh, h, out.data_ptr(), ot, oh,
+    st = lib.orbq_kv_attention(cache._packed, t, lens, cu, n, max_new, max_len, qp, qt, qh, h, out.data_ptr(), ot, oh,
                                0 if lse is None else lse.data_ptr(), code, d ** -0.5 if scale is None else scale, causal_block,
                                window, ws, ws_bytes, _stream(dev))
     if st:

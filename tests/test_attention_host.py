@@ -115,3 +115,22 @@ def test_layer_calls_run_on_the_tensors_device(two_devices):
     orbq.test_quantize_t(norms, cb)
     got = launches(two_devices)
     assert len(got) == 11 and all(device == 1 for _, device in got), got      # nine launches, two sizes
+
+
+def test_what_the_packed_structs_hold_cannot_be_replaced():
+    """The C structs keep the tensors' addresses: a tensor set on the object would not be used, and the one that it
+    replaced might be freed."""
+    torch = pytest.importorskip("torch")
+    from calibration_free_w4a4_amd import attention as at
+    x = lambda *s, dtype: Elsewhere(torch.zeros(s, dtype=dtype))  # noqa: E731
+    freqs = x(16, dtype=torch.float32)
+    r = at.Rope((32,), freqs, "halves")
+    assert (r.dims, r.layout, r.device) == ((32,), "halves", 1) and r.freqs is freqs
+    codes, scales = x(3, 2, 16, 64, dtype=torch.int8), x(3, 2, dtype=torch.float32)
+    c = at.KVCache(codes, x(3, 2, 64, 16, dtype=torch.int8), scales, scales)
+    assert c.k_codes is codes and c.v_scales is scales and (c.kv_heads, c.page_tokens, c.head_dim, c.device) == (2, 16, 64, 1)
+    for o, names in ((r, "dims freqs layout packed device"),
+                     (c, "k_codes v_codes k_scales v_scales kv_heads page_tokens head_dim packed device")):
+        for name in names.split():
+            with pytest.raises(AttributeError):
+                setattr(o, name, getattr(o, name))
