@@ -82,10 +82,26 @@ int check_strided(const void* p, int64_t token, int64_t head, int32_t width, int
   return ORBQ_OK;
 }
 
+// Whether any two rows of `width` elements, tokens `token` apart and heads `head` apart, share an element.
+bool rows_overlap(int64_t token, int64_t head, int64_t tokens, int32_t heads, int32_t width) {
+  if ((heads > 1 && head < width) || (tokens > 1 && token < width)) return true;
+  if (heads <= 1 || tokens <= 1) return false;
+  // [token][head] and [head][token], the usual orders: one dimension's rows lie between two steps of the other
+  if ((token - width) / (heads - 1) >= head || (head - width) / (tokens - 1) >= token) return false;
+  // else no number of heads may come within a row of a number of tokens
+  for (int64_t j = 1; j < heads; ++j) {
+    const unsigned __int128 at = static_cast<unsigned __int128>(j) * static_cast<uint64_t>(head);
+    const unsigned __int128 i = at / static_cast<uint64_t>(token);
+    const uint64_t rest = static_cast<uint64_t>(at % static_cast<uint64_t>(token));
+    if (i < static_cast<uint64_t>(tokens) && rest < static_cast<uint64_t>(width)) return true;
+    if (i + 1 < static_cast<uint64_t>(tokens) && static_cast<uint64_t>(token) - rest < static_cast<uint64_t>(width)) return true;
+  }
+  return false;
+}
+
 // an output whose rows must not overlap
 int check_written(int64_t token, int64_t head, int64_t tokens, int32_t heads, int32_t width, const char* what) {
-  if ((heads > 1 && head < width) || (tokens > 1 && token < width))
-    return set_error(ORBQ_ERR_INVALID_ARG, "%s: rows of the output overlap", what);
+  if (rows_overlap(token, head, tokens, heads, width)) return set_error(ORBQ_ERR_INVALID_ARG, "%s: rows of the output overlap", what);
   return ORBQ_OK;
 }
 

@@ -134,3 +134,24 @@ def test_what_the_packed_structs_hold_cannot_be_replaced():
         for name in names.split():
             with pytest.raises(AttributeError):
                 setattr(o, name, getattr(o, name))
+
+
+@pytest.mark.parametrize("tokens,heads,width", [(6, 4, 64), (2, 2, 64), (5, 7, 64), (1, 4, 64), (9, 1, 64)])
+def test_outputs_whose_rows_overlap_are_refused(tokens, heads, width):
+    """Against all pairs of rows, for strides around the row's width and in both orders of tokens and heads."""
+    import itertools
+    P, lib = 0x10000, orbq.load()
+    r = Structs._Rope(1, (ctypes.c_int32 * 4)(width), P, 0)
+    steps = sorted({width // 2, width - 2, width, width + 2, 2 * width, 3 * width, 3 * width + 2, heads * width - 2, heads * width,
+                    tokens * width - 2, tokens * width, tokens * width + 6, 5 * width // 2})
+    some = [0, 0]
+    for ts, hs in itertools.product(steps, steps):
+        rows = sorted(i * ts + j * hs for i in range(tokens) for j in range(heads))
+        bad = any(b - a < width for a, b in zip(rows, rows[1:]))
+        # the second tensor is refused in any case, with another status, so that nothing is launched
+        t = (Structs._Heads * 2)(Structs._Heads(P, P, heads, heads * width, width, ts, hs),
+                                 Structs._Heads(P, P, 20000, 128, 64, 128, 64))
+        status = lib.orbq_rope_apply(ctypes.byref(r), P, tokens, tokens, width, t, 2, 1, 0, None)
+        assert status == (-1 if bad else -2), (ts, hs, status, lib.orbq_last_error())
+        some[bad] += 1
+    assert all(some)
