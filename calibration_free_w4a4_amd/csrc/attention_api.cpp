@@ -72,13 +72,12 @@ int check_packed(int64_t total, int32_t max_rows, int32_t batch, const int32_t* 
 // there can be.
 int32_t bound_rows(int32_t max_rows, int64_t total) { return total < max_rows ? static_cast<int32_t>(total) : max_rows; }
 
-// [rows][heads][width] with strides; rows of a head are contiguous
-int check_strided(const void* p, int64_t token, int64_t head, int32_t width, int size, size_t align, const char* what) {
+// [rows][heads][...] with strides in elements of `size` bytes, which divide `align`
+int check_strided(const void* p, int64_t token, int64_t head, int size, int align, const char* what) {
   if (!p) return set_error(ORBQ_ERR_INVALID_ARG, "%s: NULL buffer", what);
   if (token < 0 || head < 0) return set_error(ORBQ_ERR_INVALID_ARG, "%s: negative stride", what);
-  if (!aligned(p, align) || (token * size) % static_cast<int64_t>(align) || (head * size) % static_cast<int64_t>(align))
-    return set_error(ORBQ_ERR_ALIGNMENT, "%s: base and strides must be multiples of %d bytes", what, static_cast<int>(align));
-  (void)width;
+  if (!aligned(p, align) || token % (align / size) || head % (align / size))
+    return set_error(ORBQ_ERR_ALIGNMENT, "%s: base and strides must be multiples of %d bytes", what, align);
   return ORBQ_OK;
 }
 
@@ -118,8 +117,8 @@ int kv_move(bool read, const orbq_kv_cache* cache, const orbq_page_table* table,
   if (!first) return set_error(ORBQ_ERR_INVALID_ARG, "%s: NULL positions", what);
   if (!aligned(first, 4)) return set_error(ORBQ_ERR_ALIGNMENT, "%s: positions misaligned", what);
   const int size = orbq::dtype_size(type);
-  if ((s = check_strided(k, kt, kh, c.d, size, 16, what))) return s;
-  if ((s = check_strided(v, vt, vh, c.d, size, 16, what))) return s;
+  if ((s = check_strided(k, kt, kh, size, 16, what))) return s;
+  if ((s = check_strided(v, vt, vh, size, 16, what))) return s;
   if (read) {
     if ((s = check_written(kt, kh, total, c.heads, c.d, what))) return s;
     if ((s = check_written(vt, vh, total, c.heads, c.d, what))) return s;
@@ -180,8 +179,8 @@ ORBQ_API int orbq_rope_apply(const orbq_rope* rope, const float* positions, int6
     if (t.heads < 0) return set_error(ORBQ_ERR_INVALID_ARG, "%s: negative heads", what);
     if (t.heads == 0) continue;
     if (t.heads > 16384) return set_error(ORBQ_ERR_UNSUPPORTED, "%s: heads above 16384", what);
-    if ((s = check_strided(t.x, t.x_token, t.x_head, head_dim, size, size, what))) return s;
-    if ((s = check_strided(t.y, t.y_token, t.y_head, head_dim, size, size, what))) return s;
+    if ((s = check_strided(t.x, t.x_token, t.x_head, size, size, what))) return s;
+    if ((s = check_strided(t.y, t.y_token, t.y_head, size, size, what))) return s;
     if ((s = check_written(t.y_token, t.y_head, n, t.heads, head_dim, what))) return s;
     a.t[i] = orbq::RopeTensor{t.x, t.y, t.heads, t.x_token, t.x_head, t.y_token, t.y_head};
     all += t.heads;
@@ -249,8 +248,8 @@ ORBQ_API int orbq_kv_attention(const orbq_kv_cache* cache, const orbq_page_table
   if ((s = check_cache_buffers(a.c, what))) return s;
   if (!lens) return set_error(ORBQ_ERR_INVALID_ARG, "%s: NULL lens", what);
   if (!aligned(lens, 4) || !aligned(lse, 4)) return set_error(ORBQ_ERR_ALIGNMENT, "%s: lens or lse misaligned", what);
-  if ((s = check_strided(q, q_token, q_head, a.c.d, 2, 16, what))) return s;
-  if ((s = check_strided(o, o_token, o_head, a.c.d, 2, 8, what))) return s;
+  if ((s = check_strided(q, q_token, q_head, 2, 16, what))) return s;
+  if ((s = check_strided(o, o_token, o_head, 2, 8, what))) return s;
   if ((s = check_written(o_token, o_head, total, heads, a.c.d, what))) return s;
   max_new = bound_rows(max_new, total);
   const int64_t most = static_cast<int64_t>(a.c.max_pages) * a.c.page;
