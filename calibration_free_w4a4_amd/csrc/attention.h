@@ -85,6 +85,8 @@ struct AttnArgs {
   int32_t turned_tiles;
 };
 
+constexpr int64_t kMostTiles = 0x7fffffff;  // row tiles of a call in the form for many rows
+
 // rows of a workgroup in the form for many rows, 32 a wave
 constexpr int many_rows(int d) { return d == 128 ? 256 : 128; }
 

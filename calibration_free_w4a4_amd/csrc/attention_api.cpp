@@ -257,6 +257,8 @@ ORBQ_API int orbq_kv_attention(const orbq_kv_cache* cache, const orbq_page_table
   // tiles are turned into the workspace only where it is known how many there can be
   const orbq::AttnPlan p = orbq::plan_attention(a.c.batch, total, max_new, heads, a.c.heads, a.c.d, len, causal_block, window,
                                                 len == most, orbq::device_cus());
+  if (p.many && static_cast<int64_t>(a.c.batch) * a.c.heads * p.row_tiles > orbq::kMostTiles)
+    return set_error(ORBQ_ERR_UNSUPPORTED, "%s: more than 2^31 row tiles (batch, heads and max_new too large)", what);
   const size_t turned = turned_bytes(p, a.c.batch, a.c.heads, a.c.d), factors = factor_bytes(p, a.c.batch, a.c.heads);
   const size_t need = turned + factors + part_bytes(p, a.c.d);
   if (need) {

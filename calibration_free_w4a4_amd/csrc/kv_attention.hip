@@ -31,7 +31,7 @@ AttnPlan plan_attention(int32_t batch, int64_t total, int32_t max_new, int32_t h
   const int64_t groups = static_cast<int64_t>(batch) * kv_heads * p.row_tiles;
   int64_t splits = 1, whole = groups, part_tiles = tiles;
   p.waves = 4;
-  if (p.many) {
+  if (p.many && groups <= kMostTiles) {  // more of them are refused
     // Workgroups resident at once: one a CU (LDS and registers), three with heads of 64.  Row tiles that fill whole
     // rounds are not split, those of the last round are, so that it is full too (2 x 4605 queries of 8 heads of 256,
     // 576 row tiles: all in three parts 528 us, the last 64 in four 435).  Sequences of unequal rows leave row
@@ -68,9 +68,9 @@ AttnPlan plan_attention(int32_t batch, int64_t total, int32_t max_new, int32_t h
     if (window) readers = std::min<int64_t>(readers, (static_cast<int64_t>(window) + causal_block + 63) / tile_tokens + 1);
     if (bound && d > 64 && readers >= 8 && static_cast<int64_t>(batch) * kv_heads * tiles * d <= (int64_t{1} << 22))
       p.turned = static_cast<int32_t>(tiles);  // at most 1 GiB of workspace
-  } else if (p.rt == 1 && d <= 128 && (tiles * d <= 17 * 128 || (4 * groups >= 3 * cus && groups <= cus))) {
+  } else if (!p.many && p.rt == 1 && d <= 128 && (tiles * d <= 17 * 128 || (4 * groups >= 3 * cus && groups <= cus))) {
     p.waves = 8;
-  } else {
+  } else if (!p.many) {
     // as many workgroups as are resident at once (two a CU), if that leaves few idle; else enough small
     // ones that the dispatcher evens them out
     const int64_t want = static_cast<int64_t>(cus) * 2, fit = want / groups;
@@ -79,7 +79,7 @@ AttnPlan plan_attention(int32_t batch, int64_t total, int32_t max_new, int32_t h
   }
   p.chunk = static_cast<int32_t>((part_tiles + splits - 1) / splits);
   p.splits = static_cast<int32_t>((part_tiles + p.chunk - 1) / p.chunk);
-  p.whole = static_cast<int32_t>(std::min<int64_t>(whole, 0x7fffffff));
+  p.whole = static_cast<int32_t>(std::min<int64_t>(whole, kMostTiles));
   p.part_rows = p.many ? (groups - whole) * tile_rows : total * heads;
   return p;
 }

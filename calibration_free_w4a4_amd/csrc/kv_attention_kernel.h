@@ -1029,7 +1029,7 @@ template <int D, bool FEW> __global__ __launch_bounds__(256) void k_join(const A
 template <int D> int launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   if (p.many) {
     const int64_t tiles = static_cast<int64_t>(a.c.batch) * a.c.heads * a.row_tiles, grid = a.whole + (tiles - a.whole) * a.splits;
-    if (tiles > 0x7fffffff || grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
     const dim3 g(static_cast<uint32_t>(grid)), t(attn::Many<D>::kThreads);
     if constexpr (D > 64) {
       if (p.turned) {
