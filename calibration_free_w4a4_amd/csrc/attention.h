@@ -78,6 +78,7 @@ struct AttnArgs {
   // the launch
   int32_t row_tiles, splits, chunk;  // chunk: 64-key tiles of a split
   int32_t whole;                     // many: the first row tiles in turn, which are not split
+  int32_t first;                     // many: the launch's first workgroup
   float* part_o;                     // [rows][splits][d], splits > 1; rows as AttnPlan::part_rows counts them
   float* part_ml;                    // [rows][splits][2]
   void* turned;                      // AttnPlan::turned: f16 tiles [batch][cache heads][turned_tiles][16 d][8]

@@ -489,7 +489,7 @@ template <int D, bool TURNED = false> struct ManyRows {
     // Row tiles of all streams (sequence, head) in turn, the last rows, which see most under a causal mask, first;
     // from a.whole on each in a.splits parts.  Keeping a stream on one die instead leaves the dies unevenly loaded
     // where sequences differ (the ragged prompts: 142 us, 82 in this order) and gains nothing where they do not.
-    int n = blockIdx.x;
+    int n = a.first + static_cast<int>(blockIdx.x);
     parts = 1;
     split = 0;
     if (n >= a.whole) {
@@ -1030,16 +1030,22 @@ template <int D> int launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream
   if (p.many) {
     const int64_t tiles = static_cast<int64_t>(a.c.batch) * a.c.heads * a.row_tiles, grid = a.whole + (tiles - a.whole) * a.splits;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    const dim3 g(static_cast<uint32_t>(grid)), t(attn::Many<D>::kThreads);
     if constexpr (D > 64) {
-      if (p.turned) {
-        hipLaunchKernelGGL((attn::k_turn<D>), dim3(p.turned, a.c.heads, a.c.batch), dim3(256), 0, stream, a);
-        hipLaunchKernelGGL((attn::k_turned<D>), g, t, 0, stream, a);
-      }
+      if (p.turned) hipLaunchKernelGGL((attn::k_turn<D>), dim3(p.turned, a.c.heads, a.c.batch), dim3(256), 0, stream, a);
     }
-    if (!p.turned) {
-      if constexpr (D <= 128) hipLaunchKernelGGL((attn::k_many<D>), g, t, 0, stream, a);
-      else hipLaunchKernelGGL((attn::k_wide<D>), g, t, 0, stream, a);
+    // a launch takes fewer than 2^32 threads; row tiles come near where a caller bounds ragged sequences loosely
+    constexpr int64_t most = 0xffffffffu / attn::Many<D>::kThreads;
+    for (int64_t first = 0; first < grid; first += most) {
+      AttnArgs s = a;
+      s.first = static_cast<int32_t>(first);
+      const dim3 g(static_cast<uint32_t>(std::min(most, grid - first))), t(attn::Many<D>::kThreads);
+      if constexpr (D > 64) {
+        if (p.turned) hipLaunchKernelGGL((attn::k_turned<D>), g, t, 0, stream, s);
+      }
+      if (!p.turned) {
+        if constexpr (D <= 128) hipLaunchKernelGGL((attn::k_many<D>), g, t, 0, stream, s);
+        else hipLaunchKernelGGL((attn::k_wide<D>), g, t, 0, stream, s);
+      }
     }
   } else {
     const dim3 grid(a.splits, a.c.heads * a.row_tiles, a.c.batch);

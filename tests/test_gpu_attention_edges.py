@@ -96,3 +96,25 @@ def test_no_expected_length(orbq, new):  # noqa: F811
     table, lens = ints(np.arange(300)[None]), ints([38001])
     q, _ = dev(rng.standard_normal((new, 1, 128)), "bf16")
     assert torch.equal(orbq.kv_attention(c, q, table, lens, max_len=0), orbq.kv_attention(c, q, table, lens))
+
+
+@pytest.mark.parametrize("d,batch,heads,kv_heads,each", [(64, 1024, 256, 64, 8), (128, 1024, 256, 64, 8)])
+def test_more_row_tiles_than_one_launch_takes(orbq, d, batch, heads, kv_heads, each):  # noqa: F811
+    """Many short sequences whose bound nobody gave: 2^24 (2^23) row tiles of 256 (512) threads, almost all of them empty."""
+    torch = torch_mod()
+    log(f"loose bound d={d} batch={batch} heads {heads}/{kv_heads}")
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    total = batch * each
+    c = orbq.KVCache.create(batch, kv_heads, d, 16)
+    for t in (c.k_codes, c.v_codes):
+        t.copy_(torch.randint(-127, 128, t.shape, generator=gen, device="cuda", dtype=torch.int8))
+    for t in (c.k_scales, c.v_scales):
+        t.fill_(1 / 40)
+    table = torch.randperm(batch, generator=gen, device="cuda").int()[:, None]
+    lens = torch.randint(each, 17, (batch,), generator=gen, device="cuda", dtype=torch.int32)
+    cu = ints(np.arange(batch + 1) * each)
+    q = torch.randn((total, heads, d), generator=gen, device="cuda").bfloat16()
+    want = orbq.kv_attention(c, q, table, lens, cu=cu, max_new=each, causal_block=1)
+    got = orbq.kv_attention(c, q, table, lens, cu=cu, causal_block=1)
+    assert -(-total * (heads // kv_heads) // (128 if d == 64 else 256)) * batch * kv_heads * (256 if d == 64 else 512) >= 2 ** 32
+    assert (got.float() - want.float()).abs().max().item() <= 2.0 ** -7 * want.float().abs().max().item()
