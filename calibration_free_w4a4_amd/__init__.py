@@ -450,7 +450,7 @@ _ATTENTION = ("Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_read"
 
 
 def __getattr__(name: str):
-    # attention.py needs torch, which this module imports only where a call needs it
+    # attention.py is loaded with the first of its names
     if name in _ATTENTION:
         from . import attention
         for n in _ATTENTION:

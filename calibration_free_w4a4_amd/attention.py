@@ -16,14 +16,25 @@ import functools
 import operator
 import struct
 
-import torch
-
 from . import OrbqError, _check, load
 
 __all__ = ["Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_read", "kv_attention",
            "kv_attention_workspace_bytes"]
 
-_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+# torch comes with the first Rope or KVCache, which every call takes: the package can be imported, with all its names,
+# where there is none.
+torch = None
+_TYPES = {}
+
+
+def _need_torch() -> None:
+    global torch
+    if torch is None:
+        import torch as t
+        _TYPES.update({t.float32: 0, t.bfloat16: 1, t.float16: 2})
+        torch = t
+
+
 LAYOUTS = {"pairs": 0, "halves": 1}  # orbq_rope_layout
 
 # The C structs, packed (a token step's calls are short: building ctypes structures would cost as much as
@@ -86,6 +97,7 @@ class Rope:
     __slots__ = ("_dims", "_freqs", "_layout", "_packed", "_device")
 
     def __init__(self, dims, freqs, layout: str = "pairs"):
+        _need_torch()
         dims = tuple(dims)
         if not 1 <= len(dims) <= 4 or layout not in LAYOUTS:
             raise _bad("Rope", f"{len(dims)} axes (1 to 4), layout {layout!r} (one of {sorted(LAYOUTS)})")
@@ -97,6 +109,7 @@ class Rope:
     @classmethod
     def create(cls, dims, theta: float = 10000.0, layout: str = "pairs", device=None) -> "Rope":
         """Frequencies theta^(-2 i / dims[a]) for pair i of axis a."""
+        _need_torch()
         f = torch.cat([theta ** (-torch.arange(0, d, 2, dtype=torch.float64) / d) for d in dims])
         return cls(tuple(dims), f.float().to(device or torch.device("cuda", torch.cuda.current_device())), layout)
 
@@ -163,6 +176,7 @@ class KVCache:
     __slots__ = ("_k_codes", "_v_codes", "_k_scales", "_v_scales", "_kv_heads", "_page_tokens", "_head_dim", "_packed", "_device")
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        _need_torch()
         if k_codes.dim() != 4:
             raise _bad("KVCache", "k_codes must be [pages, kv_heads, page_tokens, head_dim]")
         n, h, t, d = k_codes.shape
@@ -177,6 +191,7 @@ class KVCache:
 
     @classmethod
     def create(cls, num_pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device=None) -> "KVCache":
+        _need_torch()
         dev = device or torch.device("cuda", torch.cuda.current_device())
         code = lambda *s: torch.empty(s, dtype=torch.int8, device=dev)  # noqa: E731
         scale = lambda: torch.empty((num_pages, kv_heads), dtype=torch.float32, device=dev)  # noqa: E731
@@ -222,9 +237,11 @@ def kv_append(cache: KVCache, k, v, table, start, cu=None, max_new=None) -> None
     _move("kv_append", load().orbq_kv_append, cache, k, v, table, start, cu, max_new)
 
 
-def kv_read(cache: KVCache, table, first, cu, total: int, max_tokens=None, dtype=torch.bfloat16, out=None):
-    """(k, v) [total, kv_heads, head_dim] of tokens first[b] .. of each sequence, cu as in kv_append."""
+def kv_read(cache: KVCache, table, first, cu, total: int, max_tokens=None, dtype=None, out=None):
+    """(k, v) [total, kv_heads, head_dim] of tokens first[b] .. of each sequence, cu as in kv_append.  dtype: of the
+    result (None: torch.bfloat16)."""
     if out is None:
+        dtype = dtype or torch.bfloat16
         k = cache._k_scales.new_empty((total, cache._kv_heads, cache._head_dim), dtype=dtype)
         out = (k, torch.empty_like(k))
     elif out[0].shape[0] != total:

@@ -155,3 +155,15 @@ def test_outputs_whose_rows_overlap_are_refused(tokens, heads, width):
         assert status == (-1 if bad else -2), (ts, hs, status, lib.orbq_last_error())
         some[bad] += 1
     assert all(some)
+
+
+def test_the_package_is_imported_without_torch():
+    """All its names, as before there were any that work on tensors alone."""
+    import subprocess
+    import sys
+    code = ("import sys\nsys.modules['torch'] = None\nfrom calibration_free_w4a4_amd import *\n"
+            "assert callable(rope) and callable(kv_attention) and KVCache and Codebook\n"
+            "assert Codebook.lloyd_max(64, 4).centroids.shape == (16,)")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(orbq.__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
