@@ -9,6 +9,10 @@ package the functions only check and marshal arguments; the work is liborbq's HI
     o = kv_attention(cache, q, table, lens, causal_block=tokens_a_frame)
 
 Head tensors are [tokens, heads, head_dim] with the last dimension contiguous.
+
+Gradients: rope and rope_backward are part of the autograd graph (positions and frequencies are constants).  There is no
+gradient through the cache, whose entries are rounded: a backward pass that reaches kv_attention's output raises.  A call
+that is given `out` writes it and records nothing.
 """
 from __future__ import annotations
 
@@ -25,14 +29,49 @@ __all__ = ["Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_read", "
 # where there is none.
 torch = None
 _TYPES = {}
+_Turned = _Attended = None  # autograd functions of rope and kv_attention
 
 
 def _need_torch() -> None:
-    global torch
-    if torch is None:
-        import torch as t
-        _TYPES.update({t.float32: 0, t.bfloat16: 1, t.float16: 2})
-        torch = t
+    global torch, _Turned, _Attended
+    if torch is not None:
+        return
+    import torch as t
+
+    class Turned(t.autograd.Function):
+        """The map is linear and orthogonal: its gradient is the inverse turn, whose gradient is the turn again."""
+        @staticmethod
+        def forward(ctx, func, rope, positions, q, k, inverse):
+            ctx.func, ctx.rope, ctx.inverse = func, rope, inverse
+            ctx.save_for_backward(positions)
+            ctx.set_materialize_grads(False)
+            return _turn(func, rope, positions, q, k, inverse, None)
+
+        @staticmethod
+        def backward(ctx, *dy):
+            positions, = ctx.saved_tensors
+            # the gradients that are there and asked for, in one launch; an expanded one has no contiguous last dimension
+            some = [i for i, g in enumerate(dy) if g is not None and ctx.needs_input_grad[3 + i]]
+            dx = [None, None]
+            if some:
+                dy = [dy[i] if dy[i].stride(-1) == 1 else dy[i].contiguous() for i in some]
+                got = _turn(ctx.func, ctx.rope, positions, dy[0], dy[1] if len(dy) > 1 else None, 1 - ctx.inverse, None)
+                for i, g in zip(some, got if len(some) > 1 else (got,)):
+                    dx[i] = g
+            return None, None, None, *dx, None
+
+    class Attended(t.autograd.Function):
+        @staticmethod
+        def forward(ctx, cache, q, *args):
+            return kv_attention(cache, q, *args)
+
+        @staticmethod
+        def backward(ctx, do):
+            raise _bad("kv_attention", "there is no gradient through the 8-bit cache")
+
+    _TYPES.update({t.float32: 0, t.bfloat16: 1, t.float16: 2})
+    _Turned, _Attended = Turned, Attended
+    torch = t
 
 
 LAYOUTS = {"pairs": 0, "halves": 1}  # orbq_rope_layout
@@ -126,6 +165,8 @@ def _written(x, y, func: str):
 
 
 def _turn(func, rope, positions, q, k, inverse, out):
+    if out is None and (q.requires_grad or (k is not None and k.requires_grad)) and torch.is_grad_enabled():
+        return _Turned.apply(func, rope, positions, q, k, inverse)      # which comes back here, recording nothing
     if _current() != rope._device:
         with torch.cuda.device(rope._device):
             return _turn(func, rope, positions, q, k, inverse, out)
@@ -272,6 +313,8 @@ def kv_attention(cache: KVCache, q, table, lens, cu=None, max_new=None, causal_b
     1 / sqrt(head_dim) if None.  lse: float32 [total, heads] to receive the logarithms of the sums.
     max_len: expected bound of lens (None or 0: what the table holds); it only guides how the work is split."""
     func = "kv_attention"
+    if q.requires_grad and out is None and torch.is_grad_enabled():
+        return _Attended.apply(cache, q, table, lens, cu, max_new, causal_block, window, scale, max_len, out, lse, workspace)
     if _current() != cache._device:
         with torch.cuda.device(cache._device):
             return kv_attention(cache, q, table, lens, cu, max_new, causal_block, window, scale, max_len, out, lse, workspace)

@@ -118,3 +118,60 @@ def test_more_row_tiles_than_one_launch_takes(orbq, d, batch, heads, kv_heads, e
     got = orbq.kv_attention(c, q, table, lens, cu=cu, causal_block=1)
     assert -(-total * (heads // kv_heads) // (128 if d == 64 else 256)) * batch * kv_heads * (256 if d == 64 else 512) >= 2 ** 32
     assert (got.float() - want.float()).abs().max().item() <= 2.0 ** -7 * want.float().abs().max().item()
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("layout", ["pairs", "halves"])
+def test_rope_is_in_the_autograd_graph(orbq, name, layout):  # noqa: F811
+    """Its gradients are rope_backward's, whichever inputs ask for them and however the incoming ones lie."""
+    torch = torch_mod()
+    log(f"autograd {name} {layout}")
+    rng = np.random.default_rng(2)
+    r = orbq.Rope.create((16, 24, 24), layout=layout)
+    p, _ = dev(rng.integers(0, 60, (31, 3)))
+    q, k, gq, gk = (dev(rng.standard_normal((31, h, 72)), name)[0] for h in (6, 2, 6, 2))
+    want = orbq.rope(r, p, q, k)
+    back = orbq.rope_backward(r, p, gq, gk)
+    q.requires_grad_(True)
+    k.requires_grad_(True)
+    y = orbq.rope(r, p, q, k)
+    assert all(torch.equal(a, b) and a.requires_grad for a, b in zip(y, want))
+    assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(y, (q, k), (gq, gk)), back))
+    # one output's gradient alone, one input alone, one tensor alone
+    y = orbq.rope(r, p, q, k)
+    dq, dk = torch.autograd.grad(y[1], (q, k), gk, allow_unused=True)
+    assert dq is None and torch.equal(dk, back[1])
+    y = orbq.rope(r, p, q.detach(), k)
+    assert torch.equal(torch.autograd.grad(y, k, (gq, gk))[0], back[1])
+    assert torch.equal(torch.autograd.grad(orbq.rope(r, p, q), q, gq)[0], back[0])
+    # an expanded gradient, whose last dimension has no stride
+    ones = torch.ones_like(gq)
+    assert torch.equal(torch.autograd.grad(orbq.rope(r, p, q).sum(), q)[0], orbq.rope_backward(r, p, ones))
+    # the gradient's gradient is the turn again
+    v = gq.clone().requires_grad_(True)
+    dq, = torch.autograd.grad(orbq.rope(r, p, q), q, v, create_graph=True)
+    assert torch.equal(torch.autograd.grad(dq, v, gq)[0], orbq.rope(r, p, gq))
+    # nothing is recorded where nothing is asked for
+    with torch.no_grad():
+        assert not orbq.rope(r, p, q).requires_grad
+    out = torch.empty_like(gq)
+    assert orbq.rope(r, p, q, out=out) is out and not out.requires_grad and torch.equal(out, want[0])
+
+
+def test_a_gradient_through_the_cache_is_refused(orbq):  # noqa: F811
+    """Not lost without a word: the output is in the graph, and a backward pass that reaches it raises."""
+    torch = torch_mod()
+    rng = np.random.default_rng(3)
+    c = cache_of(orbq, rng, 4, 2, 64, 16)
+    table, lens = ints([[0, 1, 3]]), ints([40])
+    q, _ = dev(rng.standard_normal((5, 4, 64)), "bf16")
+    want = orbq.kv_attention(c, q, table, lens, causal_block=1)
+    q.requires_grad_(True)
+    o = orbq.kv_attention(c, q, table, lens, causal_block=1)
+    assert torch.equal(o, want) and o.requires_grad
+    with pytest.raises(orbq.OrbqError):
+        o.sum().backward()
+    with torch.no_grad():
+        assert not orbq.kv_attention(c, q, table, lens, causal_block=1).requires_grad
+    out = torch.empty_like(want)
+    assert orbq.kv_attention(c, q, table, lens, causal_block=1, out=out) is out and not out.requires_grad and torch.equal(out, want)
