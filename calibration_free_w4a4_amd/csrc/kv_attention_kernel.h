@@ -5,16 +5,19 @@
 //   k_j = kc_j ks[block of j],  v_j = vc_j vs[block of j].
 //
 // Both products run on the matrix cores in f16 with fp32 accumulation, on the codes themselves: a
-// code is exact in f16, q enters as q 2^-e with 2^e its row's magnitude (exact for f16 input and, but
-// for entries below 2^-14 of the row's largest, for bf16), and the key scale joins the softmax's
+// code is exact in f16, q enters as q 2^-e with 2^e its row's magnitude (exact but for entries below
+// 2^-14 of the row's largest, which are rounded by 2^-25 of it at most), and the key scale joins the softmax's
 // own factor.  The value scale goes into the exponent:
 //   w_j = exp2(S_j log2(e) + log2(vs_j) - m),  m the running maximum of S_j log2(e) + log2(vs_j),
 //   O = sum_j w_j vc_j / l,  l = sum over blocks (1/vs) sum_j w_j,
 // so no element is multiplied by a scale and the rounding of w to f16 is relative to the row's largest
-// weight whatever the scales are.  m, l and O are fp32.  m may lag behind the true maximum by up
-// to 2^kSlack (w stays below the f16 limit), which saves most of the rescaling of O.
+// weight whatever the scales are.  m, l and O are fp32.  m may lag behind the true maximum, which saves most of the
+// rescaling of O: it is set 2^kRise below the largest weight and set again when a weight passes 2^kSlack.  What f16
+// holds above that is used for the small ones: a weight is rounded by half a unit of its 11 bits or, below 2^-14, by
+// 2^-25, which is 2^-28 of the row's largest or less (with m at the maximum itself it would be 2^-25: 60000 keys at
+// 2^-25.4 of one large one were lost altogether, and now lose 1 % of their share).
 // The exponent is one fused operation on the raw score and log2(vs_j) - m, both rounded apart: a relative error of
-// 2^-24 of the score each, which the row's sum shares.  With scores to 2^25 it adds 4 to the 8 of kSlack at most, and
+// 2^-24 of the score each, which the row's sum shares.  With scores to 2^25 it adds 4 to the 11 of kSlack at most, and
 // w stays within f16 (2^16); subtracting rounded scores instead would need no such limit and one more
 // instruction for each weight.
 //
@@ -47,7 +50,8 @@
 namespace orbq {
 namespace attn {
 
-constexpr float kSlack = 8.0f;       // log2 by which a weight may pass 1 before O is rescaled
+constexpr float kSlack = 11.0f;      // log2 of what a weight may reach before O is rescaled
+constexpr float kRise = 3.0f;        // log2 of the largest weight then
 constexpr float kNone = -1.0e30f;    // running maximum before the first visible key
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -327,7 +331,7 @@ template <int D, int RT, int NW> __global__ __launch_bounds__(64 * NW) void k_fe
       top = __builtin_fmaf(top, c, lv);
       top = max_over32(max_over16(top));
       if (__any(top > m[rt] + kSlack)) {
-        const float mn = __builtin_fmaxf(m[rt], top), by = exp2_fast(m[rt] - mn);
+        const float mn = __builtin_fmaxf(m[rt], top - kRise), by = exp2_fast(m[rt] - mn);
         m[rt] = mn;
         l[rt] *= by;
 #pragma unroll
@@ -708,7 +712,7 @@ template <int D, bool TURNED = false> struct ManyRows {
   }
   __device__ __forceinline__ void raise(float top) {
     if (__any(top > m + kSlack)) {
-      const float mn = __builtin_fmaxf(m, top), by = exp2_fast(m - mn);
+      const float mn = __builtin_fmaxf(m, top - kRise), by = exp2_fast(m - mn);
       m = mn;
       l *= by;
 #pragma unroll

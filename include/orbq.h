@@ -380,7 +380,10 @@ int orbq_kv_read(const orbq_kv_cache* cache, const orbq_page_table* table, const
  *   lens  [device] int32[batch], tokens held (kept inside [0, max_pages * page_tokens])
  *   q, o  [device] head tensors of `total` packed rows and `heads` heads, bf16 or f16; heads a multiple of
  *         kv_heads, query head h reads cache head h / (heads / kv_heads).  q 16-byte, o 8-byte addresses
- *         and strides.  Products on the codes in f16 with fp32 accumulation, softmax in fp32.
+ *         and strides.  Products on the codes in f16 with fp32 accumulation, softmax in fp32.  Rounded to f16 are
+ *         q (exact but for entries below 2^-14 of their row's largest, which are rounded by 2^-25 of it at most)
+ *         and, after their sum was taken, the softmax's weights times their value's scale: to 11 bits, and those
+ *         below 2^-17 of the row's largest by at most 2^-28 of it, so n such keys lose at most n 2^-28 of it.
  *         Scores scale q . k are taken up to 2^25 in magnitude; a row with larger ones may be not finite.
  *   lse   [device] float[total][heads] or NULL: natural log of the sum of exponentials
  *   max_new  bound of the queries of a sequence;  max_len  expected bound of lens (0: the page table's);

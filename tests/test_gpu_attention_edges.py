@@ -1,5 +1,7 @@
 """Calls at the edges of what the attention-side operators take: bounds below the counts, positions outside the
 sequence, bounds far above the work."""
+import math
+
 import numpy as np
 import pytest
 
@@ -175,3 +177,41 @@ def test_a_gradient_through_the_cache_is_refused(orbq):  # noqa: F811
         assert not orbq.kv_attention(c, q, table, lens, causal_block=1).requires_grad
     out = torch.empty_like(want)
     assert orbq.kv_attention(c, q, table, lens, causal_block=1, out=out) is out and not out.requires_grad and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("d,batch,heads,kv_heads,new,n,unbound", [
+    (64, 64, 16, 16, 1, 12000, False), (128, 64, 16, 16, 1, 12000, False), (256, 64, 16, 16, 1, 12000, False),
+    (64, 32, 1280, 32, 1, 12000, False), (128, 32, 1280, 32, 1, 12000, False),
+    (64, 1, 64, 1, 1536, 60000, False), (128, 1, 64, 1, 1024, 60000, True), (128, 1, 64, 1, 1024, 60000, False),
+    (256, 1, 64, 1, 512, 60000, True), (256, 1, 64, 1, 512, 60000, False)])
+def test_many_small_weights_beside_a_large_one(orbq, d, batch, heads, kv_heads, new, n, unbound):  # noqa: F811
+    """One key in the first tile of each wave takes nearly all the weight, with a value of zero; all others have 2^-25.4 of it
+    and a value of one.  A weight is rounded by 2^-28 of the largest at most, so n of them lose n 2^-28 of it."""
+    torch = torch_mod()
+    page = 64
+    pages = -(-n // page)
+    few = new * heads // kv_heads <= 64
+    tiles = 4 if few else 1                  # the first tiles of the waves; a workgroup of the few-row form has four of them
+    log(f"small weights d={d} {'few' if few else 'many'} unbound {unbound}")
+    c = orbq.KVCache.create(pages, kv_heads, d, page)
+    c.k_codes.zero_()
+    c.v_codes.fill_(127)
+    c.k_codes[:tiles, :, 0, 0] = 127
+    c.v_codes[:tiles, :, :, 0] = 0
+    c.k_scales.fill_(1 / 127)
+    c.v_scales.fill_(1 / 127)
+    table = ints(np.tile(np.arange(pages), (batch, 1)))
+    q = torch.zeros((batch * new, heads, d), dtype=torch.float16, device="cuda")
+    q[:, :, 0] = 16.0
+    bits = 25.4
+    ks = float(np.float32(1 / 127)) * 127
+    scale = float(np.float32(bits * math.log(2) / (16 * ks)))
+    w = math.exp(-scale * 16 * ks)
+    want = (n - tiles) * w / (tiles + (n - tiles) * w)
+    # nothing is split: the workspace has room for turned tiles alone
+    assert orbq.kv_attention_workspace_bytes(c, batch, batch * new, new, heads, pages * page) == (0 if few or d == 64 else
+                                                                                                   pages * (256 * d + 64))
+    o = orbq.kv_attention(c, q, table, ints([n] * batch), scale=scale, max_len=n if unbound else None).double()
+    tol = (n - tiles) * 2.0 ** -28 / tiles + 2.0 ** -9 * want + 2.0 ** -25
+    assert tol < want / 2
+    assert (o - want).abs().max().item() <= tol, ((o - want).abs().max().item(), want, tol)
