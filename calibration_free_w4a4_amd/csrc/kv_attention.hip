@@ -14,17 +14,18 @@ AttnPlan plan_attention(int32_t batch, int64_t total, int32_t max_new, int32_t h
   AttnPlan p{};
   const int64_t rows = static_cast<int64_t>(max_new) * (heads / kv_heads);
   // The few-row form reads the cache once for each of its row tiles.  For 17 to 32 rows two single tiles beat
-  // one double one while the second reading finds the cache on the card (60000 tokens of 8 heads of 128, 123 MB:
-  // 36 us against 42; 2000 of 64: 10 against 14) and lose beyond (262157 of 8 heads of 64, 268 MB: 78 against
-  // 60).  Above 32 rows double tiles win (64 rows over 60000 tokens: 53 against 55, heads of 64 31 against 35) and
-  // beat the many-row form up to 64 rows (82); with heads of 256 a double tile's registers spill, and the many-row
-  // form takes over at 33 rows.
+  // one double one while the second reading finds the cache on the card, and lose beyond (32 rows, 8 heads of 128: 61 MB
+  // of cache 29 us against 35, 102 MB 40 and 45, 123 MB 47 and 48, 150 MB 55 and 52, 268 MB 85 and 73; heads of 64, whose
+  // tiles cost less, are even at 61 MB, and 123 MB takes 43 and 37).  Above 32 rows double tiles win (64 rows over
+  // 60000 tokens: 53 against 55, heads of 64 31 against 35) and beat the many-row form up to 64 rows (82); with heads of
+  // 256 a double tile's registers spill, and the many-row form takes over at 33 rows.
   const double cached = 2.0 * max_len * batch * kv_heads * d;
   p.many = rows > (d == 256 ? 32 : 64);
   p.rt = d < 256 && (rows > 32 || (rows > 16 && cached > 0x1p27)) ? 2 : 1;
   const int tile_rows = p.many ? many_rows(d) : 16 * p.rt;
   p.row_tiles = static_cast<int32_t>((rows + tile_rows - 1) / tile_rows);
-  // the keys that one row tile can see, in 64-key tiles
+  // the keys that the rows of one stream can see together, in 64-key tiles: under a window more than one row tile sees,
+  // so that the splits of a windowed call are longer than they need be and the last ones have nothing
   int64_t span = max_len;
   if (window) span = std::min<int64_t>(span, static_cast<int64_t>(window) + max_new + causal_block);
   const int64_t tiles = std::max<int64_t>(1, (span + 63) / 64 + (window ? 1 : 0));
@@ -69,6 +70,10 @@ AttnPlan plan_attention(int32_t batch, int64_t total, int32_t max_new, int32_t h
     if (bound && d > 64 && readers >= 8 && static_cast<int64_t>(batch) * kv_heads * tiles * d <= (int64_t{1} << 22))
       p.turned = static_cast<int32_t>(tiles);  // at most 1 GiB of workspace
   } else if (!p.many && p.rt == 1 && d <= 128 && (tiles * d <= 17 * 128 || (4 * groups >= 3 * cus && groups <= cus))) {
+    // Eight waves and no join, where the keys are few or where one such workgroup a CU fills the card without a second
+    // round.  12 streams of heads of 128: 500 tokens 9.2 us against 10.2 with four waves and split keys, 1088 (17 tiles)
+    // 12.2 and 12.3, 1400 14.4 and 13.1; of heads of 64: 2000 10.3 and 11.4, 2176 10.6 and 9.0.
+    // 12000 tokens of heads of 128: 96 streams 90 and 66, 192 107 and 126, 256 141 and 153, 264 207 and 169.
     p.waves = 8;
   } else if (!p.many) {
     // as many workgroups as are resident at once (two a CU), if that leaves few idle; else enough small
