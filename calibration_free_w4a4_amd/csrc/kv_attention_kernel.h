@@ -36,10 +36,10 @@
 // Either splits the keys over workgroups, few where there are few rows, many where the last round of workgroups
 // would leave CUs idle; k_join joins the parts.
 //
-// Measured: few, one token of 48 sequences to 16384 long, 32 / 8 heads of 128: 170 us, 5.0 TB/s of cache; 4 tokens
-// over 262157, 64 / 8 heads of 64: 52 us, 5.2 TB/s, and 6 us of joining.  many, 4680 queries over 32760 tokens, 12
-// heads of 128: 0.96 ms, 0.94 PFLOP/s (a library f16 product of 8192^3 on the same card: 1.20); heads of 256,
-// 2 x 4605 queries that all see all: 437 us, 0.79 PFLOP/s; heads of 64, ragged prompts with a window of 1024: 83 us,
+// Measured: few, one token of 48 sequences to 16384 long, 32 / 8 heads of 128: 169 us and 6 of joining, 5.1 TB/s of
+// cache; 4 tokens over 262157, 64 / 8 heads of 64: 60 us, 6 of them joining, 4.5 TB/s.  many, 4680 queries over 32760
+// tokens, 12 heads of 128: 0.94 ms, 0.95 PFLOP/s (a library f16 product of 8192^3 on such a card: 1.20); heads of 256,
+// 2 x 4605 queries that all see all: 444 us, 0.78 PFLOP/s; heads of 64, ragged prompts with a window of 1024: 83 us,
 // 0.43 PFLOP/s.
 #pragma once
 

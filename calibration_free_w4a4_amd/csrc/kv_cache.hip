@@ -17,7 +17,7 @@
 // One workgroup for each (touched page, head, keys or values): it holds the page's new values in
 // registers between the maximum and the quantisation, so every byte crosses HBM once, and no two
 // workgroups write the same page (no atomics; the result does not depend on any order).  4680 tokens of 12 heads
-// of 128 in bf16: append 10.7 us (29 MB in, 14 out), read 9.2 us; the quantisation's vector work and the chain of
+// of 128 in bf16: append 10.7 us (29 MB in, 14 out), read 9.5 us; the quantisation's vector work and the chain of
 // dependent reads (counts, table, scale) keep it from the memory's rate.  One token for 48 sequences of 8
 // heads: 7 us each, latency alone.
 #include <type_traits>

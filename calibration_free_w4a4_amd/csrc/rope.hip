@@ -6,8 +6,8 @@
 // Each element is read once and written once, so the call is bound by HBM bytes.  A thread owns
 // one 16-byte column of a head row (two columns in the split-half order, whose pairs lie
 // half a rotary width apart) for one token, finds the columns' sines and cosines once and goes over
-// `per` heads with them, q's heads first, then k's.  32760 tokens, 12 + 12 heads of 128 in bf16: 82 us, 4.9 TB/s
-// (a large copy on the same card: 4.7); 4605 tokens, 24 + 8 heads in f32: 25 us; one token: 3.5 us.
+// `per` heads with them, q's heads first, then k's.  32760 tokens, 12 + 12 heads of 128 in bf16: 84 us, 4.8 TB/s
+// (a large copy on the same card: 4.7); 4605 tokens, 24 + 8 heads in f32: 26 us; one token: 3.5 us.
 //
 // Angles: the product is exact in 64 bits (24 + 24 bits of the factors), is turned into
 // revolutions and loses its whole turns there, so that a position far along an axis is as exact

@@ -6,7 +6,8 @@ over it.  Each step takes the tokens of some new frames; every token sees its ow
     python examples/streaming_video_attention.py --frames 6 --chunk 2 --height 8 --width 12
 
 Weights and activations are random (this repository has no trained ones); the sizes are those of the
-video layers in workloads/.
+video layers in workloads/.  The normalisation of q and k that such layers have before the rotary
+positions is left out.
 """
 from __future__ import annotations
 

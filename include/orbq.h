@@ -271,7 +271,8 @@ int32_t orbq_rht_passes(float rho3, float rhoinf, int32_t d, int32_t vector_quan
 
 /* ==== attention-side operators ================================================================
  * What a transformer block has between its quantized QKV projection and its quantized output
- * projection: rotary positions over several axes, a key/value cache in 8 bits, attention over it.
+ * projection (but for a normalisation of q and k, where a model has one): rotary positions over
+ * several axes, a key/value cache in 8 bits, attention over it.
  *
  * Head tensors are [token][head][head_dim] with the last dimension contiguous and any
  * non-negative token and head strides (in elements), so the parts of a fused projection are taken
@@ -373,7 +374,8 @@ int orbq_kv_read(const orbq_kv_cache* cache, const orbq_page_table* table, const
  * position) stands at position lens[b] - n + i, so the cache holds the queries' own tokens already
  * (orbq_kv_append first).  Visible are tokens lo <= j < hi:
  *   hi = lens[b] with causal_block = 0; else min(lens[b], (position / causal_block + 1) * causal_block), and 0 at
- *        a negative position (1: causal; tokens a frame: each frame sees itself and earlier ones)
+ *        a negative position (1: causal; tokens a frame: each frame sees itself and earlier ones; blocks count
+ *        from token 0 of the sequence)
  *   lo = max(0, hi - window), or 0 with window = 0
  * A query that sees nothing gets O = 0, lse = -infinity.  Tokens that are not visible have no influence,
  * whatever their codes and scales hold.
