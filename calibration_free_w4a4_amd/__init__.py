@@ -269,6 +269,15 @@ def rpbh_quantize(X, rot: Rotation, cb: Codebook, eps: float = 1e-8, out_codes=N
     return codes, norms
 
 
+def _y_type(torch, Y) -> int:
+    """The type of a product's output, which the kernels write as fp32 or bf16."""
+    if Y.dtype == torch.bfloat16:
+        return BF16
+    if Y.dtype == torch.float32:
+        return F32
+    raise OrbqError(-1, "out", f"the output must be float32 or bfloat16, got {Y.dtype}")
+
+
 ACTIVATIONS = {"none": 0, "gelu_tanh": 1, "gelu_erf": 2}   # orbq_activation
 
 
@@ -288,7 +297,7 @@ def lut_gemm(x_codes, x_norms, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook,
     n, m = x_codes.shape[0], w_codes.shape[0]
     Y = out if out is not None else torch.empty((n, m), dtype=out_dtype, device=x_codes.device)
     a, w = cb_a.struct(), cb_w.struct()
-    yt = BF16 if Y.dtype == torch.bfloat16 else F32
+    yt = _y_type(torch, Y)
     code = _act(act)
     if code == 0:
         _check(load().orbq_lut_gemm(x_codes.data_ptr(), x_norms.data_ptr(), ctypes.byref(a), w_codes.data_ptr(),
@@ -316,7 +325,7 @@ def linear(X, rot: Rotation, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook, e
         workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=X.device)
     Y = out if out is not None else torch.empty((n, m), dtype=out_dtype, device=X.device)
     r, a, w = rot.struct(), cb_a.struct(), cb_w.struct()
-    yt = BF16 if Y.dtype == torch.bfloat16 else F32
+    yt = _y_type(torch, Y)
     ws_bytes = workspace.numel() * workspace.element_size()
     code = _act(act)
     if code == 0:
@@ -347,7 +356,7 @@ def linear_noalloc(X, rot: Rotation, cb_a: Codebook, w_codes, w_norms, cb_w: Cod
     m = w_codes.shape[0]
     Y = out if out is not None else torch.empty((n, m), dtype=out_dtype, device=X.device)
     r, a, w = rot.struct(), cb_a.struct(), cb_w.struct()
-    yt = BF16 if Y.dtype == torch.bfloat16 else F32
+    yt = _y_type(torch, Y)
     _check(load().orbq_linear_noalloc(X.data_ptr(), n, d, X.stride(0), ctypes.byref(r), ctypes.byref(a), eps,
                                       w_codes.data_ptr(), w_norms.data_ptr(), ctypes.byref(w), m, _act(act),
                                       Y.data_ptr(), yt, Y.stride(0), _stream(torch, X.device)), "orbq_linear_noalloc")
@@ -377,7 +386,7 @@ def linear_a16(X, rot: Rotation, w_codes, w_norms, cb_w: Codebook, out_dtype=Non
     _check(load().orbq_linear_a16(X.data_ptr(), n, d, X.stride(0), ctypes.byref(r), w_codes.data_ptr(),
                                   w_norms.data_ptr(), ctypes.byref(w), m, workspace.data_ptr(),
                                   workspace.numel() * workspace.element_size(), Y.data_ptr(),
-                                  BF16 if Y.dtype == torch.bfloat16 else F32, Y.stride(0), _stream(torch, X.device)),
+                                  _y_type(torch, Y), Y.stride(0), _stream(torch, X.device)),
            "orbq_linear_a16")
     return Y
 

@@ -167,3 +167,24 @@ def test_the_package_is_imported_without_torch():
     root = os.path.dirname(os.path.dirname(os.path.abspath(orbq.__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_products_refuse_outputs_of_other_types(two_devices):
+    """Narrower ones would be written beyond their end."""
+    import numpy as np
+    import torch
+    x = lambda *s, dtype=torch.bfloat16: Elsewhere(torch.zeros(s, dtype=dtype))  # noqa: E731
+    rot = orbq.Rotation(64, 64, None, torch.zeros(64, dtype=torch.int8))
+    cb = orbq.Codebook.from_centroids(64, 4, np.arange(16) - 7.5)
+    X, codes, norms, ws = x(2, 64), x(2, 32, dtype=torch.uint8), x(2, dtype=torch.float32), x(512, dtype=torch.uint8)
+    calls = [lambda **kw: orbq.lut_gemm(codes, norms, cb, codes, norms, cb, 64, **kw),
+             lambda **kw: orbq.linear(X, rot, cb, codes, norms, cb, workspace=ws, **kw),
+             lambda **kw: orbq.linear_noalloc(X, rot, cb, codes, norms, cb, **kw),
+             lambda **kw: orbq.linear_a16(X, rot, codes, norms, cb, workspace=ws, **kw)]
+    for call in calls:
+        for kw in (dict(out_dtype=torch.float16), dict(out=x(2, 2, dtype=torch.float16)), dict(out=x(2, 2, dtype=torch.int8))):
+            with pytest.raises(orbq.OrbqError):
+                call(**kw)
+        for dt in (torch.float32, torch.bfloat16):
+            assert call(out_dtype=dt).dtype == dt
+    assert not [n for n, _ in two_devices if not n.endswith("bytes")][8:]
