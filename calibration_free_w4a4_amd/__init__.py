@@ -11,7 +11,8 @@ library is not built or no GPU is present the calls raise.
     Y = linear(X, rot, cb_a, w_codes, w_norms, cb_w)    # online
 
 The attention-side operators (rotary positions, the 8-bit key/value cache, attention over it) are in
-attention.py and reached from here as well: orbq.rope, orbq.kv_append, orbq.kv_attention, ...
+attention.py, the norms around a block in block.py; both are reached from here as well: orbq.rope, orbq.kv_append,
+orbq.kv_attention, orbq.block_norm, ...
 """
 from __future__ import annotations
 
@@ -28,6 +29,7 @@ __all__ = [
     "test_mfma_rate",
     "F32", "BF16",
     "Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_read", "kv_attention", "kv_attention_workspace_bytes",
+    "block_norm", "block_norm_backward", "NormGrads",
 ]
 
 F32, BF16 = 0, 1
@@ -92,6 +94,10 @@ _SIGS = {
     "orbq_kv_attention_workspace_bytes": (ctypes.c_size_t, [_P, _I32, _I64, _I32, _I32, _I64, _I32, _I32]),
     "orbq_kv_attention": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _I64, _P, _I64, _I64, _I32, _P, _I64, _I64, _P,
                                          ctypes.c_int, _F, _I32, _I32, _P, ctypes.c_size_t, _P]),
+    "orbq_block_norm": (ctypes.c_int, [_P, _I64, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, ctypes.c_int, ctypes.c_int, _P]),
+    "orbq_block_norm_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I32, _I32]),
+    "orbq_block_norm_backward": (ctypes.c_int, [_P, _I64, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
+                                                ctypes.c_int, ctypes.c_int, _P, ctypes.c_size_t, _P]),
     "orbq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "orbq_last_error": (ctypes.c_char_p, []),
     "orbq_test_rotate": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(_Rpbh), _P, _P, _P]),
@@ -453,16 +459,24 @@ def test_mfma_rate(workgroups: int, iters: int, sink=None, device=None) -> float
     return flops.value
 
 
-# ------------------------------------------------------------------------ the attention-side operators
+# ------------------------------------------- the attention-side operators and the norms around a block
 _ATTENTION = ("Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_read", "kv_attention",
               "kv_attention_workspace_bytes")
 
 
+_BLOCK = ("block_norm", "block_norm_backward", "NormGrads")
+
+
 def __getattr__(name: str):
-    # attention.py is loaded with the first of its names
+    # attention.py and block.py are loaded with the first of their names
     if name in _ATTENTION:
         from . import attention
         for n in _ATTENTION:
             globals()[n] = getattr(attention, n)
+        return globals()[name]
+    if name in _BLOCK:
+        from . import block
+        for n in _BLOCK:
+            globals()[n] = getattr(block, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

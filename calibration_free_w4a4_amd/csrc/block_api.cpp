@@ -1,0 +1,203 @@
+// C ABI of a block's operators beside its products and its attention (declared and documented in include/orbq.h):
+// argument checks on the host, then asynchronous launches.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "../../include/orbq.h"
+#include "block_norm.h"
+#include "internal.h"
+
+#define ORBQ_API extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+using orbq::set_error;
+using orbq::set_ok;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int hip_status(int e, const char* what) {
+  if (e != hipSuccess) return set_error(ORBQ_ERR_HIP, "%s: %s", what, hipGetErrorString(static_cast<hipError_t>(e)));
+  return set_ok();
+}
+
+bool known_type(int t) { return t == ORBQ_F32 || t == ORBQ_BF16 || t == ORBQ_F16; }
+bool known_norm(int k) { return k == ORBQ_NORM_NONE || k == ORBQ_NORM_LAYER || k == ORBQ_NORM_RMS; }
+
+// Whether 16-byte columns of 8 entries fit the rows at p; NULL fits.
+bool fits(const void* p, int64_t ld, int size) { return !p || (aligned(p, 16) && ld * size % 16 == 0); }
+
+// rows of d entries of `size` bytes, `ld` apart; shared: one row is meant by 0
+int check_rows(const void* p, int64_t ld, int64_t rows, int32_t d, int size, bool written, const char* name, const char* what) {
+  if (!p) return ORBQ_OK;
+  if (ld < 0) return set_error(ORBQ_ERR_INVALID_ARG, "%s: negative stride of %s", what, name);
+  if (!aligned(p, size)) return set_error(ORBQ_ERR_ALIGNMENT, "%s: %s misaligned", what, name);
+  if (written && rows > 1 && ld < d) return set_error(ORBQ_ERR_INVALID_ARG, "%s: rows of %s overlap", what, name);
+  return ORBQ_OK;
+}
+
+int check_norms(const orbq_norms* p, int64_t n, int32_t d, bool branch, int stream_type, int branch_type, orbq::NormArgs* a,
+                const char* what) {
+  int s;
+  if (!p) return set_error(ORBQ_ERR_INVALID_ARG, "%s: norms are NULL", what);
+  if (!known_norm(p->norm) || !known_norm(p->post))
+    return set_error(ORBQ_ERR_INVALID_ARG, "%s: norm %d, post %d", what, static_cast<int>(p->norm), static_cast<int>(p->post));
+  if (!known_type(stream_type) || !known_type(branch_type) || !known_type(p->weight_type) || !known_type(p->mod_type))
+    return set_error(ORBQ_ERR_INVALID_ARG, "%s: unknown type", what);
+  if (stream_type != branch_type && stream_type != ORBQ_F32)
+    return set_error(ORBQ_ERR_UNSUPPORTED, "%s: a stream of 16 bits with a branch of another type", what);
+  if (n < 0 || d < 1) return set_error(ORBQ_ERR_INVALID_ARG, "%s: n %lld, d %d", what, static_cast<long long>(n), d);
+  if (d > 16384) return set_error(ORBQ_ERR_UNSUPPORTED, "%s: d %d above 16384", what, d);
+  if (n > (int64_t{1} << 30)) return set_error(ORBQ_ERR_UNSUPPORTED, "%s: more than 2^30 rows", what);
+  if (p->groups < 1) return set_error(ORBQ_ERR_INVALID_ARG, "%s: %d groups", what, p->groups);
+  if (p->groups > (1 << 30)) return set_error(ORBQ_ERR_UNSUPPORTED, "%s: more than 2^30 groups", what);
+  if (!p->cu && n % p->groups) return set_error(ORBQ_ERR_INVALID_ARG, "%s: without cu every group has n / groups rows", what);
+  if (!aligned(p->cu, 4)) return set_error(ORBQ_ERR_ALIGNMENT, "%s: cu misaligned", what);
+  if (!(p->eps >= 0.0f) || !std::isfinite(p->eps) || !(p->post_eps >= 0.0f) || !std::isfinite(p->post_eps))
+    return set_error(ORBQ_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", what);
+  if (p->norm == ORBQ_NORM_NONE && (p->weight || p->scale || p->shift))
+    return set_error(ORBQ_ERR_INVALID_ARG, "%s: weight, scale or shift without a norm", what);
+  if (p->post == ORBQ_NORM_NONE && p->post_weight) return set_error(ORBQ_ERR_INVALID_ARG, "%s: post_weight without post", what);
+  if (!branch && (p->gate || p->post != ORBQ_NORM_NONE))
+    return set_error(ORBQ_ERR_INVALID_ARG, "%s: gate or post without y", what);
+  if (!branch && p->norm == ORBQ_NORM_NONE) return set_error(ORBQ_ERR_INVALID_ARG, "%s: neither y nor a norm", what);
+  const int wsize = orbq::dtype_size(p->weight_type), msize = orbq::dtype_size(p->mod_type);
+  if ((s = check_rows(p->weight, 0, 1, d, wsize, false, "weight", what))) return s;
+  if ((s = check_rows(p->post_weight, 0, 1, d, wsize, false, "post_weight", what))) return s;
+  if ((s = check_rows(p->gate, p->gate_ld, p->groups, d, msize, false, "gate", what))) return s;
+  if ((s = check_rows(p->scale, p->scale_ld, p->groups, d, msize, false, "scale", what))) return s;
+  if ((s = check_rows(p->shift, p->shift_ld, p->groups, d, msize, false, "shift", what))) return s;
+  a->n = n;
+  a->d = d;
+  a->groups = p->groups;
+  a->cu = p->cu;
+  a->norm = p->norm;
+  a->post = p->post;
+  a->eps = p->eps;
+  a->post_eps = p->post_eps;
+  a->w = p->weight;
+  a->pw = p->post_weight;
+  a->wtype = p->weight_type;
+  a->mtype = p->mod_type;
+  a->gate = p->gate;
+  a->scale = p->scale;
+  a->shift = p->shift;
+  a->gld = p->gate_ld;
+  a->scld = p->scale_ld;
+  a->shld = p->shift_ld;
+  return ORBQ_OK;
+}
+
+bool vectors_fit(const orbq::NormArgs& a) {
+  const int w = orbq::dtype_size(a.wtype), m = orbq::dtype_size(a.mtype);
+  return a.d % 8 == 0 && fits(a.w, 0, w) && fits(a.pw, 0, w) && fits(a.gate, a.gld, m) && fits(a.scale, a.scld, m) &&
+         fits(a.shift, a.shld, m);
+}
+
+// places of a backward pass's partial sums: see block_norm_backward.hip
+int64_t norm_places(int64_t n, int32_t d, int32_t groups, int32_t* chunk_rows) {
+  *chunk_rows = orbq::norm_chunk_rows(n, d, orbq::device_cus());
+  const int64_t places = (n + *chunk_rows - 1) / *chunk_rows + groups - 1;
+  return places ? places : 1;
+}
+
+}  // namespace
+
+ORBQ_API int orbq_block_norm(const orbq_norms* norms, int64_t n, int32_t d, const void* x, int64_t x_ld, const void* y,
+                             int64_t y_ld, void* r, int64_t r_ld, void* h, int64_t h_ld, orbq_dtype stream_type,
+                             orbq_dtype branch_type, void* stream) {
+  const char* what = "orbq_block_norm";
+  orbq::NormArgs a{};
+  int s;
+  if ((s = check_norms(norms, n, d, y != nullptr, stream_type, branch_type, &a, what))) return s;
+  if (n == 0) return set_ok();
+  if (!x) return set_error(ORBQ_ERR_INVALID_ARG, "%s: NULL x", what);
+  if ((norms->norm != ORBQ_NORM_NONE) != (h != nullptr)) return set_error(ORBQ_ERR_INVALID_ARG, "%s: h goes with a norm", what);
+  if (!h && !r) return set_error(ORBQ_ERR_INVALID_ARG, "%s: neither r nor h to write", what);
+  const int ss = orbq::dtype_size(stream_type), bs = orbq::dtype_size(branch_type);
+  if ((s = check_rows(x, x_ld, n, d, ss, false, "x", what))) return s;
+  if ((s = check_rows(y, y_ld, n, d, bs, false, "y", what))) return s;
+  if (y && (s = check_rows(r, r_ld, n, d, ss, true, "r", what))) return s;
+  if ((s = check_rows(h, h_ld, n, d, bs, true, "h", what))) return s;
+  a.x = x;
+  a.y = y;
+  a.r = y ? r : nullptr;
+  a.h = h;
+  a.xld = x_ld;
+  a.yld = y_ld;
+  a.rld = r_ld;
+  a.hld = h_ld;
+  const bool wide = vectors_fit(a) && fits(x, x_ld, ss) && fits(y, y_ld, bs) && fits(a.r, r_ld, ss) && fits(h, h_ld, bs);
+  return hip_status(orbq::launch_block_norm(a, stream_type, branch_type, wide, static_cast<hipStream_t>(stream)), what);
+}
+
+ORBQ_API size_t orbq_block_norm_backward_workspace_bytes(int64_t n, int32_t d, int32_t groups) {
+  if (n < 0 || n > (int64_t{1} << 30) || d < 1 || d > 16384 || groups < 1 || groups > (1 << 30)) return 0;
+  int32_t chunk;
+  return static_cast<size_t>(norm_places(n, d, groups, &chunk)) * 3 * d * sizeof(float);
+}
+
+ORBQ_API int orbq_block_norm_backward(const orbq_norms* norms, int64_t n, int32_t d, const void* r, int64_t r_ld, const void* y,
+                                      int64_t y_ld, const void* dr, int64_t dr_ld, const void* dh, int64_t dh_ld, void* dx,
+                                      int64_t dx_ld, void* dy, int64_t dy_ld, const orbq_norms_grads* grads,
+                                      orbq_dtype stream_type, orbq_dtype branch_type, void* workspace, size_t ws_bytes,
+                                      void* stream) {
+  const char* what = "orbq_block_norm_backward";
+  orbq::NormArgs a{};
+  int s;
+  if ((s = check_norms(norms, n, d, y != nullptr, stream_type, branch_type, &a, what))) return s;
+  const orbq_norms_grads none{};
+  const orbq_norms_grads& g = grads ? *grads : none;
+  const bool normed = norms->norm != ORBQ_NORM_NONE;
+  if (!normed && (g.scale || g.shift || g.weight))
+    return set_error(ORBQ_ERR_INVALID_ARG, "%s: gradient of scale, shift or weight without a norm", what);
+  if (!y && (g.gate || g.post_weight || dy)) return set_error(ORBQ_ERR_INVALID_ARG, "%s: gradient of gate, post_weight or y without y", what);
+  if (g.post_weight && norms->post == ORBQ_NORM_NONE)
+    return set_error(ORBQ_ERR_INVALID_ARG, "%s: gradient of post_weight without post", what);
+  const int ss = orbq::dtype_size(stream_type), bs = orbq::dtype_size(branch_type), wsize = orbq::dtype_size(norms->weight_type),
+            msize = orbq::dtype_size(norms->mod_type);
+  if ((s = check_rows(g.gate, g.gate_ld, g.gate_ld ? a.groups : 1, d, msize, true, "the gate's gradient", what))) return s;
+  if ((s = check_rows(g.scale, g.scale_ld, g.scale_ld ? a.groups : 1, d, msize, true, "the scale's gradient", what))) return s;
+  if ((s = check_rows(g.shift, g.shift_ld, g.shift_ld ? a.groups : 1, d, msize, true, "the shift's gradient", what))) return s;
+  if ((s = check_rows(g.weight, 0, 1, d, wsize, true, "the weight's gradient", what))) return s;
+  if ((s = check_rows(g.post_weight, 0, 1, d, wsize, true, "the post_weight's gradient", what))) return s;
+  const bool vectors = g.gate || g.scale || g.shift || g.weight || g.post_weight;
+  if (n == 0 && !vectors) return set_ok();
+  if (n) {
+    if (normed && !r) return set_error(ORBQ_ERR_INVALID_ARG, "%s: NULL r", what);
+    if (normed != (dh != nullptr)) return set_error(ORBQ_ERR_INVALID_ARG, "%s: dh goes with a norm", what);
+    if (!dh && !dr) return set_error(ORBQ_ERR_INVALID_ARG, "%s: neither dr nor dh", what);
+    if (!vectors && !dx && !dy) return set_ok();
+    if ((s = check_rows(r, r_ld, n, d, ss, false, "r", what))) return s;
+    if ((s = check_rows(y, y_ld, n, d, bs, false, "y", what))) return s;
+    if ((s = check_rows(dr, dr_ld, n, d, ss, false, "dr", what))) return s;
+    if ((s = check_rows(dh, dh_ld, n, d, bs, false, "dh", what))) return s;
+    if ((s = check_rows(dx, dx_ld, n, d, ss, true, "dx", what))) return s;
+    if ((s = check_rows(dy, dy_ld, n, d, bs, true, "dy", what))) return s;
+  }
+  const int64_t places = norm_places(n, d, a.groups, &a.chunk_rows);
+  if (vectors) {
+    const size_t need = static_cast<size_t>(places) * 3 * d * sizeof(float);
+    if (!workspace || ws_bytes < need)
+      return set_error(ORBQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, workspace ? ws_bytes : 0, need);
+    if (!aligned(workspace, 16)) return set_error(ORBQ_ERR_ALIGNMENT, "%s: workspace must be 16-byte aligned", what);
+    a.part = static_cast<float*>(workspace);
+  }
+  a.x = r;
+  a.y = y;
+  a.dr = dr;
+  a.dh = dh;
+  a.dx = dx;
+  a.dy = dy;
+  a.xld = r_ld;
+  a.yld = y_ld;
+  a.drld = dr_ld;
+  a.dhld = dh_ld;
+  a.dxld = dx_ld;
+  a.dyld = dy_ld;
+  const bool wide = vectors_fit(a) && fits(r, r_ld, ss) && fits(y, y_ld, bs) && fits(dr, dr_ld, ss) && fits(dh, dh_ld, bs) &&
+                    fits(dx, dx_ld, ss) && fits(dy, dy_ld, bs);
+  const orbq::NormGrads o{g.gate, g.scale, g.shift, g.gate_ld, g.scale_ld, g.shift_ld, g.weight, g.post_weight};
+  return hip_status(orbq::launch_block_norm_backward(a, o, stream_type, branch_type, wide, static_cast<hipStream_t>(stream)), what);
+}

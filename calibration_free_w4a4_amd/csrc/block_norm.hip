@@ -1,0 +1,162 @@
+// block_norm: r = x + gate * u, u = y or post(y) post_weight;  h = norm(r) weight (1 + scale) + shift.
+//
+// norm and post are a row's layer norm, (v - mean) / sqrt(mean of (v - mean)^2 + eps), or its root mean square norm,
+// v / sqrt(mean of v^2 + eps).  gate, scale and shift belong to the row's group.  h is taken from r as it is stored, so
+// that a later reader of r, the backward pass and a call of its own for the norm see the same values.
+//
+// x and y are read once, r and h written once: HBM's bytes bound the call.  A row is held in registers by one wave (to
+// 2048 entries) or by the waves of a workgroup, which keeps the two passes of a variance free of a second reading; sums are
+// taken in fp32 in one order, so a row's result does not depend on the call it is in.  The vectors of the groups come
+// from the caches.
+#include "block_norm_device.h"
+
+namespace orbq {
+namespace {
+
+using namespace bn;
+
+constexpr int threads_of(int waves) { return waves == 1 ? 256 : 64 * waves; }
+
+// (v - mean) / sqrt(variance + eps) or v / sqrt(mean square + eps), in place; entries behind the row hold 0 and stay so
+template <int E, int V, int W>
+__device__ __forceinline__ void normalise(float (&v)[V][E], const int32_t (&col)[V], int32_t d, bool layer, float eps,
+                                          float (*place)[W][2], int& turn) {
+  const RowSum<W> sum;
+  float s = 0.0f;
+  if (layer) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) s += v[i][e];
+    sum(&s, nullptr, place, turn);
+    const float mean = s / static_cast<float>(d);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] = col[i] < d ? v[i][e] - mean : 0.0f;
+    s = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = __builtin_fmaf(v[i][e], v[i][e], s);
+  sum(&s, nullptr, place, turn);
+  const float f = 1.0f / __builtin_sqrtf(s / static_cast<float>(d) + eps);
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[i][e] *= f;
+}
+
+template <int TX, int TY, int E, int V, int W>
+__global__ __launch_bounds__(threads_of(W)) void k_block_norm(const NormArgs a, int64_t row0) {
+  __shared__ float place[2][W][2];
+  const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t row64 = row0 + (W == 1 ? blockIdx.x * int64_t{4} + (threadIdx.x >> 6) : blockIdx.x);
+  if (row64 >= a.n) return;
+  const int32_t row = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(row64));
+  int turn = 0;
+  int32_t col[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) col[i] = (i * 64 * W + t) * E;
+  float x[V][E], y[V][E] = {};
+  const Rsrc xs = row_at<TX>(a.x, row, a.xld, a.d);
+#pragma unroll
+  for (int i = 0; i < V; ++i) load<TX, E>(xs, col[i], x[i]);
+  if (a.y) {
+    const Rsrc ys = row_at<TY>(a.y, row, a.yld, a.d);
+#pragma unroll
+    for (int i = 0; i < V; ++i) load<TY, E>(ys, col[i], y[i]);
+  }
+  int32_t end;
+  const int32_t g = group_of(a, row, &end);
+  if (g < 0) return;
+  if (a.y) {
+    if (a.post != kNormNone) {
+      normalise<E, V, W>(y, col, a.d, a.post == kNormLayer, a.post_eps, place, turn);
+      if (a.pw) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float w[E];
+          load_any<E>(a.wtype, a.pw, 0, 0, a.d, col[i], w);
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[i][e] *= w[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float w[E];
+      if (a.gate) load_any<E>(a.mtype, a.gate, g, a.gld, a.d, col[i], w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        x[i][e] = a.gate ? __builtin_fmaf(w[e], y[i][e], x[i][e]) : x[i][e] + y[i][e];
+        x[i][e] = static_cast<float>(static_cast<typename Elem<TX>::T>(x[i][e]));
+      }
+      if (a.r) store<TX, E>(row_at<TX>(a.r, row, a.rld, a.d), col[i], x[i]);
+    }
+  }
+  if (a.norm == kNormNone) return;
+  normalise<E, V, W>(x, col, a.d, a.norm == kNormLayer, a.eps, place, turn);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float w[E];
+    if (a.w) {
+      load_any<E>(a.wtype, a.w, 0, 0, a.d, col[i], w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[i][e] *= w[e];
+    }
+    if (a.scale) {
+      load_any<E>(a.mtype, a.scale, g, a.scld, a.d, col[i], w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[i][e] *= 1.0f + w[e];
+    }
+    if (a.shift) {
+      load_any<E>(a.mtype, a.shift, g, a.shld, a.d, col[i], w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[i][e] += w[e];
+    }
+    store<TY, E>(row_at<TY>(a.h, row, a.hld, a.d), col[i], x[i]);
+  }
+}
+
+template <int TX, int TY, int E, int V, int W> int launch(const NormArgs& a, hipStream_t stream) {
+  constexpr int64_t kMost = (int64_t{1} << 31) / (64 * W);  // rows of a launch: 2^31 threads
+  for (int64_t row0 = 0; row0 < a.n; row0 += kMost) {
+    const int64_t rows = a.n - row0 < kMost ? a.n - row0 : kMost;
+    const int64_t blocks = W == 1 ? (rows + 3) / 4 : rows;
+    hipLaunchKernelGGL((k_block_norm<TX, TY, E, V, W>), dim3(static_cast<uint32_t>(blocks)), dim3(threads_of(W)), 0, stream, a,
+                       row0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return static_cast<int>(e);
+  }
+  return static_cast<int>(hipSuccess);
+}
+
+// the least registers that hold a row: one wave to 2048 entries, whose sums need no barrier
+template <int TX, int TY> int by_width(const NormArgs& a, bool wide, hipStream_t stream) {
+  if (!wide) {  // entries one by one: widths, strides or addresses that 16-byte columns do not fit
+    if (a.d <= 512) return launch<TX, TY, 1, 8, 1>(a, stream);
+    if (a.d <= 4096) return launch<TX, TY, 1, 8, 8>(a, stream);
+    return launch<TX, TY, 1, 16, 16>(a, stream);
+  }
+  if (a.d <= 512) return launch<TX, TY, 8, 1, 1>(a, stream);
+  if (a.d <= 1024) return launch<TX, TY, 8, 2, 1>(a, stream);
+  if (a.d <= 1536) return launch<TX, TY, 8, 3, 1>(a, stream);
+  if (a.d <= 2048) return launch<TX, TY, 8, 4, 1>(a, stream);
+  if (a.d <= 4096) return launch<TX, TY, 8, 2, 4>(a, stream);
+  if (a.d <= 8192) return launch<TX, TY, 8, 4, 4>(a, stream);
+  return launch<TX, TY, 8, 4, 8>(a, stream);
+}
+
+}  // namespace
+
+int launch_block_norm(const NormArgs& a, int stream_type, int branch_type, bool wide, hipStream_t stream) {
+  if (stream_type == kBF16) return by_width<kBF16, kBF16>(a, wide, stream);
+  if (stream_type == kF16) return by_width<kF16, kF16>(a, wide, stream);
+  if (branch_type == kBF16) return by_width<kF32, kBF16>(a, wide, stream);
+  if (branch_type == kF16) return by_width<kF32, kF16>(a, wide, stream);
+  return by_width<kF32, kF32>(a, wide, stream);
+}
+
+}  // namespace orbq

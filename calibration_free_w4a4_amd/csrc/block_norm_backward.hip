@@ -1,0 +1,311 @@
+// block_norm's gradients.  With rhat = norm(r), yhat = post(y) (or y), f and fy the factors of the two norms:
+//   t = dh weight (1 + scale);  dx = dr' = dr + f (t - [mean t] - rhat mean(t rhat))      ([..]: layer norm only)
+//   q = dr' gate post_weight;   dy = fy (q - [mean q] - yhat mean(q yhat)), or dr' gate without a norm
+//   of each group g:  A = sum dh rhat,  S = sum dh,  B = sum dr' yhat  over its rows, and from these
+//   dscale = weight A, dshift = S, dgate = post_weight B, dweight = sum over g (1 + scale) A,
+//   dpost_weight = sum over g gate B.
+// Nothing is kept from the forward pass but r, which it has written, and y: a row's statistics are taken again from
+// the registers that hold it.  r, y, dr and dh are read once, dx and dy written once: HBM's bytes bound the call.
+//
+// The sums over rows need no atomics and do not depend on scheduling: a workgroup owns a chunk of consecutive rows, and
+// the sums of (chunk c, group g) go to place c + g, which no other pair has, since along the rows each step
+// to the next place adds one to either.  A second launch adds a group's places in order.
+#include <algorithm>
+
+#include "block_norm_device.h"
+
+namespace orbq {
+namespace {
+
+using namespace bn;
+
+constexpr int threads_of(int waves) { return waves == 1 ? 256 : 64 * waves; }
+constexpr int teams_of(int waves) { return waves == 1 ? 4 : 1; }  // rows of a workgroup at a time
+
+// LATE: the branch's row is fetched only when the stream's is done with, which costs two more meetings of the waves and takes
+// the registers of one row less (the widest rows, whose registers would not do otherwise).
+template <int TX, int TY, int E, int V, int W, bool LATE>
+__global__ __launch_bounds__(threads_of(W)) void k_norm_backward(const NormArgs a) {
+  constexpr int TEAMS = teams_of(W);
+  __shared__ float place[2][W][2];
+  __shared__ float joined[TEAMS > 1 ? TEAMS - 1 : 1][TEAMS > 1 ? V * 64 * E : 1];
+  const int team = W == 1 ? threadIdx.x >> 6 : 0, t = W == 1 ? threadIdx.x & 63 : threadIdx.x;
+  int turn = 0;
+  int32_t col[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) col[i] = (i * 64 * W + t) * E;
+  typedef float Row[V][E];
+#define ORBQ_EACH(...)                    \
+  _Pragma("unroll") for (int i = 0; i < V; ++i) \
+    _Pragma("unroll") for (int e = 0; e < E; ++e) { __VA_ARGS__; }
+  const RowSum<W> sum;
+  const float each = 1.0f / static_cast<float>(a.d);
+  const bool normed = a.norm != kNormNone, layer = a.norm == kNormLayer, posted = a.y && a.post != kNormNone,
+             post_layer = posted && a.post == kNormLayer;
+  const int64_t first = blockIdx.x * static_cast<int64_t>(a.chunk_rows);
+  const int32_t last = static_cast<int32_t>(first + a.chunk_rows < a.n ? first + a.chunk_rows : a.n);
+  int32_t from = static_cast<int32_t>(first);
+  while (from < last) {
+    int32_t end;
+    const int32_t g = group_of(a, from, &end);
+    if (end > last) end = last;
+    if (g < 0) {  // nothing came of these rows
+      const float zero[E] = {};
+      for (int32_t at = from + team; at < end; at += TEAMS) {
+        const int32_t row = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (a.dx) store<TX, E>(row_at<TX>(a.dx, row, a.dxld, a.d), col[i], zero);
+          if (a.dy) store<TY, E>(row_at<TY>(a.dy, row, a.dyld, a.d), col[i], zero);
+        }
+      }
+      from = end;
+      continue;
+    }
+    Row A, S, B;
+    ORBQ_EACH(A[i][e] = S[i][e] = B[i][e] = 0.0f)
+    for (int32_t at = from + team; at < end; at += TEAMS) {
+      const int32_t row = __builtin_amdgcn_readfirstlane(at);
+      asm volatile("" ::: "memory");  // the vectors are read again for each row: held over the loop they would take the registers
+      Row r, dh, dr, y;
+      ORBQ_EACH(r[i][e] = dh[i][e] = dr[i][e] = y[i][e] = 0.0f)
+      const auto load_y = [&] {
+#pragma unroll
+        for (int i = 0; i < V; ++i) load<TY, E>(row_at<TY>(a.y, row, a.yld, a.d), col[i], y[i]);
+      };
+      if (normed) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) load<TX, E>(row_at<TX>(a.x, row, a.xld, a.d), col[i], r[i]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) load<TY, E>(row_at<TY>(a.dh, row, a.dhld, a.d), col[i], dh[i]);
+      }
+      if (!LATE && a.y) load_y();
+      if (a.dr) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) load<TX, E>(row_at<TX>(a.dr, row, a.drld, a.d), col[i], dr[i]);
+      }
+      // v becomes the normalised row, and with it w where both are there
+      const auto factors = [&](Row& v, Row& w, bool both, bool v_layer, bool w_layer, float v_eps, float w_eps, float* fv, float* fw) {
+        float s = 0.0f, u = 0.0f;
+        if (v_layer || w_layer) {
+          ORBQ_EACH(s += v[i][e])
+          if (both) ORBQ_EACH(u += w[i][e])
+          sum(&s, both ? &u : nullptr, place, turn);
+          const float mv = v_layer ? s / static_cast<float>(a.d) : 0.0f, mw = w_layer ? u / static_cast<float>(a.d) : 0.0f;
+          ORBQ_EACH(v[i][e] = col[i] < a.d ? v[i][e] - mv : 0.0f)
+          if (both) ORBQ_EACH(w[i][e] = col[i] < a.d ? w[i][e] - mw : 0.0f)
+          s = u = 0.0f;
+        }
+        ORBQ_EACH(s = __builtin_fmaf(v[i][e], v[i][e], s))
+        if (both) ORBQ_EACH(u = __builtin_fmaf(w[i][e], w[i][e], u))
+        sum(&s, both ? &u : nullptr, place, turn);
+        *fv = 1.0f / __builtin_sqrtf(s / static_cast<float>(a.d) + v_eps);
+        ORBQ_EACH(v[i][e] *= *fv)
+        if (both) {
+          *fw = 1.0f / __builtin_sqrtf(u / static_cast<float>(a.d) + w_eps);
+          ORBQ_EACH(w[i][e] *= *fw)
+        }
+      };
+      float f = 1.0f, fy = 1.0f;
+      if (normed) factors(r, y, !LATE && posted, layer, !LATE && post_layer, a.eps, a.post_eps, &f, &fy);
+      if (normed) {
+        float m = 0.0f, p = 0.0f;
+        ORBQ_EACH(A[i][e] = __builtin_fmaf(dh[i][e], r[i][e], A[i][e]); S[i][e] += dh[i][e])
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float w[E];
+          if (a.w) {
+            load_any<E>(a.wtype, a.w, 0, 0, a.d, col[i], w);
+#pragma unroll
+            for (int e = 0; e < E; ++e) dh[i][e] *= w[e];
+          }
+          if (a.scale) {
+            load_any<E>(a.mtype, a.scale, g, a.scld, a.d, col[i], w);
+#pragma unroll
+            for (int e = 0; e < E; ++e) dh[i][e] *= 1.0f + w[e];
+          }
+        }
+        ORBQ_EACH(m += dh[i][e]; p = __builtin_fmaf(dh[i][e], r[i][e], p))
+        sum(&p, layer ? &m : nullptr, place, turn);
+        m = layer ? m * each : 0.0f;
+        p *= each;
+        ORBQ_EACH(dr[i][e] = col[i] < a.d ? __builtin_fmaf(f, __builtin_fmaf(-r[i][e], p, dh[i][e] - m), dr[i][e]) : 0.0f)
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (a.dx) store<TX, E>(row_at<TX>(a.dx, row, a.dxld, a.d), col[i], dr[i]);
+      if (!a.y) continue;
+      if (LATE) load_y();
+      if (posted && (LATE || !normed)) factors(y, y, false, post_layer, false, a.post_eps, 0.0f, &fy, &fy);
+      ORBQ_EACH(B[i][e] = __builtin_fmaf(dr[i][e], y[i][e], B[i][e]))
+      if (!a.dy) continue;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float w[E];
+        if (a.gate) {
+          load_any<E>(a.mtype, a.gate, g, a.gld, a.d, col[i], w);
+#pragma unroll
+          for (int e = 0; e < E; ++e) dr[i][e] *= w[e];
+        }
+        if (a.pw) {
+          load_any<E>(a.wtype, a.pw, 0, 0, a.d, col[i], w);
+#pragma unroll
+          for (int e = 0; e < E; ++e) dr[i][e] *= w[e];
+        }
+      }
+      if (posted) {
+        float m = 0.0f, p = 0.0f;
+        ORBQ_EACH(m += dr[i][e]; p = __builtin_fmaf(dr[i][e], y[i][e], p))
+        sum(&p, post_layer ? &m : nullptr, place, turn);
+        m = post_layer ? m * each : 0.0f;
+        p *= each;
+        ORBQ_EACH(dr[i][e] = fy * __builtin_fmaf(-y[i][e], p, dr[i][e] - m))
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        store<TY, E>(row_at<TY>(a.dy, row, a.dyld, a.d), col[i], dr[i]);
+    }
+    if (a.part) {
+      float* sums = a.part + (static_cast<int64_t>(blockIdx.x) + g) * 3 * a.d;
+      // the first team adds the others' sums to its own, one of the three kinds after the other
+      const auto join = [&](Row& mine, int kind) {
+        if constexpr (TEAMS > 1) {
+          __syncthreads();
+          if (team) ORBQ_EACH(joined[team - 1][(i * E + e) * 64 + t] = mine[i][e])
+          __syncthreads();
+          if (team) return;
+#pragma unroll
+          for (int k = 0; k < TEAMS - 1; ++k) ORBQ_EACH(mine[i][e] += joined[k][(i * E + e) * 64 + t])
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          store<kF32, E>(row_at<kF32>(sums, kind, a.d, a.d), col[i], mine[i]);
+      };
+      if (normed) {
+        join(A, 0);
+        join(S, 1);
+      }
+      if (a.y) join(B, 2);
+    }
+    from = end;
+  }
+#undef ORBQ_EACH
+}
+
+// The sums of all groups, one kind a workgroup row: lanes are columns, waves share the places (few groups) or the groups.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void k_norm_grads(const NormArgs a, const NormGrads o) {
+  __shared__ float meet[kSumWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, kind = blockIdx.y;
+  const int32_t col = blockIdx.x * 64 + lane, n = static_cast<int32_t>(a.n);
+  const bool in = col < a.d;
+  void* const out = kind == 0 ? o.scale : (kind == 1 ? o.shift : o.gate);
+  const int64_t out_ld = kind == 0 ? o.scld : (kind == 1 ? o.shld : o.gld);
+  void* const total = kind == 0 ? o.w : (kind == 1 ? nullptr : o.pw);
+  if ((!out && !total) || (kind < 2 ? a.norm == kNormNone : a.y == nullptr)) return;
+  // what the sums are multiplied with for the group's gradient, and for the one summed over the groups
+  const void* const mine = kind == 0 ? a.w : (kind == 1 ? nullptr : a.pw);
+  const void* const theirs = kind == 0 ? a.scale : a.gate;
+  const int64_t theirs_ld = kind == 0 ? a.scld : a.gld;
+  float own = 1.0f;
+  if (mine) load_any<1>(a.wtype, mine, 0, 0, a.d, col, &own);
+  const auto put = [&](void* to, int type, int64_t row, int64_t ld, float v) {
+    if (type == kF32) store<kF32, 1>(row_at<kF32>(to, row, ld, a.d), col, &v);
+    else if (type == kBF16) store<kBF16, 1>(row_at<kBF16>(to, row, ld, a.d), col, &v);
+    else store<kF16, 1>(row_at<kF16>(to, row, ld, a.d), col, &v);
+  };
+  const auto meet_up = [&](float v) {  // sum of the waves' values, known to all
+    __syncthreads();
+    meet[wave][lane] = v;
+    __syncthreads();
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kSumWaves; ++w) s += meet[w][lane];
+    return s;
+  };
+  const bool by_group = a.groups >= kSumWaves;
+  float all = 0.0f, weighted = 0.0f;
+  for (int32_t g = by_group ? wave : 0; g < a.groups; g += by_group ? kSumWaves : 1) {
+    int32_t r0, r1;
+    if (a.cu) {
+      r0 = a.cu[g];
+      r1 = a.cu[g + 1];
+      r0 = r0 < 0 ? 0 : (r0 > n ? n : r0);
+      r1 = r1 < r0 ? r0 : (r1 > n ? n : r1);
+    } else {
+      const int32_t each = n / a.groups;
+      r0 = g * each;
+      r1 = r0 + each;
+    }
+    float s = 0.0f;
+    if (r1 > r0 && in) {
+      const int32_t c1 = (r1 - 1) / a.chunk_rows, step = by_group ? 1 : kSumWaves;
+      const float* p = a.part + kind * a.d + col;
+#pragma unroll 8
+      for (int32_t c = r0 / a.chunk_rows + (by_group ? 0 : wave); c <= c1; c += step) s += p[(static_cast<int64_t>(c) + g) * 3 * a.d];
+    }
+    float f = 1.0f;
+    if (theirs && total) {
+      load_any<1>(a.mtype, theirs, g, theirs_ld, a.d, col, &f);
+      if (kind == 0) f += 1.0f;
+    }
+    weighted = __builtin_fmaf(f, s, weighted);
+    all += s;
+    if (out && out_ld) {
+      if (!by_group) s = meet_up(s);
+      if (by_group || wave == 0) put(out, a.mtype, g, out_ld, s * own);
+    }
+  }
+  if (out && !out_ld) {
+    const float s = meet_up(all);
+    if (wave == 0) put(out, a.mtype, 0, 0, s * own);
+  }
+  if (total) {
+    const float s = meet_up(weighted);
+    if (wave == 0) put(total, a.wtype, 0, 0, s);
+  }
+}
+
+template <int TX, int TY, int E, int V, int W, bool LATE = false> int launch(const NormArgs& a, hipStream_t stream) {
+  const int64_t blocks = (a.n + a.chunk_rows - 1) / a.chunk_rows;
+  if (blocks == 0) return static_cast<int>(hipSuccess);
+  hipLaunchKernelGGL((k_norm_backward<TX, TY, E, V, W, LATE>), dim3(static_cast<uint32_t>(blocks)), dim3(threads_of(W)), 0, stream, a);
+  return static_cast<int>(hipGetLastError());
+}
+
+template <int TX, int TY> int by_width(const NormArgs& a, bool wide, hipStream_t stream) {
+  if (!wide) {
+    if (a.d <= 512) return launch<TX, TY, 1, 8, 1>(a, stream);
+    if (a.d <= 4096) return launch<TX, TY, 1, 8, 8>(a, stream);
+    return launch<TX, TY, 1, 32, 8, true>(a, stream);
+  }
+  if (a.d <= 512) return launch<TX, TY, 8, 1, 1>(a, stream);
+  if (a.d <= 1024) return launch<TX, TY, 8, 2, 1>(a, stream);
+  if (a.d <= 1536) return launch<TX, TY, 8, 1, 3>(a, stream);
+  if (a.d <= 2048) return launch<TX, TY, 8, 1, 4>(a, stream);
+  if (a.d <= 4096) return launch<TX, TY, 8, 2, 4>(a, stream);
+  if (a.d <= 8192) return launch<TX, TY, 8, 2, 8>(a, stream);
+  return launch<TX, TY, 8, 4, 8, true>(a, stream);
+}
+
+}  // namespace
+
+// Enough chunks to fill the card, few enough that their sums are little beside the rows.
+int32_t norm_chunk_rows(int64_t n, int32_t, int cus) {
+  const int64_t chunks = std::min<int64_t>(n, static_cast<int64_t>(cus) * 4);
+  return static_cast<int32_t>(std::max<int64_t>(1, (n + chunks - 1) / std::max<int64_t>(1, chunks)));
+}
+
+int launch_block_norm_backward(const NormArgs& a, const NormGrads& g, int stream_type, int branch_type, bool wide, hipStream_t stream) {
+  int e;
+  if (stream_type == kBF16) e = by_width<kBF16, kBF16>(a, wide, stream);
+  else if (stream_type == kF16) e = by_width<kF16, kF16>(a, wide, stream);
+  else if (branch_type == kBF16) e = by_width<kF32, kBF16>(a, wide, stream);
+  else if (branch_type == kF16) e = by_width<kF32, kF16>(a, wide, stream);
+  else e = by_width<kF32, kF32>(a, wide, stream);
+  if (e || !a.part) return e;
+  hipLaunchKernelGGL(k_norm_grads, dim3((a.d + 63) / 64, 3), dim3(64 * kSumWaves), 0, stream, a, g);
+  return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace orbq

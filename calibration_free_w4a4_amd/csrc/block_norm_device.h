@@ -1,0 +1,146 @@
+// Device helpers of block_norm's kernels.
+#pragma once
+
+#include "attention_device.h"
+#include "block_norm.h"
+
+namespace orbq {
+namespace bn {
+
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+
+// Row `row` of rows of d entries of `size` bytes, `ld` entries apart, as a buffer: entries behind the row read as zero and are
+// not written, and a column is one 32-bit offset for every row.  All of it is the same for a whole wave.
+__device__ __forceinline__ Rsrc row_at(const void* p, int64_t row, int64_t ld, int32_t d, int size) {
+  const uint64_t b = reinterpret_cast<uint64_t>(p) + static_cast<uint64_t>(row * ld * size);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0,
+                                           __builtin_amdgcn_readfirstlane(d * size), 0x00020000u);
+}
+template <int DT> __device__ __forceinline__ Rsrc row_at(const void* p, int64_t row, int64_t ld, int32_t d) {
+  return row_at(p, row, ld, d, sizeof(typename Elem<DT>::T));
+}
+
+// E entries of a row from column `col` on as floats: 8 (16 or 32 aligned bytes) or 1
+template <int DT, int E> __device__ __forceinline__ void load(Rsrc r, uint32_t col, float* f) {
+  using T = typename Elem<DT>::T;
+  if constexpr (E == 1) {
+    if constexpr (DT == kF32) f[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, col * 4, 0, 0));
+    else f[0] = static_cast<float>(__builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, col * 2, 0, 0)));
+  } else if constexpr (DT == kF32) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const f32x4_t v = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, col * 4, 16 * k, 0));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[4 * k + i] = v[i];
+    }
+  } else {
+    typedef T V __attribute__((ext_vector_type(8)));
+    const V v = __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(r, col * 2, 0, 0));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(v[i]);
+  }
+}
+template <int DT, int E> __device__ __forceinline__ void store(Rsrc r, uint32_t col, const float* f) {
+  using T = typename Elem<DT>::T;
+  if constexpr (E == 1) {
+    if constexpr (DT == kF32) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, f[0]), r, col * 4, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<T>(f[0])), r, col * 2, 0, 0);
+  } else if constexpr (DT == kF32) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const f32x4_t v = {f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]};
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, col * 4, 16 * k, 0);
+    }
+  } else {
+    typedef T V __attribute__((ext_vector_type(8)));
+    V v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = static_cast<T>(f[i]);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, col * 2, 0, 0);
+  }
+}
+// of a type that is the same for a whole launch
+template <int E> __device__ __forceinline__ void load_any(int type, const void* p, int64_t row, int64_t ld, int32_t d, uint32_t col, float* f) {
+  const Rsrc r = row_at(p, row, ld, d, type == kF32 ? 4 : 2);
+  if (type == kF32) load<kF32, E>(r, col, f);
+  else if (type == kBF16) load<kBF16, E>(r, col, f);
+  else load<kF16, E>(r, col, f);
+}
+
+template <int CTRL> __device__ __forceinline__ float moved(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float lane_of(float x, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+// sum over a wave whose lanes are all active, in one fixed order: neighbours, quads, half rows, rows, then the four rows
+__device__ __forceinline__ float wave_sum(float x) {
+  x += moved<0xB1>(x);   // quad_perm [1,0,3,2]
+  x += moved<0x4E>(x);   // quad_perm [2,3,0,1]
+  x += moved<0x141>(x);  // row_half_mirror
+  x += moved<0x140>(x);  // row_mirror
+  return (lane_of(x, 0) + lane_of(x, 16)) + (lane_of(x, 32) + lane_of(x, 48));
+}
+
+// Two sums at once over the W waves that hold a row.  `turn` tells successive sums apart: two places are enough, since
+// a wave writes a place again only behind the barrier of the sum between, which every wave reaches after reading.
+template <int W> struct RowSum {
+  __device__ __forceinline__ void operator()(float* a, float* b, float (*place)[W][2], int& turn) const {
+    *a = wave_sum(*a);
+    if (b) *b = wave_sum(*b);
+    if constexpr (W > 1) {
+      const int wave = threadIdx.x >> 6;
+      if ((threadIdx.x & 63) == 0) {
+        place[turn][wave][0] = *a;
+        if (b) place[turn][wave][1] = *b;
+      }
+      __syncthreads();
+      float s = 0.0f, t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        s += place[turn][w][0];
+        if (b) t += place[turn][w][1];
+      }
+      *a = s;
+      if (b) *b = t;
+      turn ^= 1;
+    }
+  }
+};
+
+// Group of a row, or -1 for one that no group has; *end: one past the group's rows (the next row to look at for -1).
+// Whatever cu holds, a group is within [0, groups) and *end behind the row.
+__device__ __forceinline__ int32_t group_of(const NormArgs& a, int32_t row, int32_t* end) {
+  const int32_t n = static_cast<int32_t>(a.n);
+  if (!a.cu) {
+    const int32_t each = n / a.groups, g = a.groups == 1 ? 0 : row / each;
+    *end = a.groups == 1 ? n : (g + 1) * each;
+    return g;
+  }
+  const int32_t first = a.cu[0];
+  if (row < first) {
+    *end = first < n ? first : n;
+    return -1;
+  }
+  int32_t lo = 1, hi = a.groups + 1, at = n;  // the first i with cu[i] > row lies in [lo, hi]; at: cu[hi]
+  while (lo < hi) {
+    const int32_t mid = (lo + hi) >> 1, v = a.cu[mid];
+    if (v > row) {
+      hi = mid;
+      at = v;
+    } else {
+      lo = mid + 1;
+    }
+  }
+  *end = at < n ? at : n;
+  if (hi > a.groups) {
+    *end = n;
+    return -1;
+  }
+  return hi - 1;
+}
+
+}  // namespace bn
+}  // namespace orbq

@@ -78,8 +78,8 @@ typedef enum {
   ORBQ_ERR_CODEBOOK = -6      /* codebook not ascending, not antisymmetric, not finite */
 } orbq_status;
 
-/* ORBQ_F16 is taken by the attention-side operators (orbq_rope_apply, orbq_kv_*) only; the other
- * calls refuse it with ORBQ_ERR_INVALID_ARG. */
+/* ORBQ_F16 is taken by the attention-side operators (orbq_rope_apply, orbq_kv_*) and the norms around a block
+ * (orbq_block_norm*) only; the other calls refuse it with ORBQ_ERR_INVALID_ARG. */
 typedef enum { ORBQ_F32 = 0, ORBQ_BF16 = 1, ORBQ_F16 = 2 } orbq_dtype;
 
 /* Activation applied to the product before it is stored (Nunchaku / SVDQuant in Diffusers,
@@ -402,6 +402,74 @@ int orbq_kv_attention(const orbq_kv_cache* cache, const orbq_page_table* table, 
                       int64_t total, int32_t max_new, int64_t max_len, const void* q, int64_t q_token, int64_t q_head,
                       int32_t heads, void* o, int64_t o_token, int64_t o_head, float* lse, orbq_dtype type, float scale,
                       int32_t causal_block, int32_t window, void* workspace, size_t ws_bytes, void* stream);
+
+/* ==== norms around a block =====================================================================
+ * What a transformer block has before and after each of its branches: the branch's output y goes, normalised where
+ * the model says so, through its gate onto the residual stream x, and the stream, normalised and modulated, into the
+ * next branch.  For token rows i of group g (a sample, whose modulations they share):
+ *   u = y, or post(y) * post_weight;   r = x + gate[g] * u;   h = norm(r) * weight * (1 + scale[g]) + shift[g]
+ * r is the new stream, h the next branch's input.  A missing vector is 1 (gate, the weights) or 0 (scale, shift).
+ *   norm, post  ORBQ_NORM_LAYER (v - mean) / sqrt(mean of (v - mean)^2 + eps), ORBQ_NORM_RMS v / sqrt(mean of v^2 + eps),
+ *               or ORBQ_NORM_NONE: no h, or u = y
+ *   weight, post_weight  [device] [d] of weight_type, or NULL; only with their norm
+ *   gate, scale, shift   [device] [groups] rows of d entries of mod_type, `_ld` entries apart (0: one row for all
+ *               groups), so slices of a projection are taken where they lie; or NULL.  scale and shift only with a norm
+ *   cu          [device] int32[groups + 1], ascending: group g has rows cu[g] .. cu[g + 1] - 1; rows before cu[0] and from
+ *               cu[groups] on have none and are left alone (nothing written).  NULL: n / groups rows each.  The
+ *               array is read, never validated: whatever it holds, no access leaves the buffers
+ * Sums, statistics and products are in fp32, in an order that depends on d alone; r is rounded to stream_type, and h is
+ * taken from the rounded r, so that it is what a later reader of r would get; h is rounded once.  Squares are
+ * summed in fp32: magnitudes of 2^60 and above may overflow them. */
+typedef enum { ORBQ_NORM_NONE = 0, ORBQ_NORM_LAYER = 1, ORBQ_NORM_RMS = 2 } orbq_norm_kind;
+typedef struct {
+  orbq_norm_kind norm, post;
+  float eps, post_eps;
+  const void* weight;
+  const void* post_weight;
+  const void* gate;
+  const void* scale;
+  const void* shift;
+  int64_t gate_ld, scale_ld, shift_ld;
+  orbq_dtype weight_type, mod_type;
+  const int32_t* cu;
+  int32_t groups;
+} orbq_norms;
+
+/* x, r [device] [n] rows of d entries of stream_type; y, h of branch_type; each with its own row stride (in elements).
+ * stream_type == branch_type, or ORBQ_F32 with a branch of 16 bits; weight_type and mod_type any of the three.
+ *   y   NULL: there is no branch behind (post NONE, no gate, no post_weight; r is not written and h is taken from x)
+ *   r   NULL: not stored (h is the same);  r may be x, h may be y (same address and stride); other overlaps are undefined
+ * d in [1, 16384], n at most 2^30, groups at least 1 (and dividing n without cu).  Addresses and strides need their type's
+ * own alignment; 16-byte columns are used where d and all of them allow it. */
+int orbq_block_norm(const orbq_norms* norms, int64_t n, int32_t d, const void* x, int64_t x_ld, const void* y, int64_t y_ld,
+                    void* r, int64_t r_ld, void* h, int64_t h_ld, orbq_dtype stream_type, orbq_dtype branch_type, void* stream);
+
+/* Gradients of the vectors: rows of the types of the vectors themselves; NULL where not asked for.  `_ld` 0: one
+ * row, the sum over the groups (for a vector that they share); else a row for each group, zero where it has no rows.
+ * weight and post_weight: [d], sums over all rows. */
+typedef struct {
+  void* gate;
+  void* scale;
+  void* shift;
+  int64_t gate_ld, scale_ld, shift_ld;
+  void* weight;
+  void* post_weight;
+} orbq_norms_grads;
+
+/* The gradients of orbq_block_norm's inputs from those of its outputs, dr (what later uses of the stream say) and dh.
+ * `norms` as in the forward pass (shift is not read); r is its output, or x where there was no y.
+ *   dr   stream_type, NULL: zero;  dh  branch_type, given exactly where there is a norm
+ *   dx   stream_type; dy branch_type (only with y); NULL: not asked for.  dx may be dr or r, dy may be y or dh (same address
+ *        and stride); other overlaps are undefined.  Rows that have no group get zeros
+ *   grads  NULL: none asked for
+ *   workspace [device] >= orbq_block_norm_backward_workspace_bytes(n, d, groups), 16-byte aligned, where a vector's
+ *        gradient is asked for: sums over the rows of a group are taken in two steps, in one fixed order
+ * All sums are in fp32. */
+size_t orbq_block_norm_backward_workspace_bytes(int64_t n, int32_t d, int32_t groups);
+int orbq_block_norm_backward(const orbq_norms* norms, int64_t n, int32_t d, const void* r, int64_t r_ld, const void* y,
+                             int64_t y_ld, const void* dr, int64_t dr_ld, const void* dh, int64_t dh_ld, void* dx, int64_t dx_ld,
+                             void* dy, int64_t dy_ld, const orbq_norms_grads* grads, orbq_dtype stream_type,
+                             orbq_dtype branch_type, void* workspace, size_t ws_bytes, void* stream);
 
 /* Human-readable name of a status code, and the detail of the last error on this thread. */
 const char* orbq_status_string(int status);
