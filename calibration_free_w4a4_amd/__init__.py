@@ -28,8 +28,8 @@ __all__ = [
     "rpbh_quantize", "lut_gemm", "linear_workspace_bytes", "linear", "linear_noalloc", "test_rotate", "test_quantize_t",
     "test_mfma_rate",
     "F32", "BF16",
-    "Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_read", "kv_attention", "kv_attention_workspace_bytes",
-    "block_norm", "block_norm_backward", "NormGrads",
+    "Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_append_rope", "kv_read", "kv_attention",
+    "kv_attention_workspace_bytes", "block_norm", "block_norm_backward", "NormGrads",
 ]
 
 F32, BF16 = 0, 1
@@ -90,6 +90,8 @@ _SIGS = {
     "orbq_rht_passes": (ctypes.c_int32, [ctypes.c_float, ctypes.c_float, _I32, _I32]),
     "orbq_rope_apply": (ctypes.c_int, [_P, _P, _I64, _I64, _I32, _P, _I32, ctypes.c_int, _I32, _P]),
     "orbq_kv_append": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, ctypes.c_int, _P]),
+    "orbq_kv_append_rope": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _P, _P, _I64, _P, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _F,
+                                           ctypes.c_int, _P]),
     "orbq_kv_read": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, ctypes.c_int, _P]),
     "orbq_kv_attention_workspace_bytes": (ctypes.c_size_t, [_P, _I32, _I64, _I32, _I32, _I64, _I32, _I32]),
     "orbq_kv_attention": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _I64, _P, _I64, _I64, _I32, _P, _I64, _I64, _P,
@@ -460,7 +462,7 @@ def test_mfma_rate(workgroups: int, iters: int, sink=None, device=None) -> float
 
 
 # ------------------------------------------- the attention-side operators and the norms around a block
-_ATTENTION = ("Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_read", "kv_attention",
+_ATTENTION = ("Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_append_rope", "kv_read", "kv_attention",
               "kv_attention_workspace_bytes")
 
 

@@ -6,13 +6,14 @@ package the functions only check and marshal arguments; the work is liborbq's HI
     q, k = rope(r, positions, q, k)                        # gradients: rope_backward(r, positions, dq, dk)
     cache = KVCache.create(num_pages, kv_heads, head_dim)  # int8 codes, a scale for each page and head
     kv_append(cache, k, v, table, held)                    # quantise and write behind `held` tokens
+    q = kv_append_rope(cache, r, positions, q, k, v, table, held)   # both in one launch, and the norms of q and k
     o = kv_attention(cache, q, table, lens, causal_block=tokens_a_frame)
 
 Head tensors are [tokens, heads, head_dim] with the last dimension contiguous.
 
 Gradients: rope and rope_backward are part of the autograd graph (positions and frequencies are constants).  There is no
-gradient through the cache, whose entries are rounded: a backward pass that reaches kv_attention's output raises.  A call
-that is given `out` writes it and records nothing.
+gradient through the cache, whose entries are rounded: a backward pass that reaches the output of kv_attention or of
+kv_append_rope raises.  A call that is given `out` writes it and records nothing.
 """
 from __future__ import annotations
 
@@ -22,18 +23,18 @@ import struct
 
 from . import OrbqError, _check, load
 
-__all__ = ["Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_read", "kv_attention",
+__all__ = ["Rope", "rope", "rope_backward", "KVCache", "kv_append", "kv_append_rope", "kv_read", "kv_attention",
            "kv_attention_workspace_bytes"]
 
 # torch comes with the first Rope or KVCache, which every call takes: the package can be imported, with all its names,
 # where there is none.
 torch = None
 _TYPES = {}
-_Turned = _Attended = None  # autograd functions of rope and kv_attention
+_Turned = _Attended = _Appended = None  # autograd functions of rope, kv_attention and kv_append_rope
 
 
 def _need_torch() -> None:
-    global torch, _Turned, _Attended
+    global torch, _Turned, _Attended, _Appended
     if torch is not None:
         return
     import torch as t
@@ -69,8 +70,17 @@ def _need_torch() -> None:
         def backward(ctx, do):
             raise _bad("kv_attention", "there is no gradient through the 8-bit cache")
 
+    class Appended(t.autograd.Function):
+        @staticmethod
+        def forward(ctx, *args):
+            return kv_append_rope(*args)
+
+        @staticmethod
+        def backward(ctx, dq):
+            raise _bad("kv_append_rope", "there is no gradient: use rope where one is needed")
+
     _TYPES.update({t.float32: 0, t.bfloat16: 1, t.float16: 2})
-    _Turned, _Attended = Turned, Attended
+    _Turned, _Attended, _Appended = Turned, Attended, Appended
     torch = t
 
 
@@ -276,6 +286,58 @@ def kv_append(cache: KVCache, k, v, table, start, cu=None, max_new=None) -> None
     holds.  table int32 [batch, pages]; start int32 [batch]; cu int32 [batch + 1]: rows of each sequence (None:
     equal shares); max_new: no sequence has more (None: the most there can be)."""
     _move("kv_append", load().orbq_kv_append, cache, k, v, table, start, cu, max_new)
+
+
+def kv_append_rope(cache: KVCache, rope: Rope, positions, q, k, v, table, start, cu=None, max_new=None, q_weight=None,
+                   k_weight=None, eps: float = 1e-6, out=None):
+    """q turned by its positions, and k, turned, and v quantised and written behind the start[b] tokens that sequence b holds
+    (as rope, then kv_append; k is rounded once, to its codes).  q [total, heads, head_dim] or None; k, v [total,
+    kv_heads, head_dim]; positions float32 [total or a divisor of it, axes].  q_weight, k_weight: float32 [head_dim], the
+    weights of an RMS norm over each head before the turn (None: no norm), eps: its own.  table, start, cu, max_new as in
+    kv_append.  out: where to write q (q itself: in place)."""
+    func = "kv_append_rope"
+    if out is None and torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, q_weight)):
+        return _Appended.apply(cache, rope, positions, q, k, v, table, start, cu, max_new, q_weight, k_weight, eps)
+    dev = cache._device
+    if _current() != dev:
+        with torch.cuda.device(dev):
+            return kv_append_rope(cache, rope, positions, q, k, v, table, start, cu, max_new, q_weight, k_weight, eps, out)
+    t, batch, _ = _table(table, cache, func)
+    n, h, d, kt, kh, kp, code = _lay(k, func, "k")
+    nv, hv, dv, vt, vh, vp, code_v = _lay(v, func, "v")
+    if h != cache._kv_heads or d != cache._head_dim or (nv, hv, dv, code_v) != (n, h, d, code) or k.get_device() != dev or \
+            v.get_device() != dev:
+        raise _bad(func, f"k and v must be [tokens, {cache._kv_heads}, {cache._head_dim}] of one type on cuda:{dev}")
+    if rope._device != dev:
+        raise _bad(func, f"the frequencies must be on cuda:{dev}")
+    if positions.dtype != torch.float32 or positions.get_device() != dev or positions.dim() != 2 or \
+            positions.shape[1] != len(rope._dims) or not positions.is_contiguous():
+        raise _bad(func, f"positions must be contiguous float32 [tokens, {len(rope._dims)}] on cuda:{dev}")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.dtype != torch.float32 or w.get_device() != dev or w.shape != (d,) or not w.is_contiguous()):
+            raise _bad(func, f"{name} must be contiguous float32 [{d}] on cuda:{dev}")
+    heads = 0
+    if q is not None:
+        nq, hq, dq, qt, qh, qp, code_q = _lay(q, func, "q")
+        if (nq, dq, code_q) != (n, d, code) or q.get_device() != dev:
+            raise _bad(func, "q must agree with k in tokens, head_dim, type and device")
+        if out is None:
+            out, yt, yh = _like(q), hq * d, d
+        else:
+            yt, yh = _written(q, out, func)
+        heads = _HEADS.pack(qp, out.data_ptr(), hq, qt, qh, yt, yh)
+    elif out is not None or q_weight is not None:
+        raise _bad(func, "out or q_weight without q")
+    start = _ints(start, dev, batch, func, "start")
+    cu = 0 if cu is None else _ints(cu, dev, batch + 1, func, "cu")
+    if max_new is None:
+        max_new = n if cu else n // max(1, batch)
+    st = load().orbq_kv_append_rope(cache._packed, t, start, cu, n, max_new, rope._packed, positions.data_ptr(), positions.shape[0],
+                                    heads or None, 0 if q_weight is None else q_weight.data_ptr(), kp, kt, kh,
+                                    0 if k_weight is None else k_weight.data_ptr(), vp, vt, vh, eps, code, _stream(dev))
+    if st:
+        _check(st, "orbq_kv_append_rope")
+    return out
 
 
 def kv_read(cache: KVCache, table, first, cu, total: int, max_tokens=None, dtype=None, out=None):

@@ -59,6 +59,23 @@ struct KvTokens {         // the tokens of a call, packed: sequence b has rows c
 int launch_kv_append(const KvCache& c, const KvTokens& x, int dtype, hipStream_t stream);
 int launch_kv_read(const KvCache& c, const KvTokens& x, int dtype, hipStream_t stream);
 
+// what kv_append_rope does to q and k on the way
+struct TurnArgs {
+  const float* pos;    // [n_pos][axes]
+  const float* freqs;  // [pairs]
+  int64_t n_pos;
+  int32_t axes, pairs, halves, inverse;  // inverse: 0
+  int32_t ends[4];
+  const float* q_weight;  // [d] or NULL: no norm
+  const float* k_weight;
+  float eps;
+  RopeTensor q;  // heads 0: none
+};
+
+int launch_kv_append_rope_f32(const KvCache& c, const KvTokens& x, const TurnArgs& r, hipStream_t stream);
+int launch_kv_append_rope_bf16(const KvCache& c, const KvTokens& x, const TurnArgs& r, hipStream_t stream);
+int launch_kv_append_rope_f16(const KvCache& c, const KvTokens& x, const TurnArgs& r, hipStream_t stream);
+
 // ------------------------------------------------------------------------------------ attention
 struct AttnArgs {
   KvCache c;

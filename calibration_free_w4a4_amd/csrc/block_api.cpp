@@ -2,25 +2,16 @@
 // argument checks on the host, then asynchronous launches.
 #include <hip/hip_runtime.h>
 
-#include <cmath>
-
-#include "../../include/orbq.h"
+#include "attention_checks.h"
 #include "block_norm.h"
-#include "internal.h"
 
 #define ORBQ_API extern "C" __attribute__((visibility("default")))
 
 namespace {
 
+using namespace orbq::checks;
 using orbq::set_error;
 using orbq::set_ok;
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int hip_status(int e, const char* what) {
-  if (e != hipSuccess) return set_error(ORBQ_ERR_HIP, "%s: %s", what, hipGetErrorString(static_cast<hipError_t>(e)));
-  return set_ok();
-}
 
 bool known_type(int t) { return t == ORBQ_F32 || t == ORBQ_BF16 || t == ORBQ_F16; }
 bool known_norm(int k) { return k == ORBQ_NORM_NONE || k == ORBQ_NORM_LAYER || k == ORBQ_NORM_RMS; }
@@ -200,4 +191,46 @@ ORBQ_API int orbq_block_norm_backward(const orbq_norms* norms, int64_t n, int32_
                     fits(dx, dx_ld, ss) && fits(dy, dy_ld, bs);
   const orbq::NormGrads o{g.gate, g.scale, g.shift, g.gate_ld, g.scale_ld, g.shift_ld, g.weight, g.post_weight};
   return hip_status(orbq::launch_block_norm_backward(a, o, stream_type, branch_type, wide, static_cast<hipStream_t>(stream)), what);
+}
+
+ORBQ_API int orbq_kv_append_rope(const orbq_kv_cache* cache, const orbq_page_table* table, const int32_t* start,
+                                 const int32_t* cu, int64_t total, int32_t max_new, const orbq_rope* rope,
+                                 const float* positions, int64_t n_positions, const orbq_heads* q, const float* q_weight,
+                                 const void* k, int64_t k_token, int64_t k_head, const float* k_weight, const void* v,
+                                 int64_t v_token, int64_t v_head, float eps, orbq_dtype type, void* stream) {
+  const char* what = "orbq_kv_append_rope";
+  orbq::KvCache c;
+  orbq::TurnArgs r{};
+  int s;
+  if ((s = check_cache(cache, table, &c, what))) return s;
+  if ((s = check_rope(rope, c.d, type, &r, what))) return s;
+  if ((s = check_packed(total, max_new, c.batch, cu, what))) return s;
+  if (q && q->heads < 0) return set_error(ORBQ_ERR_INVALID_ARG, "%s: negative heads", what);
+  if (q && q->heads > 16384) return set_error(ORBQ_ERR_UNSUPPORTED, "%s: heads above 16384", what);
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return set_error(ORBQ_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", what);
+  if (!aligned(q_weight, 4) || !aligned(k_weight, 4)) return set_error(ORBQ_ERR_ALIGNMENT, "%s: weights misaligned", what);
+  if (total == 0 || max_new == 0) return set_ok();
+  if ((s = check_cache_buffers(c, what))) return s;
+  if ((s = check_positions(rope, positions, n_positions, total, &r, what))) return s;
+  if (!start) return set_error(ORBQ_ERR_INVALID_ARG, "%s: NULL start", what);
+  if (!aligned(start, 4)) return set_error(ORBQ_ERR_ALIGNMENT, "%s: start misaligned", what);
+  const int size = orbq::dtype_size(type);
+  if ((s = check_strided(k, k_token, k_head, size, 16, what))) return s;
+  if ((s = check_strided(v, v_token, v_head, size, 16, what))) return s;
+  if (q && q->heads) {
+    if ((s = check_strided(q->x, q->x_token, q->x_head, size, 16, what))) return s;
+    if ((s = check_strided(q->y, q->y_token, q->y_head, size, 16, what))) return s;
+    if ((s = check_written(q->y_token, q->y_head, total, q->heads, c.d, what))) return s;
+    r.q = orbq::RopeTensor{q->x, q->y, q->heads, q->x_token, q->x_head, q->y_token, q->y_head};
+  }
+  r.q_weight = q_weight;
+  r.k_weight = k_weight;
+  r.eps = eps;
+  const orbq::KvTokens x{cu, start, total, bound_rows(max_new, total), const_cast<void*>(k), const_cast<void*>(v),
+                         k_token, k_head, v_token, v_head};
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  return hip_status(type == ORBQ_F32    ? orbq::launch_kv_append_rope_f32(c, x, r, st)
+                    : type == ORBQ_BF16 ? orbq::launch_kv_append_rope_bf16(c, x, r, st)
+                                        : orbq::launch_kv_append_rope_f16(c, x, r, st),
+                    what);
 }

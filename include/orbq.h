@@ -271,8 +271,7 @@ int32_t orbq_rht_passes(float rho3, float rhoinf, int32_t d, int32_t vector_quan
 
 /* ==== attention-side operators ================================================================
  * What a transformer block has between its quantized QKV projection and its quantized output
- * projection (but for a normalisation of q and k, where a model has one): rotary positions over
- * several axes, a key/value cache in 8 bits, attention over it.
+ * projection: rotary positions over several axes, a key/value cache in 8 bits, attention over it.
  *
  * Head tensors are [token][head][head_dim] with the last dimension contiguous and any
  * non-negative token and head strides (in elements), so the parts of a fused projection are taken
@@ -361,6 +360,24 @@ typedef struct {
 int orbq_kv_append(const orbq_kv_cache* cache, const orbq_page_table* table, const int32_t* start, const int32_t* cu,
                    int64_t total, int32_t max_new, const void* k, int64_t k_token, int64_t k_head, const void* v,
                    int64_t v_token, int64_t v_head, orbq_dtype type, void* stream);
+
+/* orbq_kv_append with the positions' rotation on the way: one launch for what orbq_rope_apply on q and k and then
+ * orbq_kv_append do, with the norms of q and k that some models have before the rotation.  For each new token's heads
+ *   q' = turn(unit(q) * q_weight),  k' = turn(unit(k) * k_weight),  unit(x) = x / sqrt(mean of x^2 + eps)
+ * with the norm (over the head's entries) only where its weight is given; turn as in orbq_rope_apply.  q' is rounded to
+ * `type` and written; k' and v are quantised and written as orbq_kv_append says, k' from its fp32 value.
+ *   positions [device] float[n_positions][axes], row i of the packed rows uses positions[i % n_positions];
+ *             n_positions divides total
+ *   q       [host] a head tensor of `total` packed rows, its y written (y == x with the same strides: in place); NULL or
+ *           without heads: none
+ *   k, v    [device] head tensors of `total` packed rows;  q_weight, k_weight [device] float[head_dim] or NULL
+ * Addresses and strides of q, q', k and v are multiples of 16 bytes.  A sequence with a negative start, and tokens without
+ * a page, are not written to the cache; their q is turned all the same. */
+int orbq_kv_append_rope(const orbq_kv_cache* cache, const orbq_page_table* table, const int32_t* start, const int32_t* cu,
+                        int64_t total, int32_t max_new, const orbq_rope* rope, const float* positions, int64_t n_positions,
+                        const orbq_heads* q, const float* q_weight, const void* k, int64_t k_token, int64_t k_head,
+                        const float* k_weight, const void* v, int64_t v_token, int64_t v_head, float eps, orbq_dtype type,
+                        void* stream);
 
 /* Reads tokens first[b] .. of each sequence (cu gives how many) back as code * scale, rounded to `type`; tokens at
  * negative positions and of absent pages read as zero.

@@ -98,3 +98,36 @@ def test_workspace_bytes():
     assert f(1000, 64, 5) == f(1000, 64, 1) + 4 * 3 * 64 * 4           # a place more for each group
     assert f(10 ** 6, 64, 1) < 5000 * 3 * 64 * 4                      # chunks go by the card, not by the rows
     assert f(-1, 64, 1) == f(1, 0, 1) == f(1, 16385, 1) == f(1, 64, 0) == 0
+
+
+# ------------------------------------------------------------------------------------- kv_append_rope
+def append(c=None, t=None, start=P, cu=P, total=6, most=3, r=None, pos=P, n_pos=6, q=None, qw=None, k=P, kt=256, kh=128, kw=None, v=P,
+           vt=256, vh=128, eps=1e-6, dtype=1):
+    from tests.test_attention_abi import Structs, cache, table
+    c = None if c == "null" else ctypes.byref(cache(Structs, **(c or {})))
+    t = None if t == "null" else ctypes.byref(table(Structs, **(t or {})))
+    f = dict(axes=1, dims=(ctypes.c_int32 * 4)(128), freqs=P, layout=0)
+    f.update({} if r == "null" else r or {})
+    r = None if r == "null" else ctypes.byref(Structs._Rope(f["axes"], (ctypes.c_int32 * 4)(*f["dims"]), f["freqs"], f["layout"]))
+    h = dict(x=P, y=P, heads=4, x_token=512, x_head=128, y_token=512, y_head=128)
+    h.update({} if q == "null" else q or {})
+    q = None if q == "null" else ctypes.byref(Structs._Heads(*h.values()))
+    return orbq.load().orbq_kv_append_rope(c, t, start, cu, total, most, r, pos, n_pos, q, qw, k, kt, kh, kw, v, vt, vh, eps, dtype, None)
+
+
+def test_kv_append_rope():
+    from tests.test_attention_abi import CACHE_ERRORS
+    for c, t, want in CACHE_ERRORS:
+        assert append(c, t) == want, (c, t, orbq.load().orbq_last_error())
+    for kw, want in ((dict(c="null"), ARG), (dict(t="null"), ARG), (dict(r="null"), ARG), (dict(r=dict(axes=5)), UNSUPPORTED),
+                     (dict(r=dict(dims=(130, 0, 0, 0))), ARG), (dict(r=dict(dims=(33, 0, 0, 0))), ARG), (dict(r=dict(dims=(0, 0, 0, 0))), ARG),
+                     (dict(r=dict(layout=3)), ARG), (dict(r=dict(freqs=None)), ARG), (dict(pos=None), ARG), (dict(pos=P + 2), ALIGN),
+                     (dict(n_pos=0), ARG), (dict(n_pos=4), ARG), (dict(start=None), ARG), (dict(start=P + 2), ALIGN), (dict(cu=P + 1), ALIGN),
+                     (dict(cu=None, total=5), ARG), (dict(total=-1), ARG), (dict(most=-1), ARG), (dict(total=1 << 31), UNSUPPORTED),
+                     (dict(t=dict(batch=0)), ARG), (dict(k=None), ARG), (dict(v=None), ARG), (dict(k=P + 8), ALIGN), (dict(kt=260), ALIGN),
+                     (dict(vh=132), ALIGN), (dict(vt=-8), ARG), (dict(dtype=7), ARG), (dict(eps=-1.0), ARG), (dict(eps=float("inf")), ARG),
+                     (dict(qw=P + 2), ALIGN), (dict(kw=P + 1), ALIGN), (dict(q=dict(x=None)), ARG), (dict(q=dict(y=P + 8)), ALIGN),
+                     (dict(q=dict(heads=-1)), ARG), (dict(q=dict(heads=20000)), UNSUPPORTED), (dict(q=dict(y_head=64)), ARG),
+                     (dict(q=dict(y_token=64)), ARG), (dict(q=dict(x_token=-512)), ARG),
+                     (dict(total=0, start=None, k=None, pos=None, n_pos=0), OK), (dict(most=0, q="null", v=None), OK)):
+        assert append(**kw) == want, (kw, orbq.load().orbq_last_error())
