@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -83,6 +84,13 @@ _SIGS = {
     "orbq_linear_noalloc": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(_Rpbh), ctypes.POINTER(_Codebook), _F,
                                            _P, _P, ctypes.POINTER(_Codebook), _I64, ctypes.c_int, _P, ctypes.c_int, _I64,
                                            _P]),
+    "orbq_lut_gemm_fused": (ctypes.c_int, [_P, _P, ctypes.POINTER(_Codebook), _P, _P, ctypes.POINTER(_Codebook),
+                                           _I64, _I64, _I64, _P, _P, ctypes.c_int, _I64, _P]),
+    "orbq_linear_fused": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(_Rpbh), ctypes.POINTER(_Codebook), _F,
+                                         _P, _P, ctypes.POINTER(_Codebook), _I64, _P, ctypes.c_size_t, _P,
+                                         _P, ctypes.c_int, _I64, _P]),
+    "orbq_linear_a16_fused": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(_Rpbh), _P, _P, ctypes.POINTER(_Codebook),
+                                             _I64, _P, ctypes.c_size_t, _P, _P, ctypes.c_int, _I64, _P]),
     "orbq_rpbh_flatness": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P]),
     "orbq_linear_a16_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "orbq_linear_a16": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(_Rpbh), _P, _P, ctypes.POINTER(_Codebook),
@@ -295,19 +303,84 @@ def _act(act: str) -> int:
     return ACTIVATIONS[act]
 
 
+_EPILOGUE = struct.Struct("<i4xQi4xQi4xqQqQi4x")   # orbq_epilogue
+
+
+def _epilogue(torch, func, act: str, n: int, m: int, Y, bias, gate, residual, cu):
+    """The packed orbq_epilogue of a product Y [n, m]."""
+    dev = Y.device
+    y_type = _y_type(torch, Y)
+    kind = {torch.float32: F32, torch.bfloat16: BF16}
+    for t, name in ((bias, "bias"), (gate, "gate"), (residual, "residual")):
+        if t is not None and (t.device != dev or t.dtype not in kind or (t.shape[-1] > 1 and t.stride(-1) != 1)):
+            raise OrbqError(-1, func, f"{name} must be float32 or bfloat16 with contiguous rows on {dev}")
+    if bias is not None and bias.shape != (m,):
+        raise OrbqError(-1, func, f"bias must be [{m}], got {list(bias.shape)}")
+    if residual is not None and (residual.shape != (n, m) or residual.dtype != Y.dtype):
+        raise OrbqError(-1, func, f"residual must be [{n}, {m}] of the output's type, got {list(residual.shape)} of {residual.dtype}")
+    groups, gate_ld = 1, 0
+    if cu is not None:
+        if cu.dtype != torch.int32 or cu.device != dev or cu.dim() != 1 or cu.numel() < 2 or not cu.is_contiguous():
+            raise OrbqError(-1, func, f"cu must be contiguous int32 [groups + 1] on {dev}")
+        groups = cu.numel() - 1
+    elif gate is not None and gate.dim() == 2:
+        groups = max(1, gate.shape[0])
+    if gate is not None:
+        if gate.shape not in ((m,), (1, m), (groups, m)):
+            raise OrbqError(-1, func, f"gate must be [{m}] or [{groups}, {m}], got {list(gate.shape)}")
+        gate_ld = gate.stride(0) if gate.dim() == 2 and gate.shape[0] > 1 else 0
+    at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    of = lambda t: 0 if t is None else kind[t.dtype]  # noqa: E731
+    # a single row has no stride of its own: any that is wide enough and aligned does
+    ld = 0 if residual is None else residual.stride(0) if n > 1 else (m + 7) // 8 * 8
+    return _EPILOGUE.pack(_act(act), at(bias), of(bias), at(gate), of(gate), gate_ld, at(residual), ld, at(cu), groups)
+
+
+def _without_gradient(call):
+    """`call`, a product, in the autograd graph where its bias, gate or residual is: a backward pass that reaches it raises,
+    instead of leaving their gradients out."""
+    @functools.wraps(call)
+    def product(*args, **kw):
+        leaves = [kw.get(n) for n in ("bias", "gate", "residual")]
+        if not any(t is not None and t.requires_grad for t in leaves) or kw.get("out") is not None:
+            return call(*args, **kw)
+        torch = _torch()
+        if not torch.is_grad_enabled():
+            return call(*args, **kw)
+
+        class Product(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, *leaves):
+                return call(*args, **kw)
+
+            @staticmethod
+            def backward(ctx, dy):
+                raise OrbqError(-1, call.__name__, "there is no gradient through the quantized product")
+        return Product.apply(*leaves)
+    return product
+
+
+@_without_gradient
 @_on_its_device
 def lut_gemm(x_codes, x_norms, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook, d: int, out_dtype=None, out=None,
-             act: str = "none"):
-    """Y [n, m] = act(diag(s) C_a[x_codes] C_w[w_codes]^T diag(r')); act "none" calls
-    orbq_lut_gemm, "gelu_tanh" / "gelu_erf" orbq_lut_gemm_act."""
+             act: str = "none", *, bias=None, gate=None, residual=None, cu=None):
+    """Y [n, m] = residual + gate * act(diag(s) C_a[x_codes] C_w[w_codes]^T diag(r') + bias); without bias, gate, residual
+    and cu act "none" calls orbq_lut_gemm, "gelu_tanh" / "gelu_erf" orbq_lut_gemm_act, with one orbq_lut_gemm_fused.
+    bias [m]; gate [m] or [groups, m], a row for each group of tokens (n / groups each, or as cu int32 [groups + 1] says);
+    residual [n, m] of the output's type, `out` itself to add in place."""
     torch = _torch()
-    out_dtype = out_dtype or torch.float32
+    out_dtype = out_dtype or (torch.float32 if residual is None else residual.dtype)
     n, m = x_codes.shape[0], w_codes.shape[0]
     Y = out if out is not None else torch.empty((n, m), dtype=out_dtype, device=x_codes.device)
     a, w = cb_a.struct(), cb_w.struct()
     yt = _y_type(torch, Y)
     code = _act(act)
-    if code == 0:
+    if bias is not None or gate is not None or residual is not None or cu is not None:
+        e = _epilogue(torch, "lut_gemm", act, n, m, Y, bias, gate, residual, cu)
+        _check(load().orbq_lut_gemm_fused(x_codes.data_ptr(), x_norms.data_ptr(), ctypes.byref(a), w_codes.data_ptr(),
+                                          w_norms.data_ptr(), ctypes.byref(w), n, m, d, e, Y.data_ptr(), yt, Y.stride(0),
+                                          _stream(torch, x_codes.device)), "orbq_lut_gemm_fused")
+    elif code == 0:
         _check(load().orbq_lut_gemm(x_codes.data_ptr(), x_norms.data_ptr(), ctypes.byref(a), w_codes.data_ptr(),
                                     w_norms.data_ptr(), ctypes.byref(w), n, m, d, Y.data_ptr(), yt, Y.stride(0),
                                     _stream(torch, x_codes.device)), "orbq_lut_gemm")
@@ -318,14 +391,15 @@ def lut_gemm(x_codes, x_norms, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook,
     return Y
 
 
+@_without_gradient
 @_on_its_device
 def linear(X, rot: Rotation, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook, eps: float = 1e-8, out_dtype=None,
-           workspace=None, out=None, act: str = "none"):
-    """The online layer: Y [n, m] from bf16 tokens X [n, d] and folded weights (act as in
-    lut_gemm: "none" calls orbq_linear, a GELU form orbq_linear_act)."""
+           workspace=None, out=None, act: str = "none", *, bias=None, gate=None, residual=None, cu=None):
+    """The online layer: Y [n, m] from bf16 tokens X [n, d] and folded weights (act, bias, gate, residual and cu as in
+    lut_gemm: act "none" calls orbq_linear, a GELU form orbq_linear_act, with one of the others orbq_linear_fused)."""
     torch = _torch()
     _dev_tensor(X, torch.bfloat16, "linear")
-    out_dtype = out_dtype or torch.float32
+    out_dtype = out_dtype or (torch.float32 if residual is None else residual.dtype)
     n, d = X.shape
     m = w_codes.shape[0]
     need = linear_workspace_bytes(n, d, cb_a.bits)
@@ -336,7 +410,13 @@ def linear(X, rot: Rotation, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook, e
     yt = _y_type(torch, Y)
     ws_bytes = workspace.numel() * workspace.element_size()
     code = _act(act)
-    if code == 0:
+    if bias is not None or gate is not None or residual is not None or cu is not None:
+        e = _epilogue(torch, "linear", act, n, m, Y, bias, gate, residual, cu)
+        _check(load().orbq_linear_fused(X.data_ptr(), n, d, X.stride(0), ctypes.byref(r), ctypes.byref(a), eps,
+                                        w_codes.data_ptr(), w_norms.data_ptr(), ctypes.byref(w), m, workspace.data_ptr(),
+                                        ws_bytes, e, Y.data_ptr(), yt, Y.stride(0), _stream(torch, X.device)),
+               "orbq_linear_fused")
+    elif code == 0:
         _check(load().orbq_linear(X.data_ptr(), n, d, X.stride(0), ctypes.byref(r), ctypes.byref(a), eps,
                                   w_codes.data_ptr(), w_norms.data_ptr(), ctypes.byref(w), m, workspace.data_ptr(),
                                   ws_bytes, Y.data_ptr(), yt, Y.stride(0), _stream(torch, X.device)), "orbq_linear")
@@ -377,13 +457,15 @@ def linear_a16_workspace_bytes(n: int, d: int, m: int) -> int:
     return int(load().orbq_linear_a16_workspace_bytes(n, d, m))
 
 
+@_without_gradient
 @_on_its_device
-def linear_a16(X, rot: Rotation, w_codes, w_norms, cb_w: Codebook, out_dtype=None, workspace=None, out=None):
+def linear_a16(X, rot: Rotation, w_codes, w_norms, cb_w: Codebook, out_dtype=None, workspace=None, out=None, act: str = "none", *,
+               bias=None, gate=None, residual=None, cu=None):
     """Weight-only product: Y [n, m] from bf16 tokens X [n, d] (rotated, not quantized) and
-    folded weight codes (orbq_linear_a16)."""
+    folded weight codes (orbq_linear_a16; with act, bias, gate, residual or cu, as in lut_gemm, orbq_linear_a16_fused)."""
     torch = _torch()
     _dev_tensor(X, torch.bfloat16, "linear_a16")
-    out_dtype = out_dtype or torch.float32
+    out_dtype = out_dtype or (torch.float32 if residual is None else residual.dtype)
     n, d = X.shape
     m = w_codes.shape[0]
     need = linear_a16_workspace_bytes(n, d, m)
@@ -391,11 +473,17 @@ def linear_a16(X, rot: Rotation, w_codes, w_norms, cb_w: Codebook, out_dtype=Non
         workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=X.device)
     Y = out if out is not None else torch.empty((n, m), dtype=out_dtype, device=X.device)
     r, w = rot.struct(), cb_w.struct()
-    _check(load().orbq_linear_a16(X.data_ptr(), n, d, X.stride(0), ctypes.byref(r), w_codes.data_ptr(),
-                                  w_norms.data_ptr(), ctypes.byref(w), m, workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), Y.data_ptr(),
-                                  _y_type(torch, Y), Y.stride(0), _stream(torch, X.device)),
-           "orbq_linear_a16")
+    yt = _y_type(torch, Y)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    if bias is not None or gate is not None or residual is not None or cu is not None or _act(act):
+        e = _epilogue(torch, "linear_a16", act, n, m, Y, bias, gate, residual, cu)
+        _check(load().orbq_linear_a16_fused(X.data_ptr(), n, d, X.stride(0), ctypes.byref(r), w_codes.data_ptr(),
+                                            w_norms.data_ptr(), ctypes.byref(w), m, workspace.data_ptr(), ws_bytes, e,
+                                            Y.data_ptr(), yt, Y.stride(0), _stream(torch, X.device)), "orbq_linear_a16_fused")
+    else:
+        _check(load().orbq_linear_a16(X.data_ptr(), n, d, X.stride(0), ctypes.byref(r), w_codes.data_ptr(),
+                                      w_norms.data_ptr(), ctypes.byref(w), m, workspace.data_ptr(), ws_bytes, Y.data_ptr(), yt,
+                                      Y.stride(0), _stream(torch, X.device)), "orbq_linear_a16")
     return Y
 
 

@@ -20,11 +20,14 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liborbq.so")
 ARCH = os.environ.get("ORBQ_OFFLOAD_ARCH", "gfx950")
 
-SOURCES = ["lut_gemm_a4.hip", "lut_gemm_a6.hip", "lut_gemm_abf.hip", "lut_gemm_a2.hip", "lut_gemm_a3.hip",
+SOURCES = ["lut_gemm_fused_a4.hip", "lut_gemm_fused_a6.hip", "lut_gemm_fused_abf.hip", "lut_gemm_fused_a2.hip", "lut_gemm_fused_a3.hip",
+           "kv_append_rope_f32.hip", "kv_append_rope_bf16.hip", "kv_append_rope_f16.hip",
+           "lut_gemm_few_a2.hip", "lut_gemm_few_a3.hip", "lut_gemm_few_a4.hip", "lut_gemm_few_a6.hip", "lut_gemm_few.hip",
+           "lut_gemm_a4.hip", "lut_gemm_a6.hip", "lut_gemm_abf.hip", "lut_gemm_a2.hip", "lut_gemm_a3.hip",
            "rpbh_quantize_b128.hip", "rpbh_quantize_b64.hip", "rpbh_quantize_b256.hip", "rpbh_quantize_b512.hip",
            "rpbh_quantize_b1024.hip", "rpbh_quantize_b2048.hip", "rpbh_quantize_b4096.hip", "rpbh_quantize.hip", "a16_gemm.hip", "lut_gemm.hip", "flatness.hip", "noalloc.hip", "mfma_probe.hip",
            "rope.hip", "kv_cache.hip", "kv_attention_d64.hip", "kv_attention_d128.hip", "kv_attention_d256.hip", "kv_attention.hip",
-           "kv_append_rope_f32.hip", "kv_append_rope_bf16.hip", "kv_append_rope_f16.hip", "block_norm.hip", "block_norm_backward.hip",
+           "block_norm.hip", "block_norm_backward.hip",
            "api.cpp", "attention_api.cpp", "block_api.cpp",
            "codebook.cpp"]
 

@@ -1,7 +1,7 @@
 // a16_gemm: the weight-only product with bf16 activations (W{2,3,4,6}A16).
 #include <algorithm>
 
-#include "lut_gemm_kernel.h"
+#include "code_rows.h"
 
 namespace orbq {
 namespace lg {
@@ -18,17 +18,6 @@ namespace {
 // them 8 at a time in four MFMAs, each with the matching 16 bytes of x' (already in the
 // decoders' k order 0,2,4,6,1,3,5,7 within each 8).  The waves' partial sums meet in LDS, where they are added
 // in split order and scaled by r'.
-// A buffer resource from wave-uniform values, forced into scalar registers: the compiler keeps
-// values derived from 64-bit compares and selects in VGPRs, which would wrap every load that
-// uses the resource in a waterfall loop.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, uint32_t bytes) {
-  const uint64_t b = reinterpret_cast<uint64_t>(base);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32));
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0,
-                                           __builtin_amdgcn_readfirstlane(bytes), kBufWord3);
-}
-
 constexpr int kA16MaxSplits = 16;            // waves per workgroup, one K split each
 constexpr int kA16MaxCB = 5;                  // 16-row MFMA column blocks per workgroup (2 to 5)
 constexpr int kA16SS = 128;                   // codes per super-step
@@ -55,6 +44,9 @@ struct A16Args {
   float inv_scale;       // 1 / sqrt(h)
   uint32_t x_bytes;      // nt * ldx * 2 (< 2^31)
   uint32_t slice_off;
+  // more behind the product (orbq_linear_a16_fused)
+  int32_t fused, act;
+  EpilogueArgs e;
 };
 
 // x[i] += sgn * (x[i] in the DPP partner lane), for 8 registers, one v_fmac_f32_dpp each; the
@@ -154,68 +146,6 @@ __device__ __forceinline__ void a16_rotate_slice(const A16Args& a, int lane, int
   }
 }
 
-template <int BW>
-struct CodesA16;  // the 32 codes of one (row, super-step) lane slot and their decode
-
-template <>
-struct CodesA16<4> {
-  uint4 w;
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-    w = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
-  }
-  __device__ __forceinline__ uint4 get(int s, const Tab4& t, const void*) const {
-    const uint32_t x = s == 0 ? w.x : s == 1 ? w.y : s == 2 ? w.z : w.w;
-    return decode4_b(x, decode4_a(x, t));
-  }
-};
-
-template <>
-struct CodesA16<2> {
-  v2u_t w;
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-    w = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
-  }
-  __device__ __forceinline__ uint4 get(int s, const Tab4& t, const void*) const {
-    const uint32_t x = ((s < 2 ? w.x : w.y) >> (16 * (s & 1))) & 0xFFFFu;
-    return decode2_b(decode2_a(x, t), t);
-  }
-};
-
-template <>
-struct CodesA16<3> {
-  v2u_t a;
-  uint32_t b;
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-    a = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
-    b = __builtin_amdgcn_raw_buffer_load_b32(rs, off + 8, 0, 0);
-  }
-  __device__ __forceinline__ uint4 get(int s, const Tab4& t, const void*) const {
-    // 24 bits per 8 codes: s = 0 -> a.x [0, 24), 1 -> (a.x, a.y) [24, 48), 2 -> (a.y, b) [48, 72), 3 -> b [72, 96)
-    const uint32_t x = s == 0 ? a.x : s == 1 ? __builtin_amdgcn_alignbit(a.y, a.x, 24)
-                     : s == 2 ? __builtin_amdgcn_alignbit(b, a.y, 16) : (b >> 8);
-    return decode3_b(decode3_a(x, t), t);
-  }
-};
-
-template <>
-struct CodesA16<6> {
-  uint4 a;
-  v2u_t b;
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-    a = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
-    b = __builtin_amdgcn_raw_buffer_load_b64(rs, off + 16, 0, 0);
-  }
-  __device__ __forceinline__ uint4 get(int s, const Tab4&, const void* lut) const {
-    // 48 bits per 8 codes: s = 0 -> (a.x, a.y lo), 1 -> (a.y hi, a.z), 2 -> (a.w, b.x lo), 3 -> (b.x hi, b.y)
-    uint32_t lo, hi;
-    if (s == 0) { lo = a.x; hi = a.y & 0xFFFFu; }
-    else if (s == 1) { lo = __builtin_amdgcn_alignbit(a.z, a.y, 16); hi = a.z >> 16; }
-    else if (s == 2) { lo = a.w; hi = b.x & 0xFFFFu; }
-    else { lo = __builtin_amdgcn_alignbit(b.y, b.x, 16); hi = b.y >> 16; }
-    return decode6(lo, hi, static_cast<const uint32_t*>(lut));
-  }
-};
-
 template <int BW, bool OUT_BF16, int CB, bool ROT>
 __global__ __launch_bounds__(64 * kA16MaxSplits) void k_a16(A16Args a) {
   constexpr int kA16Rows = 16 * CB;  // weight rows of this workgroup
@@ -311,7 +241,8 @@ __global__ __launch_bounds__(64 * kA16MaxSplits) void k_a16(A16Args a) {
     float sum = 0.0f;
     for (int sp = 0; sp < a.splits; ++sp) sum += red[(sp * a.nt + t) * kA16Rows + rr];
     const float v = sum * __builtin_bit_cast(float, static_cast<uint32_t>(a.wn[j]) << 16);
-    if constexpr (OUT_BF16) reinterpret_cast<__bf16*>(a.Y)[t * a.ldy + j] = static_cast<__bf16>(v);
+    if (a.fused) finish_element(a.e, a.act, v, a.Y, a.ldy, OUT_BF16, t, j);
+    else if constexpr (OUT_BF16) reinterpret_cast<__bf16*>(a.Y)[t * a.ldy + j] = static_cast<__bf16>(v);
     else reinterpret_cast<float*>(a.Y)[t * a.ldy + j] = v;
   }
 }
@@ -404,14 +335,24 @@ void a16_setup(A16Args& a, int nt, int64_t d, const uint8_t* w_codes, const uint
   for (int i = 0; i < 32; ++i) a.mag[i] = dw.mag[i];
 }
 
+void a16_fuse(A16Args& a, const FusedRows* f, int y_bf16) {
+  if (!f) return;
+  a.fused = 1;
+  a.act = f->ep.act;
+  a.e = epilogue_args(f->ep, f->rows, f->row0, 0, y_bf16 ? 2 : 4);
+}
+
 size_t round16(size_t x) { return (x + 15) & ~size_t(15); }
 
 }  // namespace
 
-int launch_a16_gemm(const uint16_t* x_rot, int nt, int64_t d, const uint8_t* w_codes, const uint16_t* w_norms,
-                    const DecodeParams& dw, int64_t m, void* Y, int y_bf16, int64_t ldy, hipStream_t stream) {
+namespace {
+
+int launch_apart(const uint16_t* x_rot, int nt, int64_t d, const uint8_t* w_codes, const uint16_t* w_norms,
+                 const DecodeParams& dw, int64_t m, void* Y, int y_bf16, int64_t ldy, const FusedRows* fused, hipStream_t stream) {
   A16Args a{};
   a16_setup(a, nt, d, w_codes, w_norms, dw, m, Y, ldy);
+  a16_fuse(a, fused, y_bf16);
   a.xr = x_rot;
   a.xr_bytes = static_cast<uint32_t>(static_cast<int64_t>(nt) * d * 2);
   const int cb = a16_column_blocks(m, nt, a.splits);
@@ -431,13 +372,14 @@ int launch_a16_gemm(const uint16_t* x_rot, int nt, int64_t d, const uint8_t* w_c
 // 24.0 against 14.1.  For one RPBH pass with a permutation and h = 64 or 128, when X's extent
 // stays below 2^31 bytes and the x' slices (nt d bf16) fit in LDS beside the partial sums;
 // otherwise returns hipErrorNotSupported and the caller rotates in a launch of its own.
-int launch_a16_gemm_rot(const uint16_t* X, int64_t ldx, int nt, int64_t d, const int32_t* perm, const int8_t* signs,
-                        int32_t h, const uint8_t* w_codes, const uint16_t* w_norms, const DecodeParams& dw, int64_t m,
-                        void* Y, int y_bf16, int64_t ldy, hipStream_t stream) {
+int launch_rotating(const uint16_t* X, int64_t ldx, int nt, int64_t d, const int32_t* perm, const int8_t* signs, int32_t h,
+                    const uint8_t* w_codes, const uint16_t* w_norms, const DecodeParams& dw, int64_t m, void* Y, int y_bf16,
+                    int64_t ldy, const FusedRows* fused, hipStream_t stream) {
   if (!perm || (h != 64 && h != 128) || d % 128 || static_cast<int64_t>(nt) * ldx * 2 >= (int64_t(1) << 31))
     return static_cast<int>(hipErrorNotSupported);
   A16Args a{};
   a16_setup(a, nt, d, w_codes, w_norms, dw, m, Y, ldy);
+  a16_fuse(a, fused, y_bf16);
   if (nt * a.ss_per_split > 8) return static_cast<int>(hipErrorNotSupported);
   const int cb = a16_column_blocks(m, nt, a.splits);
   const size_t red = round16(static_cast<size_t>(a.splits) * nt * 16 * cb * sizeof(float));
@@ -455,6 +397,31 @@ int launch_a16_gemm_rot(const uint16_t* X, int64_t ldx, int nt, int64_t d, const
   const dim3 grid(static_cast<unsigned>((m + 16 * cb - 1) / (16 * cb))), blk(64 * a.splits);
   launch_cb<true>(cb, dw.bits, y_bf16 != 0, grid, blk, red + slices, stream, a);
   return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace
+
+int launch_a16_gemm(const uint16_t* x_rot, int nt, int64_t d, const uint8_t* w_codes, const uint16_t* w_norms,
+                    const DecodeParams& dw, int64_t m, void* Y, int y_bf16, int64_t ldy, hipStream_t stream) {
+  return launch_apart(x_rot, nt, d, w_codes, w_norms, dw, m, Y, y_bf16, ldy, nullptr, stream);
+}
+
+int launch_a16_gemm_rot(const uint16_t* X, int64_t ldx, int nt, int64_t d, const int32_t* perm, const int8_t* signs,
+                        int32_t h, const uint8_t* w_codes, const uint16_t* w_norms, const DecodeParams& dw, int64_t m,
+                        void* Y, int y_bf16, int64_t ldy, hipStream_t stream) {
+  return launch_rotating(X, ldx, nt, d, perm, signs, h, w_codes, w_norms, dw, m, Y, y_bf16, ldy, nullptr, stream);
+}
+
+int launch_a16_gemm_fused(const uint16_t* x_rot, int nt, int64_t d, const uint8_t* w_codes, const uint16_t* w_norms,
+                          const DecodeParams& dw, int64_t m, void* Y, int y_bf16, int64_t ldy, const FusedRows& fused,
+                          hipStream_t stream) {
+  return launch_apart(x_rot, nt, d, w_codes, w_norms, dw, m, Y, y_bf16, ldy, &fused, stream);
+}
+
+int launch_a16_gemm_rot_fused(const uint16_t* X, int64_t ldx, int nt, int64_t d, const int32_t* perm, const int8_t* signs,
+                              int32_t h, const uint8_t* w_codes, const uint16_t* w_norms, const DecodeParams& dw, int64_t m,
+                              void* Y, int y_bf16, int64_t ldy, const FusedRows& fused, hipStream_t stream) {
+  return launch_rotating(X, ldx, nt, d, perm, signs, h, w_codes, w_norms, dw, m, Y, y_bf16, ldy, &fused, stream);
 }
 
 }  // namespace orbq

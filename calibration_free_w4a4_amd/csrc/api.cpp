@@ -36,6 +36,11 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 bool supported_bits(int b) { return b == 2 || b == 3 || b == 4 || b == 6; }
 
+}  // namespace
+
+namespace orbq {
+namespace layer {
+
 int check_codebook(const orbq_codebook* cb, int64_t d, const char* what) {
   if (!cb) return fail(ORBQ_ERR_INVALID_ARG, "%s: codebook is NULL", what);
   if (!cb->centroids) return fail(ORBQ_ERR_INVALID_ARG, "%s: codebook centroids are NULL", what);
@@ -74,6 +79,13 @@ int check_dim(int64_t d, const char* what) {
   return ORBQ_OK;
 }
 
+}  // namespace layer
+}  // namespace orbq
+
+namespace {
+
+using namespace orbq::layer;
+
 int quant_params(const orbq_codebook* cb, orbq::QuantParams* qp, const char* what) {
   if (orbq::build_quant_params(cb->centroids, cb->bits, qp))
     return fail(ORBQ_ERR_CODEBOOK,
@@ -88,8 +100,10 @@ int hip_status(int e, const char* what) {
   return ok();
 }
 
+}  // namespace
+
 // shared by orbq_rpbh_quantize and orbq_fold_weights
-int quantize_rows(orbq::QuantMode mode, const void* X, int64_t n, int64_t d, int64_t ld, const orbq_rpbh* rot,
+int orbq::layer::quantize_rows(orbq::QuantMode mode, const void* X, int64_t n, int64_t d, int64_t ld, const orbq_rpbh* rot,
                   const orbq_codebook* cb, float eps, uint8_t* codes, void* norms, size_t norm_align,
                   void* stream, const char* what) {
   int s;
@@ -118,8 +132,6 @@ int quantize_rows(orbq::QuantMode mode, const void* X, int64_t n, int64_t d, int
                                            nullptr, static_cast<hipStream_t>(stream));
   return hip_status(e, what);
 }
-
-}  // namespace
 
 ORBQ_API int orbq_codebook_lloyd_max(int32_t d, int32_t bits, float* centroids_out) {
   if (!centroids_out) return fail(ORBQ_ERR_INVALID_ARG, "orbq_codebook_lloyd_max: output is NULL");
@@ -175,10 +187,8 @@ ORBQ_API int orbq_rpbh_quantize(const void* X, int64_t n, int64_t d, int64_t ldx
                        "orbq_rpbh_quantize");
 }
 
-namespace {
-
-int gemm_checks(const uint8_t* x_codes, const float* x_norms, const orbq_codebook* cb_a, const uint8_t* w_codes,
-                const void* w_norms, const orbq_codebook* cb_w, int64_t n, int64_t m, int64_t d, void* Y,
+int orbq::layer::check_product(const uint8_t* x_codes, const float* x_norms, const orbq_codebook* cb_a, const uint8_t* w_codes,
+                               const void* w_norms, const orbq_codebook* cb_w, int64_t n, int64_t m, int64_t d, void* Y,
                 orbq_dtype y_type, int64_t ldy, const char* what, bool check_x) {
   int s;
   if ((s = check_dim(d, what))) return s;
@@ -199,6 +209,8 @@ int gemm_checks(const uint8_t* x_codes, const float* x_norms, const orbq_codeboo
   if (!aligned(Y, 16) || (ldy * esz) % 16) return fail(ORBQ_ERR_ALIGNMENT, "%s: Y must be 16-byte aligned with a 16-byte pitch", what);
   return ORBQ_OK;
 }
+
+namespace {
 
 int gemm_launch(const uint8_t* x_codes, const float* x_norms, const orbq_codebook* cb_a, const uint8_t* w_codes,
                 const void* w_norms, const orbq_codebook* cb_w, int64_t n, int64_t m, int64_t d, void* Y,
@@ -223,12 +235,14 @@ bool valid_act(int act) { return act == ORBQ_ACT_NONE || act == ORBQ_ACT_GELU_TA
 constexpr int32_t kDecodedBits = 6;
 constexpr int64_t kDecodedMinM = 2048;
 
-size_t ws_codes_bytes(int64_t n, int64_t d, int32_t bits) {
+}  // namespace
+
+bool orbq::layer::keeps_centroids(int32_t bits_a, int64_t m) { return bits_a == kDecodedBits && m >= kDecodedMinM; }
+
+size_t orbq::layer::codes_bytes(int64_t n, int64_t d, int32_t bits) {
   const int64_t row = bits == kDecodedBits ? d * 2 : d * bits / 8;
   return (static_cast<size_t>(n) * static_cast<size_t>(row) + 255) & ~size_t(255);
 }
-
-}  // namespace
 
 ORBQ_API int orbq_lut_gemm_act(const uint8_t* x_codes, const float* x_norms, const orbq_codebook* cb_a,
                                const uint8_t* w_codes, const void* w_norms, const orbq_codebook* cb_w, int64_t n,
@@ -236,7 +250,7 @@ ORBQ_API int orbq_lut_gemm_act(const uint8_t* x_codes, const float* x_norms, con
                                void* stream) {
   const char* what = "orbq_lut_gemm_act";
   if (!valid_act(act)) return fail(ORBQ_ERR_INVALID_ARG, "%s: unknown activation %d", what, static_cast<int>(act));
-  int s = gemm_checks(x_codes, x_norms, cb_a, w_codes, w_norms, cb_w, n, m, d, Y, y_type, ldy, what, true);
+  int s = check_product(x_codes, x_norms, cb_a, w_codes, w_norms, cb_w, n, m, d, Y, y_type, ldy, what, true);
   if (s) return s;
   if (n == 0 || m == 0) return ok();
   return gemm_launch(x_codes, x_norms, cb_a, w_codes, w_norms, cb_w, n, m, d, Y, y_type, ldy, act, stream, what);
@@ -246,7 +260,7 @@ ORBQ_API int orbq_lut_gemm(const uint8_t* x_codes, const float* x_norms, const o
                            const uint8_t* w_codes, const void* w_norms, const orbq_codebook* cb_w, int64_t n, int64_t m,
                            int64_t d, void* Y, orbq_dtype y_type, int64_t ldy, void* stream) {
   const char* what = "orbq_lut_gemm";
-  int s = gemm_checks(x_codes, x_norms, cb_a, w_codes, w_norms, cb_w, n, m, d, Y, y_type, ldy, what, true);
+  int s = check_product(x_codes, x_norms, cb_a, w_codes, w_norms, cb_w, n, m, d, Y, y_type, ldy, what, true);
   if (s) return s;
   if (n == 0 || m == 0) return ok();
   return gemm_launch(x_codes, x_norms, cb_a, w_codes, w_norms, cb_w, n, m, d, Y, y_type, ldy, ORBQ_ACT_NONE, stream,
@@ -255,27 +269,27 @@ ORBQ_API int orbq_lut_gemm(const uint8_t* x_codes, const float* x_norms, const o
 
 ORBQ_API size_t orbq_linear_workspace_bytes(int64_t n, int64_t d, int32_t bits_a) {
   if (n < 0 || d <= 0 || !supported_bits(bits_a)) return 0;
-  return ws_codes_bytes(n, d, bits_a) + static_cast<size_t>(n) * sizeof(float);
+  return codes_bytes(n, d, bits_a) + static_cast<size_t>(n) * sizeof(float);
 }
 
-namespace {
-
 // the layer's argument checks, workspace aside
-int linear_args(const orbq_rpbh* rot, const orbq_codebook* cb_a, const uint8_t* w_codes, const void* w_norms,
+int orbq::layer::check_layer(const orbq_rpbh* rot, const orbq_codebook* cb_a, const uint8_t* w_codes, const void* w_norms,
                 const orbq_codebook* cb_w, int64_t n, int64_t m, int64_t d, int64_t ldx, void* Y, orbq_dtype y_type,
                 int64_t ldy, const char* what) {
-  int s = gemm_checks(nullptr, nullptr, cb_a, w_codes, w_norms, cb_w, n, m, d, Y, y_type, ldy, what, false);
+  int s = check_product(nullptr, nullptr, cb_a, w_codes, w_norms, cb_w, n, m, d, Y, y_type, ldy, what, false);
   if (s) return s;
   if ((s = check_rot(rot, d, what))) return s;
   if (ldx < d) return fail(ORBQ_ERR_INVALID_ARG, "%s: ldx < d", what);
   return ORBQ_OK;
 }
 
+namespace {
+
 int linear_impl(const void* X, int64_t n, int64_t d, int64_t ldx, const orbq_rpbh* rot, const orbq_codebook* cb_a,
                 float eps, const uint8_t* w_codes, const void* w_norms, const orbq_codebook* cb_w, int64_t m,
                 void* workspace, size_t ws_bytes, int act, void* Y, orbq_dtype y_type, int64_t ldy, void* stream,
                 const char* what) {
-  int s = linear_args(rot, cb_a, w_codes, w_norms, cb_w, n, m, d, ldx, Y, y_type, ldy, what);
+  int s = check_layer(rot, cb_a, w_codes, w_norms, cb_w, n, m, d, ldx, Y, y_type, ldy, what);
   if (s) return s;
   if (n == 0 || m == 0) return ok();
   const size_t need = orbq_linear_workspace_bytes(n, d, cb_a->bits);
@@ -283,8 +297,8 @@ int linear_impl(const void* X, int64_t n, int64_t d, int64_t ldx, const orbq_rpb
     return fail(ORBQ_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", what, ws_bytes, need);
   if (!aligned(workspace, 256)) return fail(ORBQ_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", what);
   uint8_t* codes = static_cast<uint8_t*>(workspace);
-  float* norms = reinterpret_cast<float*>(codes + ws_codes_bytes(n, d, cb_a->bits));
-  if (cb_a->bits == kDecodedBits && m >= kDecodedMinM) {
+  float* norms = reinterpret_cast<float*>(codes + codes_bytes(n, d, cb_a->bits));
+  if (keeps_centroids(cb_a->bits, m)) {
     // 6-bit activations: rpbh_quantize writes the bf16 centroids, the product stages them directly
     s = quantize_rows(orbq::QuantMode::kDecoded, X, n, d, ldx, rot, cb_a, eps, codes, norms, 4, stream, what);
     if (s) return s;
@@ -327,7 +341,7 @@ ORBQ_API int orbq_linear_noalloc(const void* X, int64_t n, int64_t d, int64_t ld
   const char* what = "orbq_linear_noalloc";
   if (!valid_act(act)) return fail(ORBQ_ERR_INVALID_ARG, "%s: unknown activation %d", what, static_cast<int>(act));
   // every argument is checked before the scratch is looked up (the lookup is a device call)
-  int s = linear_args(rot, cb_a, w_codes, w_norms, cb_w, n, m, d, ldx, Y, y_type, ldy, what);
+  int s = check_layer(rot, cb_a, w_codes, w_norms, cb_w, n, m, d, ldx, Y, y_type, ldy, what);
   if (s) return s;
   const size_t need = orbq_linear_workspace_bytes(n, d, cb_a->bits);
   if (need > ORBQ_NOALLOC_SCRATCH_BYTES)
@@ -353,14 +367,17 @@ int launch_a16_gemm_rot(const uint16_t* X, int64_t ldx, int nt, int64_t d, const
 
 namespace {
 
-constexpr int64_t kA16Tokens = 16;  // tokens per weight-only launch
-
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t orbq::layer::a16_tokens_bytes(int64_t n, int64_t d) { return round256(static_cast<size_t>(std::min(n, kA16Tokens) * d * 2)); }
+
+namespace {
 
 // [x' bf16 nt x d][norms fp32 nt]: the rotated tokens of one 16-token chunk (m does not enter)
 size_t a16_ws_bytes(int64_t n, int64_t d, int64_t /*m*/) {
-  const int64_t nt = std::min<int64_t>(n, kA16Tokens);
-  return round256(static_cast<size_t>(nt * d * 2)) + round256(static_cast<size_t>(nt * 4));
+  return a16_tokens_bytes(n, d) + round256(static_cast<size_t>(std::min(n, kA16Tokens) * 4));
 }
 
 }  // namespace
@@ -370,11 +387,9 @@ ORBQ_API size_t orbq_linear_a16_workspace_bytes(int64_t n, int64_t d, int64_t m)
   return a16_ws_bytes(std::max<int64_t>(n, 1), d, std::max<int64_t>(m, 1));
 }
 
-ORBQ_API int orbq_linear_a16(const void* X, int64_t n, int64_t d, int64_t ldx, const orbq_rpbh* rot,
-                             const uint8_t* w_codes, const void* w_norms, const orbq_codebook* cb_w, int64_t m,
-                             void* workspace, size_t ws_bytes, void* Y, orbq_dtype y_type, int64_t ldy,
-                             void* stream) {
-  const char* what = "orbq_linear_a16";
+int orbq::layer::check_a16(const void* X, int64_t n, int64_t d, int64_t ldx, const orbq_rpbh* rot, const uint8_t* w_codes,
+                           const void* w_norms, const orbq_codebook* cb_w, int64_t m, void* workspace, size_t ws_bytes, void* Y,
+                           orbq_dtype y_type, int64_t ldy, const char* what) {
   int s;
   if ((s = check_dim(d, what))) return s;
   if (d % 128) return fail(ORBQ_ERR_UNSUPPORTED, "%s: d=%lld not a multiple of 128", what, (long long)d);
@@ -382,7 +397,7 @@ ORBQ_API int orbq_linear_a16(const void* X, int64_t n, int64_t d, int64_t ldx, c
   if ((s = check_codebook(cb_w, d, what))) return s;
   if (n < 0 || m < 0 || ldx < d || ldy < m) return fail(ORBQ_ERR_INVALID_ARG, "%s: bad n, m, ldx or ldy", what);
   if (y_type != ORBQ_F32 && y_type != ORBQ_BF16) return fail(ORBQ_ERR_INVALID_ARG, "%s: bad y_type", what);
-  if (n == 0 || m == 0) return ok();
+  if (n == 0 || m == 0) return ORBQ_OK;
   if (!X || !w_codes || !w_norms || !Y) return fail(ORBQ_ERR_INVALID_ARG, "%s: NULL buffer", what);
   if (!aligned(X, 16) || (ldx * 2) % 16 || !aligned(w_codes, 16) || !aligned(w_norms, 2) ||
       !aligned(Y, y_type == ORBQ_BF16 ? 2 : 4))
@@ -391,11 +406,21 @@ ORBQ_API int orbq_linear_a16(const void* X, int64_t n, int64_t d, int64_t ldx, c
   if (!workspace || ws_bytes < need)
     return fail(ORBQ_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", what, ws_bytes, need);
   if (!aligned(workspace, 256)) return fail(ORBQ_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", what);
+  return ORBQ_OK;
+}
+
+ORBQ_API int orbq_linear_a16(const void* X, int64_t n, int64_t d, int64_t ldx, const orbq_rpbh* rot,
+                             const uint8_t* w_codes, const void* w_norms, const orbq_codebook* cb_w, int64_t m,
+                             void* workspace, size_t ws_bytes, void* Y, orbq_dtype y_type, int64_t ldy,
+                             void* stream) {
+  const char* what = "orbq_linear_a16";
+  const int s = check_a16(X, n, d, ldx, rot, w_codes, w_norms, cb_w, m, workspace, ws_bytes, Y, y_type, ldy, what);
+  if (s) return s;
+  if (n == 0 || m == 0) return ok();
   orbq::DecodeParams dw;
   orbq::build_decode_params(cb_w->centroids, cb_w->bits, &dw);
-  const int64_t nt_max = std::min<int64_t>(n, kA16Tokens);
   uint16_t* xr = static_cast<uint16_t*>(workspace);
-  float* norms = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + round256(static_cast<size_t>(nt_max * d * 2)));
+  float* norms = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + a16_tokens_bytes(n, d));
   orbq::RotArgs ra{rot->d, rot->block, rot->perm, rot->signs, rot->passes < 1 ? 1 : rot->passes};
   const int64_t esz = y_type == ORBQ_BF16 ? 2 : 4;
   const hipStream_t st = static_cast<hipStream_t>(stream);

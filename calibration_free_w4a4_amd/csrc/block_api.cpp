@@ -93,6 +93,42 @@ int64_t norm_places(int64_t n, int32_t d, int32_t groups, int32_t* chunk_rows) {
   return places ? places : 1;
 }
 
+// The epilogue of a product with n rows and m columns, into what the launchers take.  tiles: Y and the residual go in 16-byte
+// pieces, whose offsets within a tile have 32 bits.
+int check_epilogue(const orbq_epilogue* p, int64_t n, int64_t m, orbq_dtype y_type, int64_t ldy, bool tiles, orbq::ProductEpilogue* ep,
+                   const char* what) {
+  if (!p) return set_error(ORBQ_ERR_INVALID_ARG, "%s: epilogue is NULL", what);
+  if (p->act != ORBQ_ACT_NONE && p->act != ORBQ_ACT_GELU_TANH && p->act != ORBQ_ACT_GELU_ERF)
+    return set_error(ORBQ_ERR_INVALID_ARG, "%s: unknown activation %d", what, static_cast<int>(p->act));
+  const auto product_type = [](orbq_dtype t) { return t == ORBQ_F32 || t == ORBQ_BF16; };
+  if ((p->bias && !product_type(p->bias_type)) || (p->gate && !product_type(p->gate_type)))
+    return set_error(ORBQ_ERR_INVALID_ARG, "%s: bias and gate must be fp32 or bf16", what);
+  if (p->groups < 1) return set_error(ORBQ_ERR_INVALID_ARG, "%s: %d groups", what, p->groups);
+  if (p->groups > (1 << 30)) return set_error(ORBQ_ERR_UNSUPPORTED, "%s: more than 2^30 groups", what);
+  if (!p->cu && n % p->groups) return set_error(ORBQ_ERR_INVALID_ARG, "%s: without cu every group has n / groups rows", what);
+  if (p->gate && p->gate_ld < 0) return set_error(ORBQ_ERR_INVALID_ARG, "%s: negative stride of the gate", what);
+  if (p->residual && p->residual_ld < m) return set_error(ORBQ_ERR_INVALID_ARG, "%s: residual_ld < m", what);
+  const int esz = y_type == ORBQ_BF16 ? 2 : 4;
+  if (!aligned(p->cu, 4) || !aligned(p->bias, orbq::dtype_size(p->bias_type)) || !aligned(p->gate, orbq::dtype_size(p->gate_type)) ||
+      !aligned(p->residual, tiles ? 16 : esz) || (tiles && p->residual && p->residual_ld * esz % 16))
+    return set_error(ORBQ_ERR_ALIGNMENT, "%s: misaligned bias, gate, residual or cu", what);
+  if (tiles && (ldy > (1 << 21) || (p->residual && p->residual_ld > (1 << 21))))
+    return set_error(ORBQ_ERR_UNSUPPORTED, "%s: rows of Y or of the residual more than 2^21 entries apart", what);
+  *ep = orbq::ProductEpilogue{p->act, p->bias, p->gate, p->residual, p->gate_ld, p->residual_ld, p->bias_type == ORBQ_F32,
+                              p->gate_type == ORBQ_F32, p->cu, p->groups};
+  return ORBQ_OK;
+}
+
+int launch_product(const uint8_t* x_codes, const float* x_norms, const orbq::DecodeParams& da, const uint8_t* w_codes,
+                   const void* w_norms, const orbq_codebook* cb_w, int64_t n, int64_t m, int64_t d, void* Y, orbq_dtype y_type,
+                   int64_t ldy, const orbq::ProductEpilogue& ep, void* stream, const char* what) {
+  orbq::DecodeParams dw;
+  orbq::build_decode_params(cb_w->centroids, cb_w->bits, &dw);
+  const auto launch = da.bits != 16 && orbq::takes_few_rows(n, d) ? orbq::launch_lut_gemm_few : orbq::launch_lut_gemm_fused;
+  return hip_status(launch(x_codes, x_norms, da, w_codes, static_cast<const uint16_t*>(w_norms), dw, n, m, d, Y, y_type == ORBQ_BF16,
+                           ldy, ep, static_cast<hipStream_t>(stream)), what);
+}
+
 }  // namespace
 
 ORBQ_API int orbq_block_norm(const orbq_norms* norms, int64_t n, int32_t d, const void* x, int64_t x_ld, const void* y,
@@ -233,4 +269,78 @@ ORBQ_API int orbq_kv_append_rope(const orbq_kv_cache* cache, const orbq_page_tab
                     : type == ORBQ_BF16 ? orbq::launch_kv_append_rope_bf16(c, x, r, st)
                                         : orbq::launch_kv_append_rope_f16(c, x, r, st),
                     what);
+}
+
+ORBQ_API int orbq_lut_gemm_fused(const uint8_t* x_codes, const float* x_norms, const orbq_codebook* cb_a, const uint8_t* w_codes,
+                                 const void* w_norms, const orbq_codebook* cb_w, int64_t n, int64_t m, int64_t d,
+                                 const orbq_epilogue* epilogue, void* Y, orbq_dtype y_type, int64_t ldy, void* stream) {
+  const char* what = "orbq_lut_gemm_fused";
+  orbq::ProductEpilogue ep;
+  int s;
+  if ((s = orbq::layer::check_product(x_codes, x_norms, cb_a, w_codes, w_norms, cb_w, n, m, d, Y, y_type, ldy, what, true))) return s;
+  if ((s = check_epilogue(epilogue, n, m, y_type, ldy, true, &ep, what))) return s;
+  if (n == 0 || m == 0) return set_ok();
+  orbq::DecodeParams da;
+  orbq::build_decode_params(cb_a->centroids, cb_a->bits, &da);
+  return launch_product(x_codes, x_norms, da, w_codes, w_norms, cb_w, n, m, d, Y, y_type, ldy, ep, stream, what);
+}
+
+ORBQ_API int orbq_linear_fused(const void* X, int64_t n, int64_t d, int64_t ldx, const orbq_rpbh* rot, const orbq_codebook* cb_a,
+                               float eps, const uint8_t* w_codes, const void* w_norms, const orbq_codebook* cb_w, int64_t m,
+                               void* workspace, size_t ws_bytes, const orbq_epilogue* epilogue, void* Y, orbq_dtype y_type,
+                               int64_t ldy, void* stream) {
+  const char* what = "orbq_linear_fused";
+  orbq::ProductEpilogue ep;
+  int s;
+  if ((s = orbq::layer::check_layer(rot, cb_a, w_codes, w_norms, cb_w, n, m, d, ldx, Y, y_type, ldy, what))) return s;
+  if ((s = check_epilogue(epilogue, n, m, y_type, ldy, true, &ep, what))) return s;
+  if (n == 0 || m == 0) return set_ok();
+  const size_t need = orbq_linear_workspace_bytes(n, d, cb_a->bits);
+  if (!workspace || ws_bytes < need)
+    return set_error(ORBQ_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", what, workspace ? ws_bytes : 0, need);
+  if (!aligned(workspace, 256)) return set_error(ORBQ_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", what);
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  float* norms = reinterpret_cast<float*>(codes + orbq::layer::codes_bytes(n, d, cb_a->bits));
+  // 6-bit activations as in orbq_linear; few rows are decoded once for each 16 weight rows of a workgroup either way
+  const bool decoded = orbq::layer::keeps_centroids(cb_a->bits, m) && !orbq::takes_few_rows(n, d);
+  const orbq::QuantMode mode = decoded ? orbq::QuantMode::kDecoded : orbq::QuantMode::kActivations;
+  if ((s = orbq::layer::quantize_rows(mode, X, n, d, ldx, rot, cb_a, eps, codes, norms, 4, stream, what))) return s;
+  orbq::DecodeParams da{};
+  da.bits = 16;
+  if (!decoded) orbq::build_decode_params(cb_a->centroids, cb_a->bits, &da);
+  return launch_product(codes, norms, da, w_codes, w_norms, cb_w, n, m, d, Y, y_type, ldy, ep, stream, what);
+}
+
+ORBQ_API int orbq_linear_a16_fused(const void* X, int64_t n, int64_t d, int64_t ldx, const orbq_rpbh* rot, const uint8_t* w_codes,
+                                   const void* w_norms, const orbq_codebook* cb_w, int64_t m, void* workspace, size_t ws_bytes,
+                                   const orbq_epilogue* epilogue, void* Y, orbq_dtype y_type, int64_t ldy, void* stream) {
+  const char* what = "orbq_linear_a16_fused";
+  orbq::ProductEpilogue ep;
+  int s;
+  if ((s = orbq::layer::check_a16(X, n, d, ldx, rot, w_codes, w_norms, cb_w, m, workspace, ws_bytes, Y, y_type, ldy, what))) return s;
+  if ((s = check_epilogue(epilogue, n, m, y_type, ldy, false, &ep, what))) return s;
+  if (n == 0 || m == 0) return set_ok();
+  orbq::DecodeParams dw;
+  orbq::build_decode_params(cb_w->centroids, cb_w->bits, &dw);
+  uint16_t* xr = static_cast<uint16_t*>(workspace);
+  float* norms = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + orbq::layer::a16_tokens_bytes(n, d));
+  const orbq::RotArgs ra{rot->d, rot->block, rot->perm, rot->signs, rot->passes < 1 ? 1 : rot->passes};
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const int bf16 = y_type == ORBQ_BF16;
+  const uint16_t* wn = static_cast<const uint16_t*>(w_norms);
+  for (int64_t t0 = 0; t0 < n; t0 += orbq::layer::kA16Tokens) {
+    const int nt = static_cast<int>(n - t0 < orbq::layer::kA16Tokens ? n - t0 : orbq::layer::kA16Tokens);
+    const uint16_t* x = static_cast<const uint16_t*>(X) + t0 * ldx;
+    void* y = static_cast<unsigned char*>(Y) + t0 * ldy * (bf16 ? 2 : 4);
+    const orbq::FusedRows rows{ep, t0, n};
+    int e = ra.passes == 1 ? orbq::launch_a16_gemm_rot_fused(x, ldx, nt, d, ra.perm, ra.signs, ra.block, w_codes, wn, dw, m, y, bf16, ldy, rows, st)
+                           : static_cast<int>(hipErrorNotSupported);
+    if (e == hipErrorNotSupported) {  // the rotation in a launch of its own
+      e = orbq::launch_rpbh_quantize(orbq::QuantMode::kRotateBf16, x, nt, ldx, ra, nullptr, 0.0f, nullptr, norms,
+                                     reinterpret_cast<float*>(xr), st);
+      if (e == hipSuccess) e = orbq::launch_a16_gemm_fused(xr, nt, d, w_codes, wn, dw, m, y, bf16, ldy, rows, st);
+    }
+    if (e != hipSuccess) return hip_status(e, what);
+  }
+  return set_ok();
 }

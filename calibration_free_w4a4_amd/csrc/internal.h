@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/orbq.h"
+
 namespace orbq {
 
 // api.cpp: records the detail that orbq_last_error returns (of this host thread) and gives back
@@ -98,5 +100,63 @@ int launch_lut_gemm(const uint8_t* x_codes, const float* x_norms, const DecodePa
                     const uint8_t* w_codes, const uint16_t* w_norms, const DecodeParams& dw,
                     int64_t n, int64_t m, int64_t d, void* Y, int y_bf16, int64_t ldy,
                     int act, hipStream_t stream);
+
+// The checks and steps of the layer's entry points (api.cpp); each returns a status and says what it is about.
+namespace layer {
+int check_dim(int64_t d, const char* what);
+int check_rot(const orbq_rpbh* rot, int64_t d, const char* what);
+int check_codebook(const orbq_codebook* cb, int64_t d, const char* what);
+int check_product(const uint8_t* x_codes, const float* x_norms, const orbq_codebook* cb_a, const uint8_t* w_codes,
+                  const void* w_norms, const orbq_codebook* cb_w, int64_t n, int64_t m, int64_t d, void* Y,
+                  orbq_dtype y_type, int64_t ldy, const char* what, bool check_x);
+int check_layer(const orbq_rpbh* rot, const orbq_codebook* cb_a, const uint8_t* w_codes, const void* w_norms,
+                const orbq_codebook* cb_w, int64_t n, int64_t m, int64_t d, int64_t ldx, void* Y, orbq_dtype y_type,
+                int64_t ldy, const char* what);
+int check_a16(const void* X, int64_t n, int64_t d, int64_t ldx, const orbq_rpbh* rot, const uint8_t* w_codes, const void* w_norms,
+              const orbq_codebook* cb_w, int64_t m, void* workspace, size_t ws_bytes, void* Y, orbq_dtype y_type, int64_t ldy,
+              const char* what);
+int quantize_rows(QuantMode mode, const void* X, int64_t n, int64_t d, int64_t ld, const orbq_rpbh* rot,
+                  const orbq_codebook* cb, float eps, uint8_t* codes, void* norms, size_t norm_align, void* stream,
+                  const char* what);
+// the layer keeps its activations' bf16 centroids instead of their codes
+bool keeps_centroids(int32_t bits_a, int64_t m);
+size_t codes_bytes(int64_t n, int64_t d, int32_t bits);  // of the codes in the layer's workspace
+constexpr int64_t kA16Tokens = 16;                       // tokens per weight-only launch
+size_t a16_tokens_bytes(int64_t n, int64_t d);           // of the rotated tokens in its workspace
+}  // namespace layer
+
+// What the fused products do behind the scaled product: Y = residual + gate[group] act(. + bias).
+struct ProductEpilogue {
+  int act;
+  const void* bias;
+  const void* gate;
+  const void* residual;  // of Y's type
+  int64_t gate_ld, residual_ld;
+  int bias_f32, gate_f32;  // else bf16
+  const int32_t* cu;
+  int32_t groups;
+};
+
+// the rows of a call that a launch of at most 16 has
+struct FusedRows {
+  const ProductEpilogue& ep;
+  int64_t row0, rows;  // the launch's first, and how many the call has
+};
+int launch_a16_gemm_fused(const uint16_t* x_rot, int nt, int64_t d, const uint8_t* w_codes, const uint16_t* w_norms,
+                          const DecodeParams& dw, int64_t m, void* Y, int y_bf16, int64_t ldy, const FusedRows& fused,
+                          hipStream_t stream);
+int launch_a16_gemm_rot_fused(const uint16_t* X, int64_t ldx, int nt, int64_t d, const int32_t* perm, const int8_t* signs,
+                              int32_t h, const uint8_t* w_codes, const uint16_t* w_norms, const DecodeParams& dw, int64_t m,
+                              void* Y, int y_bf16, int64_t ldy, const FusedRows& fused, hipStream_t stream);
+
+int launch_lut_gemm_fused(const uint8_t* x_codes, const float* x_norms, const DecodeParams& da, const uint8_t* w_codes,
+                          const uint16_t* w_norms, const DecodeParams& dw, int64_t n, int64_t m, int64_t d, void* Y,
+                          int y_bf16, int64_t ldy, const ProductEpilogue& ep, hipStream_t stream);
+
+// The form for few token rows, whose sums are in another order.
+bool takes_few_rows(int64_t n, int64_t d);
+int launch_lut_gemm_few(const uint8_t* x_codes, const float* x_norms, const DecodeParams& da, const uint8_t* w_codes,
+                        const uint16_t* w_norms, const DecodeParams& dw, int64_t n, int64_t m, int64_t d, void* Y,
+                        int y_bf16, int64_t ldy, const ProductEpilogue& ep, hipStream_t stream);
 
 }  // namespace orbq

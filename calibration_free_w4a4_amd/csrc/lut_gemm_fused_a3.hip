@@ -1,0 +1,12 @@
+// lut_gemm kernels with the fused epilogue for 3-bit activation codes.
+#include "lut_gemm_kernel.h"
+
+namespace orbq {
+namespace lg {
+
+hipError_t launch_fused_a3(int bw, int cfg, bool out_bf16, const FusedArgs& a, int grid, size_t lds, hipStream_t st) {
+  return launch_ba<3>(bw, cfg, out_bf16, a, grid, lds, st);
+}
+
+}  // namespace lg
+}  // namespace orbq

@@ -41,6 +41,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 
@@ -51,6 +52,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int v2u_t __attribute__((ext_vector_type(2)));
+typedef unsigned int v4u_t __attribute__((ext_vector_type(4)));
 
 constexpr int KT = 64;          // K tile (codes)
 constexpr int kRow = KT * 2;    // bytes of one staged bf16 row
@@ -76,6 +78,7 @@ struct Cfg {
 };
 
 struct GemmArgs {
+  static constexpr bool kFused = false;
   const uint8_t* xc;
   const float* xs;
   const uint8_t* wc;
@@ -91,6 +94,23 @@ struct GemmArgs {
   uint32_t lt_lo_a, lt_hi_a, ht_lo_a, ht_hi_a;
   uint32_t lt_lo_w, lt_hi_w, ht_lo_w, ht_hi_w;
   uint16_t mag_a[32], mag_w[32];
+};
+
+// What more a product's epilogue may do: Y = residual + gate[group] act(product + bias).
+struct EpilogueArgs {
+  const void* bias;      // [m] or NULL, fp32 or bf16
+  const void* gate;      // [groups] rows gld apart (0: one row for all), or NULL
+  const void* residual;  // [n][ldr] of Y's type, or NULL; may be Y itself
+  int64_t gld, ldr;
+  int32_t bias_f32, gate_f32;
+  const int32_t* cu;     // [groups + 1]: rows of the groups, the others are left alone; NULL: equal shares of all rows
+  int32_t groups;
+  int64_t row_base, rows;  // of the launch's first row in the call, and of the call
+};
+
+struct FusedArgs : GemmArgs {
+  static constexpr bool kFused = true;
+  EpilogueArgs e;
 };
 
 // ----------------------------------------------------------------------------- decoders
@@ -354,8 +374,203 @@ struct ActTag {
 // chunk swizzle of a staged row: chunk c of row r sits at c ^ ((r >> 1) & 7)
 __device__ __forceinline__ uint32_t swz(uint32_t r) { return (r >> 1) & 7; }
 
-template <int BA, int BW, bool OUT_BF16, int BM, int BN>
-__global__ __launch_bounds__(kThreads) void k_lut_gemm(GemmArgs a) {
+__device__ __forceinline__ float as_float(uint16_t bf16) { return __builtin_bit_cast(float, static_cast<uint32_t>(bf16) << 16); }
+__device__ __forceinline__ float entry_of(const void* p, int f32, int64_t at) {
+  return f32 ? static_cast<const float*>(p)[at] : as_float(static_cast<const uint16_t*>(p)[at]);
+}
+
+// Group of row `row` of the call, or -1 for a row that no group has (whatever cu holds, within [-1, groups)).
+__device__ __forceinline__ int32_t group_of_row(const EpilogueArgs& a, int64_t row) {
+  if (!a.cu) return a.groups == 1 ? 0 : static_cast<int32_t>(row / (a.rows / a.groups));
+  if (row < a.cu[0]) return -1;
+  int32_t lo = 1, hi = a.groups + 1;  // the first i with cu[i] > row lies in [lo, hi]
+  while (lo < hi) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (a.cu[mid] > row) hi = mid;
+    else lo = mid + 1;
+  }
+  return hi > a.groups ? -1 : hi - 1;
+}
+
+// One element of the few-row products: v is the product, scaled.
+__device__ __forceinline__ void finish_element(const EpilogueArgs& e, int act, float v, void* Y, int64_t ldy, bool bf16, int64_t row, int64_t col) {
+  const int32_t group = e.gate || e.cu ? group_of_row(e, e.row_base + row) : 0;
+  if (group < 0) return;
+  if (e.bias) v += entry_of(e.bias, e.bias_f32, col);
+  if (act == kActGeluTanh) v = gelu_tanh(v);
+  else if (act == kActGeluErf) v = gelu_erf(v);
+  if (e.gate) v *= entry_of(e.gate, e.gate_f32, group * e.gld + col);
+  if (e.residual) v += entry_of(e.residual, !bf16, row * e.ldr + col);
+  if (bf16) static_cast<__bf16*>(Y)[row * ldy + col] = static_cast<__bf16>(v);
+  else static_cast<float*>(Y)[row * ldy + col] = v;
+}
+
+// The epilogue with bias, activation, gate and residual.  Accumulators hold a column a lane, 32 rows of it; a wave turns
+// them, a 32-row block at a time, through its part of the LDS that held the operands, so that a lane then has 16 bytes of
+// a row of Y: the residual comes and Y goes in whole 16-byte pieces, and scales, bias and gate are read from LDS by
+// rows.  A tile whose rows have one group takes its gate from LDS, others from memory.
+template <int BM, int BN> struct FusedLds {
+  static constexpr int LD = BN / 2 + 8;  // floats of a turned row: the lanes' two halves, 4 rows apart, meet no bank twice
+  static constexpr int kStage = 32 * LD * 4;  // bytes of a wave's block
+  static constexpr int kBytes = 8 * kStage + (2 * BM + 3 * BN) * 4;
+};
+
+// Some columns of a wave's turned block, from part_col on, P pieces of E entries (16 bytes of Y) wide, P a power of two: a lane has
+// one piece of every R-th row, so that its columns, and with them its scales, bias and gate, stay the same.  The residual
+// is fetched four rows ahead.
+template <bool OUT_BF16, int BM, int BN, int P>
+__device__ __forceinline__ void fused_part(const FusedArgs& a, const float* stage, const float* vectors, int part_col, int block_row,
+                                           __amdgpu_buffer_rsrc_t ys, __amdgpu_buffer_rsrc_t rs, int rows, int cols, int64_t row0,
+                                           int64_t col0, bool one_group) {
+  using F = FusedLds<BM, BN>;
+  constexpr int esz = OUT_BF16 ? 2 : 4, E = 16 / esz, R = 64 / P, ITS = 32 / R, G = ITS < 4 ? ITS : 4;
+  const EpilogueArgs& o = a.e;
+  const int lane = threadIdx.x & 63, wn = threadIdx.x >> 8;
+  const int lrow = lane / P, lcol = part_col + lane % P * E, col = wn * (BN / 2) + lcol, row = block_row + lrow;
+  const float *scale = vectors + row, *rn = vectors + BM + col, *bias = rn + BN, *gate = bias + BN;
+  const int32_t* groups = reinterpret_cast<const int32_t*>(vectors + BM + 3 * BN) + row;
+  const float* from = stage + lrow * F::LD + lcol;
+  const uint32_t yoff = static_cast<uint32_t>((row * a.ldy + col) * esz), roff = static_cast<uint32_t>((row * o.ldr + col) * esz);
+  const bool whole = col + E <= cols;
+  float w[E], b[E], g[E];
+#pragma unroll
+  for (int c = 0; c < E; ++c) {
+    w[c] = rn[c];
+    b[c] = bias[c];
+    g[c] = gate[c];
+  }
+  const auto fetch = [&](int it, v4u_t (&to)[G]) {
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      to[k] = v4u_t{0, 0, 0, 0};
+      if (o.residual && whole && row + (it + k) * R < rows)
+        to[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, roff + static_cast<uint32_t>((it + k) * R * o.ldr * esz), 0, 0);
+    }
+  };
+  v4u_t res[G], next[G];
+  fetch(0, res);
+#pragma unroll 1
+  for (int it = 0; it < ITS; it += G) {
+    if (it + G < ITS) fetch(it + G, next);
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      const int down = (it + k) * R;
+      float v[E];
+      const float s = scale[down];
+#pragma unroll
+      for (int q = 0; q < E; q += 4) {
+        const f32x4_t t = *reinterpret_cast<const f32x4_t*>(from + down * F::LD + q);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[q + c] = __builtin_fmaf(t[c] * s, w[q + c], b[q + c]);
+      }
+      if (a.act == kActGeluTanh) {
+#pragma unroll
+        for (int c = 0; c < E; ++c) v[c] = gelu_tanh(v[c]);
+      } else if (a.act == kActGeluErf) {
+#pragma unroll
+        for (int c = 0; c < E; ++c) v[c] = gelu_erf(v[c]);
+      }
+      if (row + down >= rows) continue;
+      if (one_group) {
+#pragma unroll
+        for (int c = 0; c < E; ++c) v[c] *= g[c];
+      } else {
+        const int32_t group = groups[down];
+        if (group < 0) continue;
+#pragma unroll
+        for (int c = 0; c < E; ++c)
+          if (o.gate && col + c < cols) v[c] *= entry_of(o.gate, o.gate_f32, group * o.gld + col0 + col + c);
+      }
+      if (whole) {
+        v4u_t out;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if constexpr (OUT_BF16) {
+            typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+            const bf16x2_t p = {static_cast<__bf16>(v[2 * c] + __builtin_bit_cast(float, res[k][c] << 16)),
+                                static_cast<__bf16>(v[2 * c + 1] + __builtin_bit_cast(float, res[k][c] & 0xffff0000u))};
+            out[c] = __builtin_bit_cast(uint32_t, p);
+          } else {
+            out[c] = __builtin_bit_cast(uint32_t, v[c] + __builtin_bit_cast(float, static_cast<uint32_t>(res[k][c])));
+          }
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(out, ys, yoff + static_cast<uint32_t>(down * a.ldy * esz), 0, kYStorePolicy);
+      } else {  // the row ends inside the piece
+#pragma unroll
+        for (int c = 0; c < E; ++c) {
+          if (col + c >= cols) continue;
+          const int64_t yat = (row0 + row + down) * a.ldy + col0 + col + c;
+          if (o.residual) v[c] += entry_of(o.residual, !OUT_BF16, (row0 + row + down) * o.ldr + col0 + col + c);
+          if constexpr (OUT_BF16) static_cast<__bf16*>(a.Y)[yat] = static_cast<__bf16>(v[c]);
+          else static_cast<float*>(a.Y)[yat] = v[c];
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < G; ++k) res[k] = next[k];
+  }
+}
+
+template <bool OUT_BF16, int BM, int BN>
+__device__ __forceinline__ void fused_epilogue(const FusedArgs& a, f32x16_t (&acc)[Cfg<BM, BN>::TI][Cfg<BM, BN>::TJ], int64_t row0,
+                                               int64_t col0, unsigned char* smem) {
+  using C = Cfg<BM, BN>;
+  using F = FusedLds<BM, BN>;
+  const EpilogueArgs& o = a.e;
+  const int tid = threadIdx.x;
+  int32_t group = 0;
+  if (o.gate || o.cu) {
+    group = group_of_row(o, o.row_base + row0);
+    if (group != group_of_row(o, o.row_base + min(row0 + BM, a.n) - 1)) group = -1;
+  }
+  const bool one_group = group >= 0;  // the same for the whole workgroup
+  float* scale = reinterpret_cast<float*>(smem + 8 * F::kStage);
+  float *rn = scale + BM, *bias = rn + BN, *gate = bias + BN;
+  int32_t* groups = reinterpret_cast<int32_t*>(gate + BN);
+  __syncthreads();  // the operands are read
+  for (int i = tid; i < BM; i += kThreads) {
+    scale[i] = a.xs[min(row0 + i, a.n - 1)];
+    if (!one_group) groups[i] = row0 + i < a.n ? group_of_row(o, o.row_base + row0 + i) : -1;
+  }
+  for (int i = tid; i < BN; i += kThreads) {
+    const int64_t col = min(col0 + i, a.m - 1);
+    rn[i] = as_float(a.wn[col]);
+    bias[i] = o.bias ? entry_of(o.bias, o.bias_f32, col) : 0.0f;
+    gate[i] = one_group && o.gate ? entry_of(o.gate, o.gate_f32, group * o.gld + col) : 1.0f;
+  }
+  __syncthreads();
+  constexpr int esz = OUT_BF16 ? 2 : 4, E = 16 / esz;
+  const int lane = tid & 63, wave = tid >> 6, wm = wave & 3;
+  float* stage = reinterpret_cast<float*>(smem + wave * F::kStage);
+  const __amdgpu_buffer_rsrc_t ys = __builtin_amdgcn_make_buffer_rsrc(
+      static_cast<unsigned char*>(a.Y) + (row0 * a.ldy + col0) * esz, 0, 0xFFFFFFF0u, kBufWord3);
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<unsigned char*>(static_cast<const unsigned char*>(o.residual) + (o.residual ? (row0 * o.ldr + col0) * esz : 0)), 0,
+      0xFFFFFFF0u, kBufWord3);
+  const int rows = static_cast<int>(min<int64_t>(BM, a.n - row0)), cols = static_cast<int>(min<int64_t>(BN, a.m - col0));
+#pragma unroll
+  for (int i = 0; i < C::TI; ++i) {
+    const int block_row = wm * C::TM + 32 * i;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the last block is read
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+#pragma unroll
+      for (int j = 0; j < C::TJ; ++j)
+        stage[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * F::LD + 32 * j + (lane & 31)] = acc[i][j][r];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // widths of a power of two: 128, or 64 and 32
+    if constexpr (C::TN == 128) {
+      fused_part<OUT_BF16, BM, BN, 128 / E>(a, stage, scale, 0, block_row, ys, rs, rows, cols, row0, col0, one_group);
+    } else {
+      static_assert(C::TN == 96, "");
+      fused_part<OUT_BF16, BM, BN, 64 / E>(a, stage, scale, 0, block_row, ys, rs, rows, cols, row0, col0, one_group);
+      fused_part<OUT_BF16, BM, BN, 32 / E>(a, stage, scale, 64, block_row, ys, rs, rows, cols, row0, col0, one_group);
+    }
+  }
+}
+
+template <int BA, int BW, bool OUT_BF16, int BM, int BN, class Args>
+__global__ __launch_bounds__(kThreads) void k_lut_gemm(Args a) {
   using C = Cfg<BM, BN>;
   extern __shared__ __align__(16) unsigned char smem[];
   // LDS: [A stage 0][A stage 1][B stage 0][B stage 1][6-bit tables]
@@ -583,6 +798,9 @@ __global__ __launch_bounds__(kThreads) void k_lut_gemm(GemmArgs a) {
     ktile(1, s0, f, v + 1);  // MFMAs on tile v + 1, decode of tile v + 2
   }
 
+  if constexpr (Args::kFused) {
+    fused_epilogue<OUT_BF16, BM, BN>(a, acc, row0, col0, smem);
+  } else {
   // ---- epilogue: D[row][col] of a 32x32 tile: col = lane % 32, row = 8*(r/4) + 4*(lane/32) + r%4
   // (the activation is a uniform kernel argument: one branch selects the epilogue's variant)
   auto epilogue = [&](auto tag) {
@@ -681,25 +899,26 @@ __global__ __launch_bounds__(kThreads) void k_lut_gemm(GemmArgs a) {
     case kActGeluErf: epilogue(ActTag<kActGeluErf>{}); break;
     default: epilogue(ActTag<kActNone>{}); break;
   }
+  }
 }
 
-template <int BA, int BW, int BM, int BN>
-inline hipError_t launch_cfg(bool out_bf16, const GemmArgs& a, int grid, size_t lds, hipStream_t st) {
+template <int BA, int BW, int BM, int BN, class Args>
+inline hipError_t launch_cfg(bool out_bf16, const Args& a, int grid, size_t lds, hipStream_t st) {
   if (out_bf16)
-    hipLaunchKernelGGL((k_lut_gemm<BA, BW, true, BM, BN>), dim3(grid), dim3(kThreads), lds, st, a);
+    hipLaunchKernelGGL((k_lut_gemm<BA, BW, true, BM, BN, Args>), dim3(grid), dim3(kThreads), lds, st, a);
   else
-    hipLaunchKernelGGL((k_lut_gemm<BA, BW, false, BM, BN>), dim3(grid), dim3(kThreads), lds, st, a);
+    hipLaunchKernelGGL((k_lut_gemm<BA, BW, false, BM, BN, Args>), dim3(grid), dim3(kThreads), lds, st, a);
   return hipGetLastError();
 }
 
-template <int BA, int BW>
-inline hipError_t launch_bw(int cfg, bool out_bf16, const GemmArgs& a, int grid, size_t lds, hipStream_t st) {
+template <int BA, int BW, class Args>
+inline hipError_t launch_bw(int cfg, bool out_bf16, const Args& a, int grid, size_t lds, hipStream_t st) {
   return cfg == 0 ? launch_cfg<BA, BW, 384, 192>(out_bf16, a, grid, lds, st)
                   : launch_cfg<BA, BW, 256, 256>(out_bf16, a, grid, lds, st);
 }
 
-template <int BA>
-inline hipError_t launch_ba(int bw, int cfg, bool out_bf16, const GemmArgs& a, int grid, size_t lds, hipStream_t st) {
+template <int BA, class Args>
+inline hipError_t launch_ba(int bw, int cfg, bool out_bf16, const Args& a, int grid, size_t lds, hipStream_t st) {
   if constexpr (BA == 3) {
     return launch_bw<3, 3>(cfg, out_bf16, a, grid, lds, st);  // 3-bit pairs only with 3-bit
   } else {
@@ -732,12 +951,45 @@ inline void tab4(const DecodeParams& dp, uint32_t* lt_lo, uint32_t* lt_hi, uint3
   *ht_hi = h[1];
 }
 
+// rows from r0 and columns from c0 of a call of n rows
+inline EpilogueArgs epilogue_args(const ProductEpilogue& ep, int64_t n, int64_t r0, int64_t c0, int64_t esz) {
+  const auto behind = [](const void* p, int64_t bytes) { return p ? static_cast<const char*>(p) + bytes : nullptr; };
+  EpilogueArgs e{};
+  e.bias = behind(ep.bias, c0 * (ep.bias_f32 ? 4 : 2));
+  e.gate = behind(ep.gate, c0 * (ep.gate_f32 ? 4 : 2));
+  e.residual = behind(ep.residual, (r0 * ep.residual_ld + c0) * esz);
+  e.gld = ep.gate_ld;
+  e.ldr = ep.residual_ld;
+  e.bias_f32 = ep.bias_f32;
+  e.gate_f32 = ep.gate_f32;
+  e.cu = ep.cu;
+  e.groups = ep.groups;
+  e.row_base = r0;
+  e.rows = n;
+  return e;
+}
+
 // Launchers of one activation bit width (lut_gemm_a<BA>.hip).
 hipError_t launch_gemm_a2(int bw, int cfg, bool out_bf16, const GemmArgs& a, int grid, size_t lds, hipStream_t st);
 hipError_t launch_gemm_a3(int bw, int cfg, bool out_bf16, const GemmArgs& a, int grid, size_t lds, hipStream_t st);
 hipError_t launch_gemm_a4(int bw, int cfg, bool out_bf16, const GemmArgs& a, int grid, size_t lds, hipStream_t st);
 hipError_t launch_gemm_a6(int bw, int cfg, bool out_bf16, const GemmArgs& a, int grid, size_t lds, hipStream_t st);
 hipError_t launch_gemm_abf(int bw, int cfg, bool out_bf16, const GemmArgs& a, int grid, size_t lds, hipStream_t st);
+// and with the fused epilogue (lut_gemm_fused_a<BA>.hip)
+hipError_t launch_fused_a2(int bw, int cfg, bool out_bf16, const FusedArgs& a, int grid, size_t lds, hipStream_t st);
+hipError_t launch_fused_a3(int bw, int cfg, bool out_bf16, const FusedArgs& a, int grid, size_t lds, hipStream_t st);
+hipError_t launch_fused_a4(int bw, int cfg, bool out_bf16, const FusedArgs& a, int grid, size_t lds, hipStream_t st);
+hipError_t launch_fused_a6(int bw, int cfg, bool out_bf16, const FusedArgs& a, int grid, size_t lds, hipStream_t st);
+hipError_t launch_fused_abf(int bw, int cfg, bool out_bf16, const FusedArgs& a, int grid, size_t lds, hipStream_t st);
+
+// Tile shape (0: 384 x 192, 1: 256 x 256), LDS bytes, and the arguments of a call that all its launches share.
+struct GemmPlan {
+  int cfg, bm, bn;
+  size_t lds;
+};
+GemmPlan plan_gemm(const DecodeParams& da, const DecodeParams& dw, int64_t n, int64_t m, int64_t d, GemmArgs* a);
+// b's rows r0 .. r0 + rows - 1 and columns c0 .. c0 + cols - 1 of the call, for one launch; its workgroups
+int part_of(const GemmPlan& p, const GemmArgs& a, int64_t r0, int64_t rows, int64_t c0, int64_t cols, int64_t esz, GemmArgs* b);
 
 }  // namespace lg
 }  // namespace orbq

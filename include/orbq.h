@@ -249,6 +249,47 @@ int orbq_linear_a16(const void* X, int64_t n, int64_t d, int64_t ldx, const orbq
                     void* workspace, size_t ws_bytes, void* Y, orbq_dtype y_type, int64_t ldy,
                     void* stream);
 
+/* What a block does behind a product, in the product's own epilogue:
+ *   Y[i][j] = residual[i][j] + gate[g(i)][j] * act(product[i][j] + bias[j])
+ * in fp32 behind the scaled fp32 product, rounded once to y_type.  A missing part is left out.
+ *   bias      [device] [m], fp32 or bf16 (bias_type), or NULL
+ *   gate      [device] [groups] rows of m entries, fp32 or bf16 (gate_type), gate_ld entries apart (0: one row for all), or
+ *             NULL; g(i) is the group of token row i
+ *   residual  [device] [n][residual_ld] of y_type, or NULL; it may be Y itself (same address and pitch: Y += ...), other
+ *             overlaps are undefined
+ *   cu        [device] int32[groups + 1], ascending: group g has rows cu[g] .. cu[g + 1] - 1, the others are left alone
+ *             (nothing written); read, never validated.  NULL: n / groups rows each
+ *   groups    at least 1 (also without a gate)
+ * Alignment: bias, gate and cu naturally; the residual 16 bytes, its pitch a multiple of 16 (orbq_linear_a16_fused:
+ * naturally).  In orbq_lut_gemm_fused and orbq_linear_fused rows of Y and of the residual are at most 2^21 entries apart. */
+typedef struct {
+  orbq_activation act;
+  const void* bias;
+  orbq_dtype bias_type;
+  const void* gate;
+  orbq_dtype gate_type;
+  int64_t gate_ld;
+  const void* residual;
+  int64_t residual_ld;
+  const int32_t* cu;
+  int32_t groups;
+} orbq_epilogue;
+
+/* orbq_lut_gemm, orbq_linear and orbq_linear_a16 with that epilogue; arguments and errors as theirs.  With more than 64
+ * token rows, or d not a multiple of 128, the product's sums are orbq_lut_gemm's, and an epilogue without bias, gate and
+ * residual gives orbq_lut_gemm_act's bits; fewer rows take a form of their own, bound by the weights' bytes, whose sums are
+ * in another order.  orbq_linear_a16_fused's products are orbq_linear_a16's. */
+int orbq_lut_gemm_fused(const uint8_t* x_codes, const float* x_norms, const orbq_codebook* cb_a, const uint8_t* w_codes,
+                        const void* w_norms, const orbq_codebook* cb_w, int64_t n, int64_t m, int64_t d,
+                        const orbq_epilogue* epilogue, void* Y, orbq_dtype y_type, int64_t ldy, void* stream);
+int orbq_linear_fused(const void* X, int64_t n, int64_t d, int64_t ldx, const orbq_rpbh* rot, const orbq_codebook* cb_a,
+                      float eps, const uint8_t* w_codes, const void* w_norms, const orbq_codebook* cb_w, int64_t m,
+                      void* workspace, size_t ws_bytes, const orbq_epilogue* epilogue, void* Y, orbq_dtype y_type,
+                      int64_t ldy, void* stream);
+int orbq_linear_a16_fused(const void* X, int64_t n, int64_t d, int64_t ldx, const orbq_rpbh* rot, const uint8_t* w_codes,
+                          const void* w_norms, const orbq_codebook* cb_w, int64_t m, void* workspace, size_t ws_bytes,
+                          const orbq_epilogue* epilogue, void* Y, orbq_dtype y_type, int64_t ldy, void* stream);
+
 /* The adaptive check ("Quantizing With Randomized Hadamard Transforms", gist.science,
  * "Method": an O(d) look at the input's l3 norm, for scalar quantization, or its l_inf
  * norm, for vector quantization, decides whether 1, 2 or 3 composed transforms are needed).

@@ -131,3 +131,62 @@ def test_kv_append_rope():
                      (dict(q=dict(y_token=64)), ARG), (dict(q=dict(x_token=-512)), ARG),
                      (dict(total=0, start=None, k=None, pos=None, n_pos=0), OK), (dict(most=0, q="null", v=None), OK)):
         assert append(**kw) == want, (kw, orbq.load().orbq_last_error())
+
+
+# ------------------------------------------------------------------------------- products with an epilogue
+class Epilogue(ctypes.Structure):
+    """orbq_epilogue as include/orbq.h declares it."""
+    _fields_ = [("act", ctypes.c_int), ("bias", ctypes.c_void_p), ("bias_type", ctypes.c_int), ("gate", ctypes.c_void_p),
+                ("gate_type", ctypes.c_int), ("gate_ld", ctypes.c_int64), ("residual", ctypes.c_void_p), ("residual_ld", ctypes.c_int64),
+                ("cu", ctypes.c_void_p), ("groups", ctypes.c_int32)]
+
+
+def test_the_binding_packs_the_epilogue_as_declared():
+    assert orbq._EPILOGUE.size == ctypes.sizeof(Epilogue)
+    values = (2, 1 << 40, 1, 3, 0, 4, 5, 6, 7, 8)
+    got = Epilogue.from_buffer_copy(orbq._EPILOGUE.pack(*values))
+    assert tuple(getattr(got, f[0]) for f in Epilogue._fields_) == values
+
+
+EPILOGUE_ERRORS = [
+    ("null", ARG), (dict(act=3), ARG), (dict(bias_type=F16), ARG), (dict(gate_type=7), ARG), (dict(groups=0), ARG), (dict(groups=3), ARG),
+    (dict(gate_ld=-1), ARG), (dict(residual_ld=63), ARG), (dict(bias=P + 2), ALIGN), (dict(gate=P + 1, gate_type=BF16), ALIGN),
+    (dict(cu=P + 2), ALIGN), (dict(residual=P + 2), ALIGN)]
+
+
+def epilogue(e):
+    f = dict(act=0, bias=P, bias_type=F32, gate=P, gate_type=F32, gate_ld=64, residual=P, residual_ld=64, cu=None, groups=2)
+    f.update(e or {})
+    return Epilogue(*f.values())
+
+
+def test_products(cb):
+    lib, d = orbq.load(), 256
+    c = orbq.Codebook.from_centroids(d, 4, cb(d, 4)).struct()
+    rot = orbq._Rpbh(d, 64, 0x1000, 0x2000)
+    by = ctypes.byref
+
+    def gemm(e=None, y=P, ldy=64, yt=0, n=8, x=P):
+        return lib.orbq_lut_gemm_fused(x, P, by(c), P, P, by(c), n, 64, d, None if e == "null" else by(epilogue(e)), y, yt, ldy, None)
+
+    def linear(e=None, ws_bytes=1 << 30, y=P, ldy=64, yt=0, n=8, ws=P):
+        return lib.orbq_linear_fused(P, n, d, d, by(rot), by(c), 1e-8, P, P, by(c), 64, ws, ws_bytes,
+                                     None if e == "null" else by(epilogue(e)), y, yt, ldy, None)
+
+    def a16(e=None, ws_bytes=1 << 30, y=P, ldy=64, yt=0, n=8, ws=P):
+        return lib.orbq_linear_a16_fused(P, n, d, d, by(rot), P, P, by(c), 64, ws, ws_bytes,
+                                         None if e == "null" else by(epilogue(e)), y, yt, ldy, None)
+
+    for f in (gemm, linear, a16):
+        for e, want in EPILOGUE_ERRORS:
+            assert f(e) == want, (f, e, lib.orbq_last_error())
+        for kw, want in ((dict(ldy=63), ARG), (dict(yt=2), ARG), (dict(n=-1), ARG), (dict(y=None), ARG), (dict(y=P + 2), ALIGN),
+                         (dict(n=0, y=None), OK)):
+            assert f(**kw) == want, (f, kw, lib.orbq_last_error())
+    for f in (gemm, linear):          # 16-byte pieces, 32-bit offsets within a tile
+        for e, want in ((dict(residual=P + 4), ALIGN), (dict(residual_ld=66), ALIGN), (dict(residual_ld=1 << 22), UNSUPPORTED)):
+            assert f(e) == want, (f, e, lib.orbq_last_error())
+        assert f(ldy=1 << 22) == UNSUPPORTED
+    for f in (linear, a16):
+        assert f(ws_bytes=16) == WORKSPACE and f(ws=None) == WORKSPACE and f(ws=P + 16) == ALIGN
+    assert gemm(x=None) == ARG
