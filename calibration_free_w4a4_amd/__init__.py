@@ -57,6 +57,10 @@ class _Codebook(ctypes.Structure):
     _fields_ = [("d", ctypes.c_int32), ("bits", ctypes.c_int32), ("centroids", ctypes.POINTER(ctypes.c_float))]
 
 
+# the same as bytes, for the entry points that take their structs packed
+_RPBH = struct.Struct("<iiQQi4x")
+_CODEBOOK = struct.Struct("<iiQ")
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -84,13 +88,11 @@ _SIGS = {
     "orbq_linear_noalloc": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(_Rpbh), ctypes.POINTER(_Codebook), _F,
                                            _P, _P, ctypes.POINTER(_Codebook), _I64, ctypes.c_int, _P, ctypes.c_int, _I64,
                                            _P]),
-    "orbq_lut_gemm_fused": (ctypes.c_int, [_P, _P, ctypes.POINTER(_Codebook), _P, _P, ctypes.POINTER(_Codebook),
-                                           _I64, _I64, _I64, _P, _P, ctypes.c_int, _I64, _P]),
-    "orbq_linear_fused": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(_Rpbh), ctypes.POINTER(_Codebook), _F,
-                                         _P, _P, ctypes.POINTER(_Codebook), _I64, _P, ctypes.c_size_t, _P,
+    "orbq_lut_gemm_fused": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, ctypes.c_int, _I64, _P]),
+    "orbq_linear_fused": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _F, _P, _P, _P, _I64, _P, ctypes.c_size_t, _P,
                                          _P, ctypes.c_int, _I64, _P]),
-    "orbq_linear_a16_fused": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(_Rpbh), _P, _P, ctypes.POINTER(_Codebook),
-                                             _I64, _P, ctypes.c_size_t, _P, _P, ctypes.c_int, _I64, _P]),
+    "orbq_linear_a16_fused": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P, ctypes.c_size_t, _P, _P,
+                                             ctypes.c_int, _I64, _P]),
     "orbq_rpbh_flatness": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P]),
     "orbq_linear_a16_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "orbq_linear_a16": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.POINTER(_Rpbh), _P, _P, ctypes.POINTER(_Codebook),
@@ -200,6 +202,10 @@ class Rotation:
         dperm = None if perm is None else torch.from_numpy(perm).to(dev)
         return cls(d, block, dperm, torch.from_numpy(signs).to(dev), passes)
 
+    def packed(self) -> bytes:
+        """The C struct's bytes."""
+        return _RPBH.pack(self.d, self.block, 0 if self.perm is None else self.perm.data_ptr(), self.signs.data_ptr(), self.passes)
+
     def struct(self) -> _Rpbh:
         return _Rpbh(self.d, self.block, 0 if self.perm is None else self.perm.data_ptr(), self.signs.data_ptr(),
                      self.passes)
@@ -222,6 +228,17 @@ class Codebook:
         if c.shape != (1 << bits,):
             raise OrbqError(-1, "Codebook", f"need {1 << bits} centroids")
         return cls(d, bits, c)
+
+    def packed(self) -> bytes:
+        """The C struct's bytes, which point at the live float32 array."""
+        c = self.centroids
+        kept = self.__dict__.get("_bytes")
+        if kept is not None and kept[0] is c and kept[1] == (self.d, self.bits):
+            return kept[3]
+        live = np.ascontiguousarray(c, dtype=np.float32)
+        b = _CODEBOOK.pack(self.d, self.bits, live.__array_interface__["data"][0])
+        self._bytes = (c if live is c else None, (self.d, self.bits), live, b)
+        return b
 
     def struct(self) -> _Codebook:
         c = self.centroids
@@ -306,81 +323,113 @@ def _act(act: str) -> int:
 _EPILOGUE = struct.Struct("<i4xQi4xQi4xqQqQi4x")   # orbq_epilogue
 
 
-def _epilogue(torch, func, act: str, n: int, m: int, Y, bias, gate, residual, cu):
+def _epilogue(func, act: str, n: int, m: int, Y, dev: int, bias, gate, residual, cu):
     """The packed orbq_epilogue of a product Y [n, m]."""
-    dev = Y.device
-    y_type = _y_type(torch, Y)
-    kind = {torch.float32: F32, torch.bfloat16: BF16}
-    for t, name in ((bias, "bias"), (gate, "gate"), (residual, "residual")):
-        if t is not None and (t.device != dev or t.dtype not in kind or (t.shape[-1] > 1 and t.stride(-1) != 1)):
-            raise OrbqError(-1, func, f"{name} must be float32 or bfloat16 with contiguous rows on {dev}")
-    if bias is not None and bias.shape != (m,):
-        raise OrbqError(-1, func, f"bias must be [{m}], got {list(bias.shape)}")
-    if residual is not None and (residual.shape != (n, m) or residual.dtype != Y.dtype):
-        raise OrbqError(-1, func, f"residual must be [{n}, {m}] of the output's type, got {list(residual.shape)} of {residual.dtype}")
-    groups, gate_ld = 1, 0
+    types = _PRODUCT_TYPES
+    bp = bt = gp = gt = gl = rp = rl = cup = 0
+    groups = 1
+    if bias is not None:
+        bt = types.get(bias.dtype)
+        if bt is None or bias.get_device() != dev or bias.shape != (m,) or (m > 1 and bias.stride(0) != 1):
+            raise OrbqError(-1, func, f"bias must be contiguous float32 or bfloat16 [{m}] on cuda:{dev}, got {bias.dtype} "
+                            f"{list(bias.shape)} on {bias.device}")
+        bp = bias.data_ptr()
     if cu is not None:
-        if cu.dtype != torch.int32 or cu.device != dev or cu.dim() != 1 or cu.numel() < 2 or not cu.is_contiguous():
-            raise OrbqError(-1, func, f"cu must be contiguous int32 [groups + 1] on {dev}")
-        groups = cu.numel() - 1
-    elif gate is not None and gate.dim() == 2:
-        groups = max(1, gate.shape[0])
+        if cu.get_device() != dev or cu.dim() != 1 or cu.numel() < 2 or str(cu.dtype) != "torch.int32" or not cu.is_contiguous():
+            raise OrbqError(-1, func, f"cu must be contiguous int32 [groups + 1] on cuda:{dev}")
+        groups, cup = cu.numel() - 1, cu.data_ptr()
+    elif gate is not None and gate.dim() == 2 and gate.shape[0] > 1:
+        groups = gate.shape[0]
     if gate is not None:
-        if gate.shape not in ((m,), (1, m), (groups, m)):
-            raise OrbqError(-1, func, f"gate must be [{m}] or [{groups}, {m}], got {list(gate.shape)}")
-        gate_ld = gate.stride(0) if gate.dim() == 2 and gate.shape[0] > 1 else 0
-    at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-    of = lambda t: 0 if t is None else kind[t.dtype]  # noqa: E731
-    # a single row has no stride of its own: any that is wide enough and aligned does
-    ld = 0 if residual is None else residual.stride(0) if n > 1 else (m + 7) // 8 * 8
-    return _EPILOGUE.pack(_act(act), at(bias), of(bias), at(gate), of(gate), gate_ld, at(residual), ld, at(cu), groups)
+        gt = types.get(gate.dtype)
+        if gt is None or gate.get_device() != dev or gate.shape not in ((m,), (1, m), (groups, m)) or (m > 1 and gate.stride(-1) != 1):
+            raise OrbqError(-1, func, f"gate must be float32 or bfloat16 [{m}] or [{groups}, {m}] with contiguous rows on cuda:{dev}, "
+                            f"got {gate.dtype} {list(gate.shape)} on {gate.device}")
+        gp, gl = gate.data_ptr(), gate.stride(0) if gate.dim() == 2 and gate.shape[0] > 1 else 0
+    if residual is not None:
+        if residual.shape != (n, m) or residual.dtype != Y.dtype or residual.get_device() != dev or (m > 1 and residual.stride(1) != 1):
+            raise OrbqError(-1, func, f"residual must be [{n}, {m}] of the output's type with contiguous rows on cuda:{dev}, got "
+                            f"{list(residual.shape)} of {residual.dtype} on {residual.device}")
+        # a single row has no stride of its own: any that is wide enough and aligned does
+        rp, rl = residual.data_ptr(), residual.stride(0) if n > 1 else (m + 7) // 8 * 8
+    return _EPILOGUE.pack(_act(act), bp, bt, gp, gt, gl, rp, rl, cup, groups)
 
 
-def _without_gradient(call):
-    """`call`, a product, in the autograd graph where its bias, gate or residual is: a backward pass that reaches it raises,
-    instead of leaving their gradients out."""
+_PRODUCT_TYPES = {}       # torch's types of a product's vectors and output, with the first product
+_UNTRACKED = []           # the autograd function of products whose vectors need a gradient
+
+
+def _product(call):
+    """`call`, a product, with the device of its first argument current; in the autograd graph where its bias, gate or residual
+    is: a backward pass that reaches it raises, instead of leaving their gradients out."""
+    on = _on_its_device(call)
+
     @functools.wraps(call)
     def product(*args, **kw):
-        leaves = [kw.get(n) for n in ("bias", "gate", "residual")]
-        if not any(t is not None and t.requires_grad for t in leaves) or kw.get("out") is not None:
-            return call(*args, **kw)
-        torch = _torch()
-        if not torch.is_grad_enabled():
-            return call(*args, **kw)
+        if kw.get("out") is None:
+            for name in ("bias", "gate", "residual"):
+                t = kw.get(name)
+                if t is not None and t.requires_grad:
+                    import torch
+                    if torch.is_grad_enabled():
+                        return _untracked(torch).apply(on, args, kw, *(kw.get(n) for n in ("bias", "gate", "residual")))
+        return on(*args, **kw)
+    return product
 
+
+def _untracked(torch):
+    if not _UNTRACKED:
         class Product(torch.autograd.Function):
             @staticmethod
-            def forward(ctx, *leaves):
+            def forward(ctx, call, args, kw, *leaves):
                 return call(*args, **kw)
 
             @staticmethod
             def backward(ctx, dy):
-                raise OrbqError(-1, call.__name__, "there is no gradient through the quantized product")
-        return Product.apply(*leaves)
-    return product
+                raise OrbqError(-1, "product", "there is no gradient through the quantized product")
+        _UNTRACKED.append(Product)
+    return _UNTRACKED[0]
 
 
-@_without_gradient
-@_on_its_device
+def _fused(func, x, n: int, m: int, out_dtype, out, act, bias, gate, residual, cu):
+    """(the output of a product with an epilogue, its type, the packed epilogue, the stream)"""
+    import torch
+    if not _PRODUCT_TYPES:
+        _PRODUCT_TYPES.update({torch.float32: F32, torch.bfloat16: BF16})
+    dev = x.get_device()
+    if out is None:
+        out = torch.empty((n, m), dtype=out_dtype or (torch.float32 if residual is None else residual.dtype), device=x.device)
+    elif out.shape != (n, m) or out.get_device() != dev or (m > 1 and out.stride(1) != 1):
+        raise OrbqError(-1, func, f"out must be [{n}, {m}] with contiguous rows on cuda:{dev}")
+    y_type = _PRODUCT_TYPES.get(out.dtype)
+    if y_type is None:
+        raise OrbqError(-1, func, f"the output must be float32 or bfloat16, got {out.dtype}")
+    return out, y_type, _epilogue(func, act, n, m, out, dev, bias, gate, residual, cu), torch._C._cuda_getCurrentRawStream(dev)
+
+
+@_product
 def lut_gemm(x_codes, x_norms, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook, d: int, out_dtype=None, out=None,
              act: str = "none", *, bias=None, gate=None, residual=None, cu=None):
     """Y [n, m] = residual + gate * act(diag(s) C_a[x_codes] C_w[w_codes]^T diag(r') + bias); without bias, gate, residual
     and cu act "none" calls orbq_lut_gemm, "gelu_tanh" / "gelu_erf" orbq_lut_gemm_act, with one orbq_lut_gemm_fused.
     bias [m]; gate [m] or [groups, m], a row for each group of tokens (n / groups each, or as cu int32 [groups + 1] says);
     residual [n, m] of the output's type, `out` itself to add in place."""
-    torch = _torch()
-    out_dtype = out_dtype or (torch.float32 if residual is None else residual.dtype)
     n, m = x_codes.shape[0], w_codes.shape[0]
+    if bias is not None or gate is not None or residual is not None or cu is not None:
+        Y, yt, e, stream = _fused("lut_gemm", x_codes, n, m, out_dtype, out, act, bias, gate, residual, cu)
+        st = load().orbq_lut_gemm_fused(x_codes.data_ptr(), x_norms.data_ptr(), cb_a.packed(), w_codes.data_ptr(),
+                                        w_norms.data_ptr(), cb_w.packed(), n, m, d, e, Y.data_ptr(), yt,
+                                        Y.stride(0) if n > 1 else (m + 7) // 8 * 8, stream)
+        if st:
+            _check(st, "orbq_lut_gemm_fused")
+        return Y
+    torch = _torch()
+    out_dtype = out_dtype or torch.float32
     Y = out if out is not None else torch.empty((n, m), dtype=out_dtype, device=x_codes.device)
     a, w = cb_a.struct(), cb_w.struct()
     yt = _y_type(torch, Y)
     code = _act(act)
-    if bias is not None or gate is not None or residual is not None or cu is not None:
-        e = _epilogue(torch, "lut_gemm", act, n, m, Y, bias, gate, residual, cu)
-        _check(load().orbq_lut_gemm_fused(x_codes.data_ptr(), x_norms.data_ptr(), ctypes.byref(a), w_codes.data_ptr(),
-                                          w_norms.data_ptr(), ctypes.byref(w), n, m, d, e, Y.data_ptr(), yt, Y.stride(0),
-                                          _stream(torch, x_codes.device)), "orbq_lut_gemm_fused")
-    elif code == 0:
+    if code == 0:
         _check(load().orbq_lut_gemm(x_codes.data_ptr(), x_norms.data_ptr(), ctypes.byref(a), w_codes.data_ptr(),
                                     w_norms.data_ptr(), ctypes.byref(w), n, m, d, Y.data_ptr(), yt, Y.stride(0),
                                     _stream(torch, x_codes.device)), "orbq_lut_gemm")
@@ -391,32 +440,33 @@ def lut_gemm(x_codes, x_norms, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook,
     return Y
 
 
-@_without_gradient
-@_on_its_device
+@_product
 def linear(X, rot: Rotation, cb_a: Codebook, w_codes, w_norms, cb_w: Codebook, eps: float = 1e-8, out_dtype=None,
            workspace=None, out=None, act: str = "none", *, bias=None, gate=None, residual=None, cu=None):
     """The online layer: Y [n, m] from bf16 tokens X [n, d] and folded weights (act, bias, gate, residual and cu as in
     lut_gemm: act "none" calls orbq_linear, a GELU form orbq_linear_act, with one of the others orbq_linear_fused)."""
     torch = _torch()
     _dev_tensor(X, torch.bfloat16, "linear")
-    out_dtype = out_dtype or (torch.float32 if residual is None else residual.dtype)
     n, d = X.shape
     m = w_codes.shape[0]
     need = linear_workspace_bytes(n, d, cb_a.bits)
     if workspace is None:
         workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=X.device)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    if bias is not None or gate is not None or residual is not None or cu is not None:
+        Y, yt, e, stream = _fused("linear", X, n, m, out_dtype, out, act, bias, gate, residual, cu)
+        st = load().orbq_linear_fused(X.data_ptr(), n, d, X.stride(0), rot.packed(), cb_a.packed(), eps, w_codes.data_ptr(),
+                                      w_norms.data_ptr(), cb_w.packed(), m, workspace.data_ptr(), ws_bytes, e, Y.data_ptr(), yt,
+                                      Y.stride(0) if n > 1 else (m + 7) // 8 * 8, stream)
+        if st:
+            _check(st, "orbq_linear_fused")
+        return Y
+    out_dtype = out_dtype or torch.float32
     Y = out if out is not None else torch.empty((n, m), dtype=out_dtype, device=X.device)
     r, a, w = rot.struct(), cb_a.struct(), cb_w.struct()
     yt = _y_type(torch, Y)
-    ws_bytes = workspace.numel() * workspace.element_size()
     code = _act(act)
-    if bias is not None or gate is not None or residual is not None or cu is not None:
-        e = _epilogue(torch, "linear", act, n, m, Y, bias, gate, residual, cu)
-        _check(load().orbq_linear_fused(X.data_ptr(), n, d, X.stride(0), ctypes.byref(r), ctypes.byref(a), eps,
-                                        w_codes.data_ptr(), w_norms.data_ptr(), ctypes.byref(w), m, workspace.data_ptr(),
-                                        ws_bytes, e, Y.data_ptr(), yt, Y.stride(0), _stream(torch, X.device)),
-               "orbq_linear_fused")
-    elif code == 0:
+    if code == 0:
         _check(load().orbq_linear(X.data_ptr(), n, d, X.stride(0), ctypes.byref(r), ctypes.byref(a), eps,
                                   w_codes.data_ptr(), w_norms.data_ptr(), ctypes.byref(w), m, workspace.data_ptr(),
                                   ws_bytes, Y.data_ptr(), yt, Y.stride(0), _stream(torch, X.device)), "orbq_linear")
@@ -457,15 +507,28 @@ def linear_a16_workspace_bytes(n: int, d: int, m: int) -> int:
     return int(load().orbq_linear_a16_workspace_bytes(n, d, m))
 
 
-@_without_gradient
-@_on_its_device
+@_product
 def linear_a16(X, rot: Rotation, w_codes, w_norms, cb_w: Codebook, out_dtype=None, workspace=None, out=None, act: str = "none", *,
                bias=None, gate=None, residual=None, cu=None):
     """Weight-only product: Y [n, m] from bf16 tokens X [n, d] (rotated, not quantized) and
     folded weight codes (orbq_linear_a16; with act, bias, gate, residual or cu, as in lut_gemm, orbq_linear_a16_fused)."""
+    import torch
+    if bias is not None or gate is not None or residual is not None or cu is not None or _act(act):
+        _dev_tensor(X, torch.bfloat16, "linear_a16")
+        n, d = X.shape
+        m = w_codes.shape[0]
+        Y, yt, e, stream = _fused("linear_a16", X, n, m, out_dtype, out, act, bias, gate, residual, cu)
+        if workspace is None:
+            workspace = torch.empty((max(linear_a16_workspace_bytes(n, d, m), 1),), dtype=torch.uint8, device=X.device)
+        st = load().orbq_linear_a16_fused(X.data_ptr(), n, d, X.stride(0), rot.packed(), w_codes.data_ptr(), w_norms.data_ptr(),
+                                          cb_w.packed(), m, workspace.data_ptr(), workspace.numel() * workspace.element_size(), e,
+                                          Y.data_ptr(), yt, Y.stride(0) if n > 1 else m, stream)
+        if st:
+            _check(st, "orbq_linear_a16_fused")
+        return Y
     torch = _torch()
     _dev_tensor(X, torch.bfloat16, "linear_a16")
-    out_dtype = out_dtype or (torch.float32 if residual is None else residual.dtype)
+    out_dtype = out_dtype or torch.float32
     n, d = X.shape
     m = w_codes.shape[0]
     need = linear_a16_workspace_bytes(n, d, m)
@@ -473,17 +536,11 @@ def linear_a16(X, rot: Rotation, w_codes, w_norms, cb_w: Codebook, out_dtype=Non
         workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=X.device)
     Y = out if out is not None else torch.empty((n, m), dtype=out_dtype, device=X.device)
     r, w = rot.struct(), cb_w.struct()
-    yt = _y_type(torch, Y)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    if bias is not None or gate is not None or residual is not None or cu is not None or _act(act):
-        e = _epilogue(torch, "linear_a16", act, n, m, Y, bias, gate, residual, cu)
-        _check(load().orbq_linear_a16_fused(X.data_ptr(), n, d, X.stride(0), ctypes.byref(r), w_codes.data_ptr(),
-                                            w_norms.data_ptr(), ctypes.byref(w), m, workspace.data_ptr(), ws_bytes, e,
-                                            Y.data_ptr(), yt, Y.stride(0), _stream(torch, X.device)), "orbq_linear_a16_fused")
-    else:
-        _check(load().orbq_linear_a16(X.data_ptr(), n, d, X.stride(0), ctypes.byref(r), w_codes.data_ptr(),
-                                      w_norms.data_ptr(), ctypes.byref(w), m, workspace.data_ptr(), ws_bytes, Y.data_ptr(), yt,
-                                      Y.stride(0), _stream(torch, X.device)), "orbq_linear_a16")
+    _check(load().orbq_linear_a16(X.data_ptr(), n, d, X.stride(0), ctypes.byref(r), w_codes.data_ptr(),
+                                  w_norms.data_ptr(), ctypes.byref(w), m, workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), Y.data_ptr(),
+                                  _y_type(torch, Y), Y.stride(0), _stream(torch, X.device)),
+           "orbq_linear_a16")
     return Y
 
 

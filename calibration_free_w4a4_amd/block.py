@@ -77,51 +77,70 @@ def _type(t, func: str, name: str) -> int:
     return code
 
 
-def _rows(t, like, func: str, name: str):
-    """(address, row stride) of rows [n, d] shaped as `like` is."""
-    if t.shape != like.shape or t.get_device() != like.get_device():
-        raise _bad(func, f"{name} must be {list(like.shape)} on {like.device}")
+def _rows(t, shape, dev: int, func: str, name: str):
+    """(address, row stride) of rows [n, d]."""
+    if t.shape != shape or t.get_device() != dev:
+        raise _bad(func, f"{name} must be {list(shape)} on cuda:{dev}")
     a, b = t.stride()
-    if b != 1 and t.shape[1] > 1:
+    if b != 1 and shape[1] > 1:
         raise _bad(func, f"{name} must have contiguous rows")
-    return t.data_ptr(), a if t.shape[0] > 1 else 0
+    return t.data_ptr(), a if shape[0] > 1 else 0
 
 
-def _packed(x, y, gate, weight, scale, shift, post_weight, norm, post, eps, post_eps, cu, func):
+def _vector(v, groups: int, d: int, dev: int, mod, func: str, name: str):
+    """(address, row stride) of a vector of the groups; mod: the type of those before, or None."""
+    shape, stride = v.shape, v.stride()
+    rows = shape[0] if len(shape) == 2 else 1
+    if (shape[-1] if shape else 0) != d or len(shape) > 2 or rows not in (1, groups) or v.get_device() != dev or \
+            (stride[-1] != 1 and d > 1):
+        raise _bad(func, f"{name} must be [{d}] or [{groups}, {d}] with contiguous rows on cuda:{dev}, got {list(shape)}")
+    if mod is not None and v.dtype != mod:
+        raise _bad(func, "gate, scale and shift must be of one type")
+    return v.data_ptr(), stride[0] if rows > 1 else 0
+
+
+def _packed(d, dev, gate, weight, scale, shift, post_weight, norm, post, eps, post_eps, cu, func):
     """(the packed orbq_norms, groups)"""
-    n, d = x.shape
-    dev = x.get_device()
-    if norm not in NORMS or post not in NORMS:
+    kinds = NORMS.get(norm), NORMS.get(post)
+    if None in kinds:
         raise _bad(func, f"norm {norm!r}, post {post!r} (each one of 'layer', 'rms' or None)")
+    groups, cup = 1, 0
     if cu is not None:
         if cu.dtype != torch.int32 or cu.get_device() != dev or cu.dim() != 1 or cu.numel() < 2 or not cu.is_contiguous():
             raise _bad(func, f"cu must be contiguous int32 [groups + 1] on cuda:{dev}")
-        groups = cu.numel() - 1
+        groups, cup = cu.numel() - 1, cu.data_ptr()
     else:
-        groups = max([1] + [v.shape[0] for v in (gate, scale, shift) if v is not None and v.dim() == 2])
-    at, mod = [], None
-    for v, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
-        if v is None:
-            at += [(0, 0)]
-            continue
-        if v.shape not in ((d,), (1, d), (groups, d)) or v.get_device() != dev or (v.stride(-1) != 1 and d > 1):
-            raise _bad(func, f"{name} must be [{d}] or [{groups}, {d}] with contiguous rows on cuda:{dev}, got {list(v.shape)}")
-        if mod is not None and v.dtype != mod:
-            raise _bad(func, "gate, scale and shift must be of one type")
-        mod = v.dtype
-        _type(v, func, name)
-        at += [(v.data_ptr(), v.stride(0) if v.dim() == 2 and v.shape[0] > 1 else 0)]
+        for v in (gate, scale, shift):
+            if v is not None and v.dim() == 2 and v.shape[0] > groups:
+                groups = v.shape[0]
+    gp = sp = hp = gl = sl = hl = 0
+    mod = None
+    if gate is not None:
+        gp, gl = _vector(gate, groups, d, dev, mod, func, "gate")
+        mod = gate.dtype
+    if scale is not None:
+        sp, sl = _vector(scale, groups, d, dev, mod, func, "scale")
+        mod = scale.dtype
+    if shift is not None:
+        hp, hl = _vector(shift, groups, d, dev, mod, func, "shift")
+        mod = shift.dtype
+    mtype = 0 if mod is None else _TYPES.get(mod)
+    if mtype is None:
+        raise _bad(func, f"gate, scale and shift must be float32, bfloat16 or float16, got {mod}")
+    wp = pwp = wtype = 0
     for v, name in ((weight, "weight"), (post_weight, "post_weight")):
-        if v is not None and (v.shape != (d,) or v.get_device() != dev or (v.stride(0) != 1 and d > 1)):
-            raise _bad(func, f"{name} must be contiguous [{d}] on cuda:{dev}")
-    if weight is not None and post_weight is not None and weight.dtype != post_weight.dtype:
-        raise _bad(func, "weight and post_weight must be of one type")
-    w = weight if weight is not None else post_weight
-    wtype = 0 if w is None else _type(w, func, "weight")
-    address = lambda v: 0 if v is None else v.data_ptr()  # noqa: E731
-    return _NORMS.pack(NORMS[norm], NORMS[post], eps, eps if post_eps is None else post_eps, address(weight), address(post_weight),
-                       at[0][0], at[1][0], at[2][0], at[0][1], at[1][1], at[2][1], wtype, 0 if mod is None else _TYPES[mod],
-                       address(cu), groups), groups
+        if v is not None:
+            if v.shape != (d,) or v.get_device() != dev or (v.stride(0) != 1 and d > 1):
+                raise _bad(func, f"{name} must be contiguous [{d}] on cuda:{dev}")
+            wtype = _type(v, func, name)
+    if weight is not None:
+        wp = weight.data_ptr()
+    if post_weight is not None:
+        pwp = post_weight.data_ptr()
+        if weight is not None and weight.dtype != post_weight.dtype:
+            raise _bad(func, "weight and post_weight must be of one type")
+    return _NORMS.pack(*kinds, eps, eps if post_eps is None else post_eps, wp, pwp, gp, sp, hp, gl, sl, hl, wtype, mtype, cup,
+                       groups), groups
 
 
 def _checked(x, y, func: str):
@@ -138,29 +157,39 @@ def _forward(func, x, y, gate, weight, scale, shift, post_weight, dtype, out, no
     if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _forward(func, x, y, gate, weight, scale, shift, post_weight, dtype, out, norm, post, eps, post_eps, cu)
-    if dtype is not None and NORMS.get(norm):
-        if dtype not in _TYPES or (y is not None and y.dtype != dtype):
+    shape = x.shape
+    n, d = shape
+    norms, _ = _packed(d, dev, gate, weight, scale, shift, post_weight, norm, post, eps, post_eps, cu, func)
+    normed = NORMS[norm]
+    h_type = (x if y is None else y).dtype
+    if dtype is not None and normed and dtype != h_type:
+        if y is not None or dtype not in _TYPES:
             raise _bad(func, f"h cannot be {dtype}: one of the three types, and y's where there is a y")
-        branch = _TYPES[dtype]
-    norms, _ = _packed(x, y, gate, weight, scale, shift, post_weight, norm, post, eps, post_eps, cu, func)
-    xp, xld = _rows(x, x, func, "x")
-    yp, yld = (0, 0) if y is None else _rows(y, x, func, "y")
-    n, d = x.shape
-    h_type = dtype or (x if y is None else y).dtype
+        h_type, branch = dtype, _TYPES[dtype]
+    xp, xld = _rows(x, shape, dev, func, "x")
+    yp = yld = rp = hp = 0
+    rld = hld = d
+    if y is not None:
+        yp, yld = _rows(y, shape, dev, func, "y")
     if out is None:
-        r = None if y is None else torch.empty((n, d), dtype=x.dtype, device=x.device)
-        h = torch.empty((n, d), dtype=h_type, device=x.device) if NORMS[norm] else None
+        r = h = None
+        if y is not None:
+            r = torch.empty((n, d), dtype=x.dtype, device=x.device)
+            rp = r.data_ptr()
+        if normed:
+            h = torch.empty((n, d), dtype=h_type, device=x.device)
+            hp = h.data_ptr()
     else:
         r, h = out
-        if y is None:
-            r = None
-        elif r is not None and r.dtype != x.dtype:
-            raise _bad(func, f"r must be {x.dtype}")
-        if NORMS[norm] and (h is None or h.dtype != h_type):
-            raise _bad(func, f"h must be {h_type}")
-        h = h if NORMS[norm] else None
-    rp, rld = (0, 0) if r is None else _rows(r, x, func, "r")
-    hp, hld = (0, 0) if h is None else _rows(h, x, func, "h")
+        r, h = None if y is None else r, h if normed else None
+        if r is not None:
+            if r.dtype != x.dtype:
+                raise _bad(func, f"r must be {x.dtype}")
+            rp, rld = _rows(r, shape, dev, func, "r")
+        if normed:
+            if h is None or h.dtype != h_type:
+                raise _bad(func, f"h must be {h_type}")
+            hp, hld = _rows(h, shape, dev, func, "h")
     if n:
         st = load().orbq_block_norm(norms, n, d, xp, xld, yp, yld, rp, rld, hp, hld, code, branch,
                                     torch._C._cuda_getCurrentRawStream(dev))
@@ -177,12 +206,13 @@ def block_norm(x, y=None, gate=None, weight=None, scale=None, shift=None, post_w
     or of x).  out: (r, h) to write; (x, h) writes r in place.  Rows outside cu's groups are left alone."""
     _need_torch()
     func = "block_norm"
-    how = dict(norm=norm, post=post, eps=eps, post_eps=post_eps, cu=cu)
-    if out is None and torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                                       for t in (x, y, gate, weight, scale, shift, post_weight)):
-        got = _Normed.apply(func, dtype, how, x, y, gate, weight, scale, shift, post_weight)
-        return (x, got) if y is None else got if isinstance(got, tuple) else (got, None)
-    return _forward(func, x, y, gate, weight, scale, shift, post_weight, dtype, out, **how)
+    if out is None and torch.is_grad_enabled():
+        for t in (x, y, gate, weight, scale, shift, post_weight):
+            if t is not None and t.requires_grad:
+                how = dict(norm=norm, post=post, eps=eps, post_eps=post_eps, cu=cu)
+                got = _Normed.apply(func, dtype, how, x, y, gate, weight, scale, shift, post_weight)
+                return (x, got) if y is None else got if isinstance(got, tuple) else (got, None)
+    return _forward(func, x, y, gate, weight, scale, shift, post_weight, dtype, out, norm, post, eps, post_eps, cu)
 
 
 def _backward(func, r, dh, dr, y, gate, weight, scale, shift, post_weight, needed, workspace, norm, post, eps, post_eps, cu):
@@ -192,8 +222,9 @@ def _backward(func, r, dh, dr, y, gate, weight, scale, shift, post_weight, neede
         with torch.cuda.device(dev):
             return _backward(func, r, dh, dr, y, gate, weight, scale, shift, post_weight, needed, workspace, norm, post, eps,
                              post_eps, cu)
-    norms, groups = _packed(r, y, gate, weight, scale, shift, post_weight, norm, post, eps, post_eps, cu, func)
-    n, d = r.shape
+    shape = r.shape
+    n, d = shape
+    norms, groups = _packed(d, dev, gate, weight, scale, shift, post_weight, norm, post, eps, post_eps, cu, func)
     if dh is None and dr is None:
         raise _bad(func, "neither dh nor dr")
     if dh is not None:
@@ -208,10 +239,10 @@ def _backward(func, r, dh, dr, y, gate, weight, scale, shift, post_weight, neede
         return NormGrads(*[None if t is None else t.zero_() for t in got])
     flat = lambda t: t if t is None or t.stride(-1) == 1 or d == 1 else t.contiguous()  # noqa: E731  an expanded gradient
     dh, dr = flat(dh), flat(dr)
-    rp, rld = _rows(r, r, func, "r")
-    yp, yld = (0, 0) if y is None else _rows(y, r, func, "y")
-    drp, drld = (0, 0) if dr is None else _rows(dr, r, func, "dr")
-    dhp, dhld = (0, 0) if dh is None else _rows(dh, r, func, "dh")
+    rp, rld = _rows(r, shape, dev, func, "r")
+    yp, yld = (0, 0) if y is None else _rows(y, shape, dev, func, "y")
+    drp, drld = (0, 0) if dr is None else _rows(dr, shape, dev, func, "dr")
+    dhp, dhld = (0, 0) if dh is None else _rows(dh, shape, dev, func, "dh")
     address = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
     # a vector that the groups share has one gradient, the sum of theirs
     apart = lambda t: 0 if t is None or t.dim() == 1 or (t.shape[0] == 1 and groups > 1) else d  # noqa: E731

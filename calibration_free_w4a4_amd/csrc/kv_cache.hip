@@ -28,7 +28,9 @@ namespace {
 template <int DT, int D, int PAGE>
 __global__ __launch_bounds__(threads_for(D* PAGE)) void k_append(const KvCache c, const KvTokens x) {
   __shared__ PageSpace<D, PAGE> space;
-  append_page<DT, D, PAGE>(c, x, blockIdx.z, blockIdx.y >> 1, blockIdx.y & 1, blockIdx.x, space, Unchanged{});
+  PageSpot spot;
+  if (!locate_page<PAGE>(c, x, blockIdx.z, blockIdx.x, &spot)) return;
+  append_page<DT, D, PAGE>(c, x, spot, blockIdx.y >> 1, blockIdx.y & 1, space, Unchanged{});
 }
 
 template <int DT, int D, int PAGE>

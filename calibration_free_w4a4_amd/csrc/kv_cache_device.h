@@ -110,30 +110,46 @@ template <int D, int PAGE> struct PageSpace {
   uint32_t top[S::NT / 64];
 };
 
-// The new keys (or values) of one head that fall into one page, which is the `page_of_call`th that the sequence's new tokens
-// touch: their scale, the page's earlier codes where it grows, their codes.  Called by a whole workgroup.  `change` may
-// replace the entries, as floats, before that.
+// A page that a sequence's new tokens touch.
+struct PageSpot {
+  int64_t base;    // packed row of the page's token t: base + t
+  int had, end;    // tokens held before, and after
+  int32_t entry;   // of the page table, not yet judged
+  bool inside;     // the table has one
+};
+
+// The `page_of_call`th page that sequence b's new tokens touch, if there is one.  UNPLACED: also of tokens at negative
+// positions, which have none: counted from token 0.
+template <int PAGE, bool UNPLACED = false>
+__device__ __forceinline__ bool locate_page(const KvCache& c, const KvTokens& x, int b, int64_t page_of_call, PageSpot* spot) {
+  int64_t row0;
+  int32_t rows, all;
+  rows_of(x.cu, x.total, c.batch, x.max_rows, b, &row0, &rows, &all);
+  const int64_t first = x.first[b];
+  if ((first < 0 && !UNPLACED) || rows == 0) return false;
+  const int64_t start = first < 0 ? 0 : first;
+  const int64_t p = start / PAGE + page_of_call;
+  const int64_t t0 = p * PAGE;                       // the page's first token
+  if (t0 >= start + rows) return false;
+  spot->had = static_cast<int>(start > t0 ? start - t0 : 0);
+  spot->end = static_cast<int>(start + rows - t0 < PAGE ? start + rows - t0 : PAGE);
+  spot->base = row0 + t0 - start;
+  spot->inside = first >= 0 && p < c.max_pages;
+  // the page, and with it the old scale, are looked up while the new values are on their way
+  spot->entry = c.table[b * c.ldt + (spot->inside ? p : 0)];
+  return true;
+}
+
+// The new keys (or values) of one head that fall into a page: their scale, the page's earlier codes where it grows, their
+// codes.  Called by a whole workgroup.  `change` may replace the entries, as floats, before that.
 template <int DT, int D, int PAGE, class Change>
-__device__ __forceinline__ void append_page(const KvCache& c, const KvTokens& x, int b, int head, bool values, int64_t page_of_call,
+__device__ __forceinline__ void append_page(const KvCache& c, const KvTokens& x, const PageSpot& spot, int head, bool values,
                                             PageSpace<D, PAGE>& space, const Change& change) {
   using S = Share<D, PAGE>;
   constexpr int NT = S::NT, PER = S::PER, TP = S::TP, LD = S::LD;
   auto& turned = space.turned;
   auto& top = space.top;
-  const int tid = threadIdx.x;
-  int64_t row0;
-  int32_t rows, all;
-  rows_of(x.cu, x.total, c.batch, x.max_rows, b, &row0, &rows, &all);
-  const int64_t start = x.first[b];
-  if (start < 0 || rows == 0) return;
-  const int64_t p = start / PAGE + page_of_call;
-  const int64_t t0 = p * PAGE;                       // the page's first token
-  if (t0 >= start + rows) return;
-  const int had = static_cast<int>(start > t0 ? start - t0 : 0);                        // tokens held before
-  const int end = static_cast<int>(start + rows - t0 < PAGE ? start + rows - t0 : PAGE);  // and after
-  // the page, and with it the old scale, are looked up while the new values are on their way
-  const int32_t entry = c.table[b * c.ldt + (p < c.max_pages ? p : 0)];
-
+  const int tid = threadIdx.x, had = spot.had, end = spot.end;
   const void* src = values ? x.v : x.k;
   const int64_t st = values ? x.vt : x.kt, sh = (values ? x.vh : x.kh) * head;
   // no load depends on a branch (a token that is not new reads a neighbour's row), so that all are under way at once
@@ -144,11 +160,11 @@ __device__ __forceinline__ void append_page(const KvCache& c, const KvTokens& x,
   for (int i = 0; i < PER; ++i) {
     int t = S::token(tid, i);
     t = t < had ? had : (t >= end ? end - 1 : t);
-    const T* from = static_cast<const T*>(src) + (row0 + t0 + t - start) * st + sh + S::entry(tid);
+    const T* from = static_cast<const T*>(src) + (spot.base + t) * st + sh + S::entry(tid);
 #pragma unroll
     for (int w = 0; w < W; ++w) raw[i][w] = reinterpret_cast<const u32x4_t*>(from)[w];
   }
-  const int32_t pg = p < c.max_pages && entry >= 0 && entry < c.pages ? entry : -1;
+  const int32_t pg = spot.inside && spot.entry >= 0 && spot.entry < c.pages ? spot.entry : -1;
   if (pg < 0) return;
   const int64_t slot = static_cast<int64_t>(pg) * c.heads + head;
   float* scales = (values ? c.vs : c.ks) + slot;
@@ -170,7 +186,7 @@ __device__ __forceinline__ void append_page(const KvCache& c, const KvTokens& x,
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[i][j] = static_cast<float>(reinterpret_cast<const T*>(&raw[i][0])[j]);
   constexpr int BITS = Change::kChanges ? static_cast<int>(kF32) : DT;  // changed entries are floats
-  if constexpr (Change::kChanges) change(f, src, sh, st, row0 + t0 - start, had, end);
+  if constexpr (Change::kChanges) change(f);
   // the largest magnitude, as the integer that its bits are
   uint32_t big;
   if constexpr (Change::kChanges) {

@@ -190,3 +190,23 @@ def test_products(cb):
     for f in (linear, a16):
         assert f(ws_bytes=16) == WORKSPACE and f(ws=None) == WORKSPACE and f(ws=P + 16) == ALIGN
     assert gemm(x=None) == ARG
+
+
+def test_the_binding_packs_rotations_and_codebooks_as_declared(cb):
+    class Tensor:
+        def __init__(self, at):
+            self.data_ptr = lambda: at
+
+    r = orbq._Rpbh.from_buffer_copy(orbq.Rotation(256, 64, Tensor(1 << 40), Tensor(3), 2).packed())
+    assert (r.d, r.block, r.perm, r.signs, r.passes) == (256, 64, 1 << 40, 3, 2)
+    assert not orbq._Rpbh.from_buffer_copy(orbq.Rotation(256, 64, None, Tensor(3)).packed()).perm
+    book = orbq.Codebook.from_centroids(256, 4, cb(256, 4))
+    for _ in range(2):      # the second time as kept
+        c = orbq._Codebook.from_buffer_copy(book.packed())
+        assert (c.d, c.bits) == (256, 4) and c.centroids[:16] == book.centroids.tolist()
+    book.centroids = book.centroids * 2
+    assert orbq._Codebook.from_buffer_copy(book.packed()).centroids[:16] == book.centroids.tolist()
+    book.bits = 3
+    assert orbq._Codebook.from_buffer_copy(book.packed()).bits == 3
+    wide = orbq.Codebook(256, 4, cb(256, 4).astype("float64"))      # a copy that the codebook keeps alive
+    assert orbq._Codebook.from_buffer_copy(wide.packed()).centroids[:16] == cb(256, 4).tolist()

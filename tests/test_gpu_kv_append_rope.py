@@ -269,3 +269,26 @@ def test_refusals(orbq):
         q.float().sum().backward()
     with torch.no_grad():
         assert not c.call(c.cache(), q=leaf).requires_grad
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("layout", ["pairs", "halves"])
+def test_every_form(orbq, name, d, layout):
+    """Every page size, whole and part of the head turned, in whole columns of 8 and not, a token and several pages: the bits of rope
+    and kv_append without norms, and with norms whose weights are 1 of rows that are normalised to a power of two already."""
+    torch = torch_mod()
+    ones = torch.ones(d, device="cuda")
+    for page in (16, 32, 64, 128):
+        for dims in ((d,), (d // 2,), (d // 4, 6)):
+            for new in ([1, 1], [2 * page + 5, 3]):
+                c = Case(orbq, new, [3, page - 1], 5, 3, d, page, dims, layout, name, seed=page + d)
+                want, got = c.cache(), c.cache()
+                q_want, q = c.apart(want), c.call(got)
+                assert torch.equal(q, q_want) and same(got, want), (page, dims, new)
+                # entries of magnitude 2: the mean square is 4, its root 2, exactly, and so is the quotient
+                c.q, c.k = (torch.where(t > 0, 2.0, -2.0).to(c.dtype) for t in (c.q, c.k))
+                got, half = c.cache(), c.cache()
+                q = c.call(got, q_weight=ones, k_weight=ones, eps=0.0)
+                c.q, c.k = c.q / 2, c.k / 2
+                assert torch.equal(q, c.apart(half)) and same(got, half), (page, dims, new)
