@@ -27,6 +27,7 @@ constexpr int teams_of(int waves) { return waves == 1 ? 4 : 1; }  // rows of a w
 template <int TX, int TY, int E, int V, int W, bool LATE>
 __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(const NormArgs a) {
   constexpr int TEAMS = teams_of(W);
+  constexpr bool AHEAD = E == 8 && !LATE;
   __shared__ float place[2][W][2];
   __shared__ float joined[TEAMS > 1 ? TEAMS - 1 : 1][TEAMS > 1 ? V * 64 * E : 1];
   const int team = W == 1 ? threadIdx.x >> 6 : 0, t = W == 1 ? threadIdx.x & 63 : threadIdx.x;
@@ -64,25 +65,59 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(const NormArgs 
     }
     Row A, S, B;
     ORBQ_EACH(A[i][e] = S[i][e] = B[i][e] = 0.0f)
+    // AHEAD: the next row's inputs are under way while one is worked on
+    struct Inputs {
+      Piece<TX> r[V], dr[V];
+      Piece<TY> dh[V], y[V];
+    };
+    Inputs next;
+    const auto fetch = [&](int32_t at) {
+      const int32_t row = __builtin_amdgcn_readfirstlane(at);
+      const auto rows = [&](auto& piece, Rsrc s) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) piece[i].fetch(s, col[i]);
+      };
+      if (normed) {
+        rows(next.r, row_at<TX>(a.x, row, a.xld, a.d));
+        rows(next.dh, row_at<TY>(a.dh, row, a.dhld, a.d));
+      }
+      if (a.y) rows(next.y, row_at<TY>(a.y, row, a.yld, a.d));
+      if (a.dr) rows(next.dr, row_at<TX>(a.dr, row, a.drld, a.d));
+    };
+    if constexpr (AHEAD) {
+      if (from + team < end) fetch(from + team);
+    }
     for (int32_t at = from + team; at < end; at += TEAMS) {
       const int32_t row = __builtin_amdgcn_readfirstlane(at);
-      asm volatile("" ::: "memory");  // the vectors are read again for each row: held over the loop they would take the registers
       Row r, dh, dr, y;
       ORBQ_EACH(r[i][e] = dh[i][e] = dr[i][e] = y[i][e] = 0.0f)
       const auto load_y = [&] {
 #pragma unroll
         for (int i = 0; i < V; ++i) load<TY, E>(row_at<TY>(a.y, row, a.yld, a.d), col[i], y[i]);
       };
-      if (normed) {
+      if constexpr (AHEAD) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) load<TX, E>(row_at<TX>(a.x, row, a.xld, a.d), col[i], r[i]);
+        for (int i = 0; i < V; ++i) {
+          if (normed) {
+            next.r[i].get(r[i]);
+            next.dh[i].get(dh[i]);
+          }
+          if (a.y) next.y[i].get(y[i]);
+          if (a.dr) next.dr[i].get(dr[i]);
+        }
+        if (at + TEAMS < end) fetch(at + TEAMS);
+      } else {
+        if (normed) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) load<TY, E>(row_at<TY>(a.dh, row, a.dhld, a.d), col[i], dh[i]);
-      }
-      if (!LATE && a.y) load_y();
-      if (a.dr) {
+          for (int i = 0; i < V; ++i) load<TX, E>(row_at<TX>(a.x, row, a.xld, a.d), col[i], r[i]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) load<TX, E>(row_at<TX>(a.dr, row, a.drld, a.d), col[i], dr[i]);
+          for (int i = 0; i < V; ++i) load<TY, E>(row_at<TY>(a.dh, row, a.dhld, a.d), col[i], dh[i]);
+        }
+        if (!LATE && a.y) load_y();
+        if (a.dr) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) load<TX, E>(row_at<TX>(a.dr, row, a.drld, a.d), col[i], dr[i]);
+        }
       }
       // v becomes the normalised row, and with it w where both are there
       const auto factors = [&](Row& v, Row& w, bool both, bool v_layer, bool w_layer, float v_eps, float w_eps, float* fv, float* fw) {
@@ -192,23 +227,22 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(const NormArgs 
 #undef ORBQ_EACH
 }
 
-// The sums of all groups, one kind a workgroup row: lanes are columns, waves share the places (few groups) or the groups.
-constexpr int kSumWaves = 16;
-__global__ __launch_bounds__(64 * kSumWaves) void k_norm_grads(const NormArgs a, const NormGrads o) {
+// The sums of the groups: lanes are columns, blockIdx.y is the kind.  Workgroups z = 0, which take longest and start first, add up
+// all groups, each times its factor, for the vectors that they share; z > 0 add up the places of groups z - 1, z - 1 + own_z, ...,
+// one group at a time with its places shared by the waves.
+constexpr int kSumWaves = 16;  // 9001 rows of 4096 in 7 groups: 4, 8 and 16 waves 36, 25 and 22 us
+__global__ __launch_bounds__(64 * kSumWaves) void k_norm_grads(const NormArgs a, const NormGrads o, int own_z) {
   __shared__ float meet[kSumWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, kind = blockIdx.y;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kind = blockIdx.y;
   const int32_t col = blockIdx.x * 64 + lane, n = static_cast<int32_t>(a.n);
-  const bool in = col < a.d;
   void* const out = kind == 0 ? o.scale : (kind == 1 ? o.shift : o.gate);
   const int64_t out_ld = kind == 0 ? o.scld : (kind == 1 ? o.shld : o.gld);
   void* const total = kind == 0 ? o.w : (kind == 1 ? nullptr : o.pw);
-  if ((!out && !total) || (kind < 2 ? a.norm == kNormNone : a.y == nullptr)) return;
+  if (kind < 2 ? a.norm == kNormNone : a.y == nullptr) return;
   // what the sums are multiplied with for the group's gradient, and for the one summed over the groups
   const void* const mine = kind == 0 ? a.w : (kind == 1 ? nullptr : a.pw);
   const void* const theirs = kind == 0 ? a.scale : a.gate;
   const int64_t theirs_ld = kind == 0 ? a.scld : a.gld;
-  float own = 1.0f;
-  if (mine) load_any<1>(a.wtype, mine, 0, 0, a.d, col, &own);
   const auto put = [&](void* to, int type, int64_t row, int64_t ld, float v) {
     if (type == kF32) store<kF32, 1>(row_at<kF32>(to, row, ld, a.d), col, &v);
     else if (type == kBF16) store<kBF16, 1>(row_at<kBF16>(to, row, ld, a.d), col, &v);
@@ -223,9 +257,8 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_norm_grads(const NormArgs a,
     for (int w = 0; w < kSumWaves; ++w) s += meet[w][lane];
     return s;
   };
-  const bool by_group = a.groups >= kSumWaves;
-  float all = 0.0f, weighted = 0.0f;
-  for (int32_t g = by_group ? wave : 0; g < a.groups; g += by_group ? kSumWaves : 1) {
+  // first and last chunk of a group's rows; none: the last before the first
+  const auto chunks_of = [&](int32_t g, int32_t* c0, int32_t* c1) {
     int32_t r0, r1;
     if (a.cu) {
       r0 = a.cu[g];
@@ -237,26 +270,70 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_norm_grads(const NormArgs a,
       r0 = g * each;
       r1 = r0 + each;
     }
-    float s = 0.0f;
-    if (r1 > r0 && in) {
-      const int32_t c1 = (r1 - 1) / a.chunk_rows, step = by_group ? 1 : kSumWaves;
-      const float* p = a.part + kind * a.d + col;
-#pragma unroll 8
-      for (int32_t c = r0 / a.chunk_rows + (by_group ? 0 : wave); c <= c1; c += step) s += p[(static_cast<int64_t>(c) + g) * 3 * a.d];
+    *c0 = r0 / a.chunk_rows;
+    *c1 = r1 > r0 ? (r1 - 1) / a.chunk_rows : *c0 - 1;
+  };
+  const int64_t stride = 3 * static_cast<int64_t>(a.d);
+  const float* const column = a.part + kind * a.d + min(col, a.d - 1);
+  const auto place = [&](int32_t c, int32_t g) { return column[(static_cast<int64_t>(c) + g) * stride]; };
+  float own = 1.0f;
+  if (mine) load_any<1>(a.wtype, mine, 0, 0, a.d, col, &own);
+
+  if (blockIdx.z > 0) {
+    if (!out || !out_ld) return;
+    constexpr int kAhead = 8;  // loads under way together: one that is not there reads the last place
+    for (int32_t g = blockIdx.z - 1; g < a.groups; g += own_z) {
+      int32_t c0, c1;
+      chunks_of(g, &c0, &c1);
+      float s = 0.0f;
+      for (int32_t c = c0 + wave; c <= c1; c += kAhead * kSumWaves) {
+        float v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) v[k] = place(min(c + k * kSumWaves, c1), g);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) s += c + k * kSumWaves <= c1 ? v[k] : 0.0f;
+      }
+      s = meet_up(s);
+      if (wave == 0) put(out, a.mtype, g, out_ld, s * own);
     }
-    float f = 1.0f;
-    if (theirs && total) {
-      load_any<1>(a.mtype, theirs, g, theirs_ld, a.d, col, &f);
-      if (kind == 0) f += 1.0f;
+    return;
+  }
+
+  const bool shared = out && !out_ld;
+  if (!shared && !total) return;
+  // all places of all groups in one row, of which a wave has every sixteenth
+  constexpr int kAhead = 16;
+  int32_t g = 0, c, c1;
+  chunks_of(0, &c, &c1);
+  const auto advance = [&](int32_t by) {  // to the by-th place from here; g == a.groups behind the last
+    c += by;
+    while (c > c1) {
+      const int32_t over = c - c1 - 1;
+      if (++g >= a.groups) return;
+      chunks_of(g, &c, &c1);
+      c += over;
     }
-    weighted = __builtin_fmaf(f, s, weighted);
-    all += s;
-    if (out && out_ld) {
-      if (!by_group) s = meet_up(s);
-      if (by_group || wave == 0) put(out, a.mtype, g, out_ld, s * own);
+  };
+  advance(wave);
+  float all = 0.0f, weighted = 0.0f;
+  while (g < a.groups) {
+    float v[kAhead], f[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      v[k] = 0.0f;
+      f[k] = 1.0f;
+      if (g >= a.groups) continue;
+      v[k] = place(c, g);
+      if (theirs && total) load_any<1>(a.mtype, theirs, g, theirs_ld, a.d, col, &f[k]);
+      advance(kSumWaves);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      all += v[k];
+      weighted = __builtin_fmaf(theirs && kind == 0 ? 1.0f + f[k] : f[k], v[k], weighted);
     }
   }
-  if (out && !out_ld) {
+  if (shared) {
     const float s = meet_up(all);
     if (wave == 0) put(out, a.mtype, 0, 0, s * own);
   }
@@ -280,19 +357,22 @@ template <int TX, int TY> int by_width(const NormArgs& a, bool wide, hipStream_t
     return launch<TX, TY, 1, 32, 8, true>(a, stream);
   }
   if (a.d <= 512) return launch<TX, TY, 8, 1, 1>(a, stream);
-  if (a.d <= 1024) return launch<TX, TY, 8, 2, 1>(a, stream);
+  // one column a thread as far as a workgroup goes: a thread then holds the next row's inputs too
+  if (a.d <= 1024) return launch<TX, TY, 8, 1, 2>(a, stream);
   if (a.d <= 1536) return launch<TX, TY, 8, 1, 3>(a, stream);
   if (a.d <= 2048) return launch<TX, TY, 8, 1, 4>(a, stream);
-  if (a.d <= 4096) return launch<TX, TY, 8, 2, 4>(a, stream);
-  if (a.d <= 8192) return launch<TX, TY, 8, 2, 8>(a, stream);
+  if (a.d <= 4096) return launch<TX, TY, 8, 1, 8>(a, stream);
+  if (a.d <= 8192) return TX == kF32 ? launch<TX, TY, 8, 2, 8>(a, stream) : launch<TX, TY, 8, TX == kF32 ? 2 : 1, TX == kF32 ? 8 : 16>(a, stream);
   return launch<TX, TY, 8, 4, 8, true>(a, stream);
 }
 
 }  // namespace
 
-// Enough chunks to fill the card, few enough that their sums are little beside the rows.
-int32_t norm_chunk_rows(int64_t n, int32_t, int cus) {
-  const int64_t chunks = std::min<int64_t>(n, static_cast<int64_t>(cus) * 4);
+// As many chunks as workgroups are resident at once (32760 rows of 1536, a stream in fp32: 2, 4 and 6 for each compute unit 226, 200
+// and 227 us; 9001 rows of 4096 in bf16: 2 and 4 134 and 139).
+int32_t norm_chunk_rows(int64_t n, int32_t d, int cus) {
+  const int each = d <= 512 ? 4 : d <= 1024 ? 6 : d <= 2048 ? 4 : d <= 4096 ? 2 : 1;
+  const int64_t chunks = std::min<int64_t>(n, static_cast<int64_t>(cus) * each);
   return static_cast<int32_t>(std::max<int64_t>(1, (n + chunks - 1) / std::max<int64_t>(1, chunks)));
 }
 
@@ -304,7 +384,8 @@ int launch_block_norm_backward(const NormArgs& a, const NormGrads& g, int stream
   else if (branch_type == kF16) e = by_width<kF32, kF16>(a, wide, stream);
   else e = by_width<kF32, kF32>(a, wide, stream);
   if (e || !a.part) return e;
-  hipLaunchKernelGGL(k_norm_grads, dim3((a.d + 63) / 64, 3), dim3(64 * kSumWaves), 0, stream, a, g);
+  const int own_z = std::min(a.groups, 256);
+  hipLaunchKernelGGL(k_norm_grads, dim3((a.d + 63) / 64, 3, own_z + 1), dim3(64 * kSumWaves), 0, stream, a, g, own_z);
   return static_cast<int>(hipGetLastError());
 }
 

@@ -61,6 +61,26 @@ template <int DT, int E> __device__ __forceinline__ void store(Rsrc r, uint32_t 
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, col * 2, 0, 0);
   }
 }
+// 8 entries on their way: fetched, and made floats where they are needed
+template <int DT> struct Piece {
+  static constexpr int kSize = sizeof(typename Elem<DT>::T), kWords = kSize / 2;
+  u32x4_t raw[kWords];
+  __device__ __forceinline__ void fetch(Rsrc r, uint32_t col) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) raw[k] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, col * kSize, 16 * k, 0));
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    if constexpr (DT == kF32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __builtin_bit_cast(float, static_cast<uint32_t>(raw[i / 4][i % 4]));
+    } else {
+      typedef typename Elem<DT>::T V __attribute__((ext_vector_type(8)));
+      const V v = __builtin_bit_cast(V, raw[0]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(v[i]);
+    }
+  }
+};
 // of a type that is the same for a whole launch
 template <int E> __device__ __forceinline__ void load_any(int type, const void* p, int64_t row, int64_t ld, int32_t d, uint32_t col, float* f) {
   const Rsrc r = row_at(p, row, ld, d, type == kF32 ? 4 : 2);

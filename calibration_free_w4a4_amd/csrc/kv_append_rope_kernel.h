@@ -262,11 +262,14 @@ template <int DT, int D, int PAGE, bool HALVES> struct Turned {
   }
 };
 
-constexpr int kPageQueries = 1;   // queries go with the pages from so many pages of new tokens on
-#ifndef WPC
-#define WPC 16
-#endif
-constexpr int kWavesPerCu = WPC;
+// The registers of four waves a SIMD for pages of which a thread has up to four columns (4680 tokens, 12 + 12 heads of 128: 20.4 us,
+// with what the compiler takes by itself, three waves, 23.4; five 31.5), what they need for larger ones.
+constexpr int waves_for(int bytes) { return bytes <= 8192 ? 4 : 1; }
+// Queries go with the pages where a sequence may fill one.
+constexpr int kPageQueries = 1;
+// Waves for each compute unit that the pages' heads are dealt to: fewer share the sines of more heads and the way to the page
+// (same call: 12 19.2 us, 8 20.8, 6 26.0, 16 20.4, 24 22.7).
+constexpr int kWavesPerCu = 12;
 
 struct AppendGrid {
   int64_t kv_items;          // workgroups of pages, for each sequence
@@ -278,7 +281,7 @@ struct AppendGrid {
 };
 
 template <int DT, int D, int PAGE, bool HALVES>
-__global__ __launch_bounds__(threads_for(D* PAGE)) void k_append_rope(const KvCache c, const KvTokens x, const TurnArgs r, const AppendGrid g) {
+__global__ __launch_bounds__(threads_for(D* PAGE), waves_for(D* PAGE)) void k_append_rope(const KvCache c, const KvTokens x, const TurnArgs r, const AppendGrid g) {
   using S = Share<D, PAGE>;
   using C = Column<DT, D, HALVES>;
   using T = typename Elem<DT>::T;
