@@ -119,12 +119,18 @@ int check_epilogue(const orbq_epilogue* p, int64_t n, int64_t m, orbq_dtype y_ty
   return ORBQ_OK;
 }
 
+// Whether the product takes the few-row form.  An epilogue that adds nothing to the product gives orbq_lut_gemm_act's bits at
+// any size, so it takes that product's tiles.
+bool few_rows(const orbq::ProductEpilogue& ep, int64_t n, int64_t m, int64_t d) {
+  return (ep.bias || ep.gate || ep.residual) && orbq::takes_few_rows(n, m, d);
+}
+
 int launch_product(const uint8_t* x_codes, const float* x_norms, const orbq::DecodeParams& da, const uint8_t* w_codes,
                    const void* w_norms, const orbq_codebook* cb_w, int64_t n, int64_t m, int64_t d, void* Y, orbq_dtype y_type,
                    int64_t ldy, const orbq::ProductEpilogue& ep, void* stream, const char* what) {
   orbq::DecodeParams dw;
   orbq::build_decode_params(cb_w->centroids, cb_w->bits, &dw);
-  const auto launch = da.bits != 16 && orbq::takes_few_rows(n, d) ? orbq::launch_lut_gemm_few : orbq::launch_lut_gemm_fused;
+  const auto launch = da.bits != 16 && few_rows(ep, n, m, d) ? orbq::launch_lut_gemm_few : orbq::launch_lut_gemm_fused;
   return hip_status(launch(x_codes, x_norms, da, w_codes, static_cast<const uint16_t*>(w_norms), dw, n, m, d, Y, y_type == ORBQ_BF16,
                            ldy, ep, static_cast<hipStream_t>(stream)), what);
 }
@@ -301,8 +307,8 @@ ORBQ_API int orbq_linear_fused(const void* X, int64_t n, int64_t d, int64_t ldx,
   if (!aligned(workspace, 256)) return set_error(ORBQ_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", what);
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   float* norms = reinterpret_cast<float*>(codes + orbq::layer::codes_bytes(n, d, cb_a->bits));
-  // 6-bit activations as in orbq_linear; few rows are decoded once for each 16 weight rows of a workgroup either way
-  const bool decoded = orbq::layer::keeps_centroids(cb_a->bits, m) && !orbq::takes_few_rows(n, d);
+  // 6-bit activations as in orbq_linear; the few-row form takes codes
+  const bool decoded = orbq::layer::keeps_centroids(cb_a->bits, m) && !few_rows(ep, n, m, d);
   const orbq::QuantMode mode = decoded ? orbq::QuantMode::kDecoded : orbq::QuantMode::kActivations;
   if ((s = orbq::layer::quantize_rows(mode, X, n, d, ldx, rot, cb_a, eps, codes, norms, 4, stream, what))) return s;
   orbq::DecodeParams da{};

@@ -154,7 +154,7 @@ int launch_lut_gemm_fused(const uint8_t* x_codes, const float* x_norms, const De
                           int y_bf16, int64_t ldy, const ProductEpilogue& ep, hipStream_t stream);
 
 // The form for few token rows, whose sums are in another order.
-bool takes_few_rows(int64_t n, int64_t d);
+bool takes_few_rows(int64_t n, int64_t m, int64_t d);
 int launch_lut_gemm_few(const uint8_t* x_codes, const float* x_norms, const DecodeParams& da, const uint8_t* w_codes,
                         const uint16_t* w_norms, const DecodeParams& dw, int64_t n, int64_t m, int64_t d, void* Y,
                         int y_bf16, int64_t ldy, const ProductEpilogue& ep, hipStream_t stream);

@@ -4,7 +4,7 @@
 namespace orbq {
 namespace lg {
 
-hipError_t launch_few_a6(int bw, int cb, const FewArgs& a, hipStream_t st) { return launch_few_ba<6>(bw, cb, a, st); }
+hipError_t launch_few_a6(int bw, const FewPlan& p, const FewArgs& a, hipStream_t st) { return launch_few_ba<6>(bw, p, a, st); }
 
 }  // namespace lg
 }  // namespace orbq

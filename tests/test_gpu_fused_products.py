@@ -125,6 +125,24 @@ def test_lut_gemm(orbq, n, m, d, ba, bw, groups, cu, name):
         c.check(c.call(ALL, "none", name), ALL, "none", name)
 
 
+@pytest.mark.parametrize("ba,bw", [(2, 2), (2, 4), (2, 6), (3, 3), (4, 2), (4, 4), (4, 6), (6, 2), (6, 4), (6, 6)])
+def test_every_few_row_form(orbq, ba, bw):
+    """16, 32 and 64 tokens of a workgroup, 16 and 32 weight rows, 16 and 4 waves; one and several super-steps of a wave, ends within
+    a block of tokens and of weight rows."""
+    for n, m, d in ((7, 72, 2176), (13, 4200, 384), (20, 72, 640), (50, 88, 2176), (70, 2200, 640), (200, 2200, 2176), (1100, 520, 384)):
+        c = Case(orbq, n, m, d, ba, bw, 2, [0, n // 3, n], seed=5)
+        for name in ("f32", "bf16"):
+            c.check(c.call(ALL, "gelu_tanh", name), ALL, "gelu_tanh", name)
+
+
+def test_either_side_of_the_few_rows(orbq):
+    """64 and 65 tokens, and sizes of which the tiles take some and the few-row form the others."""
+    for n, m, d in ((64, 520, 256), (65, 520, 256), (64, 16400, 256), (65, 16400, 256), (300, 6000, 128), (800, 6000, 128), (4096, 64, 128),
+                    (4097, 64, 128)):
+        c = Case(orbq, n, m, d, 4, 4, 1, None, seed=6)
+        c.check(c.call(ALL, "none", "bf16"), ALL, "none", "bf16")
+
+
 @pytest.mark.parametrize("name", ["f32", "bf16"])
 @pytest.mark.parametrize("n,m,d", [(9, 104, 256), (64, 1000, 128), (200, 104, 256), (800, 1000, 128)])
 def test_strides_in_place_and_rows_left_alone(orbq, n, m, d, name):
