@@ -447,6 +447,7 @@ __device__ __forceinline__ void fused_part(const FusedArgs& a, const float* stag
         to[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, roff + static_cast<uint32_t>((it + k) * R * o.ldr * esz), 0, 0);
     }
   };
+  int32_t held = -1;  // the group that g is of, where the tile's rows have several
   v4u_t res[G], next[G];
   fetch(0, res);
 #pragma unroll 1
@@ -471,16 +472,18 @@ __device__ __forceinline__ void fused_part(const FusedArgs& a, const float* stag
         for (int c = 0; c < E; ++c) v[c] = gelu_erf(v[c]);
       }
       if (row + down >= rows) continue;
-      if (one_group) {
-#pragma unroll
-        for (int c = 0; c < E; ++c) v[c] *= g[c];
-      } else {
+      if (!one_group) {
         const int32_t group = groups[down];
         if (group < 0) continue;
+        if (o.gate && group != held) {
+          const int64_t at = group * o.gld + col0;
 #pragma unroll
-        for (int c = 0; c < E; ++c)
-          if (o.gate && col + c < cols) v[c] *= entry_of(o.gate, o.gate_f32, group * o.gld + col0 + col + c);
+          for (int c = 0; c < E; ++c) g[c] = entry_of(o.gate, o.gate_f32, at + min(col + c, cols - 1));
+          held = group;
+        }
       }
+#pragma unroll
+      for (int c = 0; c < E; ++c) v[c] *= g[c];
       if (whole) {
         v4u_t out;
 #pragma unroll
