@@ -1,0 +1,117 @@
+"""A video transformer's block, generated frame by frame for a batch of clips: the norms before and between its branches
+with their modulations, quantized projections with bias, GELU, gate and residual in their epilogue, q and k normalised and turned
+on their way into an 8-bit cache of the frames so far, and attention over it.
+
+    python examples/video_transformer_block.py                # 1536 wide, 12 heads, 8960 hidden, 21 frames of 30 x 52 tokens
+    python examples/video_transformer_block.py --clips 2 --frames 6 --chunk 2 --height 8 --width 12
+
+Weights and activations are random (this repository has no trained ones); the sizes are those of the video layers in
+workloads/.  The residual stream is kept in 32 bits and updated in place.
+"""
+from __future__ import annotations
+
+import argparse
+import os
+import sys
+import time
+
+import numpy as np
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+import calibration_free_w4a4_amd as orbq  # noqa: E402
+import workloads  # noqa: E402
+
+
+class Projection:
+    """A folded linear layer with a bias."""
+
+    def __init__(self, d: int, m: int, bits: int, block: int, seed: int):
+        dev = torch.device("cuda", torch.cuda.current_device())
+        self.rot = orbq.Rotation.create(d, block, *workloads.rotation(d))
+        self.cb = orbq.Codebook.lloyd_max(d, bits)
+        w = torch.from_numpy(workloads.weights(m, d, seed).view(np.int16)).view(torch.bfloat16).to(dev)
+        self.w = orbq.fold_weights(w, self.rot, self.cb)
+        self.bias = 0.1 * torch.randn(m, generator=torch.Generator(device=dev).manual_seed(seed), device=dev)
+
+    def __call__(self, x, **how):
+        return orbq.linear(x, self.rot, self.cb, *self.w, self.cb, bias=self.bias, **how)
+
+    def from_16_bits(self, x, **how):
+        """From activations that are not quantized: the few rows of the conditioning."""
+        return orbq.linear_a16(x, self.rot, *self.w, self.cb, bias=self.bias, **how)
+
+
+class StreamingBlock:
+    """One block for `clips` sequences of one length: d = heads * head_dim, W4A4 projections, int8 cache for up to max_tokens of each."""
+
+    def __init__(self, d: int, heads: int, hidden: int, clips: int, max_tokens: int, tokens_per_frame: int, dims=(44, 42, 42),
+                 block: int = 128, bits: int = 4, page_tokens: int = 64, seed: int = 7):
+        dev = torch.device("cuda", torch.cuda.current_device())
+        self.d, self.heads, self.hd, self.clips, self.frame = d, heads, d // heads, clips, tokens_per_frame
+        self.modulation = Projection(d, 6 * d, bits, block, seed)
+        self.qkv = Projection(d, 3 * d, bits, block, seed + 1)
+        self.out = Projection(d, d, bits, block, seed + 2)
+        self.up = Projection(d, hidden, bits, block, seed + 3)
+        self.down = Projection(hidden, d, bits, block, seed + 4)
+        self.q_weight, self.k_weight = 1 + 0.1 * torch.randn((2, self.hd), generator=torch.Generator().manual_seed(seed)).to(dev)
+        self.rope = orbq.Rope.create(dims)
+        pages = (max_tokens + page_tokens - 1) // page_tokens
+        self.cache = orbq.KVCache.create(clips * pages, heads, self.hd, page_tokens)
+        self.table = torch.arange(clips * pages, dtype=torch.int32, device=dev).view(clips, pages)
+        self.held = torch.zeros(clips, dtype=torch.int32, device=dev)   # on the GPU: a step never waits for the host
+
+    def step(self, x, positions, condition):
+        """x float32 [clips * n, d], the tokens of whole frames in order, clip after clip, updated in place; positions float32
+        [n, 3], the same for every clip; condition bf16 [clips, d]."""
+        n = x.shape[0] // self.clips
+        m = self.modulation.from_16_bits(condition, out_dtype=torch.float32).view(self.clips, 6, self.d)
+        shift1, scale1, gate1, shift2, scale2, gate2 = m.unbind(1)       # slices of one tensor: nothing is copied
+        _, h = orbq.block_norm(x, scale=scale1, shift=shift1, dtype=torch.bfloat16)
+        q, k, v = self.qkv(h, out_dtype=torch.bfloat16).view(-1, 3, self.heads, self.hd).unbind(1)
+        orbq.kv_append_rope(self.cache, self.rope, positions, q, k, v, self.table, self.held, q_weight=self.q_weight,
+                            k_weight=self.k_weight, out=q)
+        self.held += n
+        o = orbq.kv_attention(self.cache, q, self.table, self.held, causal_block=self.frame)
+        y = self.out(o.view(-1, self.d), out_dtype=torch.bfloat16)
+        _, h = orbq.block_norm(x, y, gate=gate1, scale=scale2, shift=shift2, out=(x, h))
+        u = self.up(h, act="gelu_tanh", out_dtype=torch.bfloat16)
+        return self.down(u, gate=gate2, residual=x, out=x)
+
+
+def grid_positions(frames: range, height: int, width: int, device="cuda"):
+    """(time, height, width) of each token of some frames, float32 [tokens, 3]."""
+    return torch.cartesian_prod(torch.arange(frames.start, frames.stop, dtype=torch.float32, device=device),
+                                torch.arange(height, dtype=torch.float32, device=device),
+                                torch.arange(width, dtype=torch.float32, device=device)).reshape(-1, 3)
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
+    ap.add_argument("--width-d", type=int, default=1536, help="model width")
+    ap.add_argument("--heads", type=int, default=12)
+    ap.add_argument("--hidden", type=int, default=8960)
+    ap.add_argument("--clips", type=int, default=1)
+    ap.add_argument("--frames", type=int, default=21)
+    ap.add_argument("--chunk", type=int, default=3, help="frames a step")
+    ap.add_argument("--height", type=int, default=30)
+    ap.add_argument("--width", type=int, default=52)
+    a = ap.parse_args()
+    frame = a.height * a.width
+    block = StreamingBlock(a.width_d, a.heads, a.hidden, a.clips, a.frames * frame, frame)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    for f in range(0, a.frames, a.chunk):
+        frames = range(f, min(f + a.chunk, a.frames))
+        x = torch.randn((a.clips * len(frames) * frame, a.width_d), generator=gen, device="cuda")
+        condition = torch.randn((a.clips, a.width_d), generator=gen, device="cuda").bfloat16()
+        pos = grid_positions(frames, a.height, a.width)
+        torch.cuda.synchronize()
+        t = time.perf_counter()
+        y = block.step(x, pos, condition)
+        torch.cuda.synchronize()
+        print(f"frames {frames.start}-{frames.stop - 1}: {x.shape[0]} tokens over {a.clips * frames.stop * frame} cached, "
+              f"{(time.perf_counter() - t) * 1e3:.2f} ms, |x| {y.norm().item():.4g}", flush=True)
+
+
+if __name__ == "__main__":
+    main()
