@@ -5,7 +5,10 @@
 //   dscale = weight A, dshift = S, dgate = post_weight B, dweight = sum over g (1 + scale) A,
 //   dpost_weight = sum over g gate B.
 // Nothing is kept from the forward pass but r, which it has written, and y: a row's statistics are taken again from
-// the registers that hold it.  r, y, dr and dh are read once, dx and dy written once: HBM's bytes bound the call.
+// the registers that hold it.  r, y, dr and dh are read once, dx and dy written once: HBM's bytes bound the call.  32760 rows of
+// 1536, the stream in fp32 and the branch in bf16 (906 MB): 189 us, 4.8 TB/s; 9001 rows of 4096 in bf16 in 7 groups, rms norms on
+// either side (442 MB): 98 us, 4.5 TB/s; the second launch 10 and 20 us.  What took it there, us of the latter: the next row fetched
+// ahead 165 -> 136, the groups' factors kept in LDS 136 -> 119, sums handed on in registers 119 -> 98.
 //
 // The sums over rows need no atomics and do not depend on scheduling: a workgroup owns a chunk of consecutive rows, and
 // the sums of (chunk c, group g) go to place c + g, which no other pair has, since along the rows each step
@@ -29,6 +32,10 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(const NormArgs 
   constexpr int TEAMS = teams_of(W);
   constexpr bool AHEAD = E == 8 && !LATE;
   __shared__ float place[2][W][2];
+  // weight (1 + scale) and gate post_weight of the group at hand: a thread's own columns, so that nothing has to be waited for
+  constexpr int PIECES = E == 8 ? 2 : 1, T = threads_of(W);
+  typedef float Part __attribute__((ext_vector_type(E == 8 ? 4 : 1)));
+  __shared__ Part kept[LATE ? 1 : 2][LATE ? 1 : V * PIECES][LATE ? 1 : T];
   __shared__ float joined[TEAMS > 1 ? TEAMS - 1 : 1][TEAMS > 1 ? V * 64 * E : 1];
   const int team = W == 1 ? threadIdx.x >> 6 : 0, t = W == 1 ? threadIdx.x & 63 : threadIdx.x;
   int turn = 0;
@@ -65,6 +72,55 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(const NormArgs 
     }
     Row A, S, B;
     ORBQ_EACH(A[i][e] = S[i][e] = B[i][e] = 0.0f)
+    // v times the factors 0: weight (1 + scale), 1: gate post_weight, from memory
+    const auto times = [&](int which, int i, float* v) {
+      float w[E];
+      const void* const per_column = which ? a.pw : a.w;
+      const void* const per_group = which ? a.gate : a.scale;
+      if (per_column) {
+        load_any<E>(a.wtype, per_column, 0, 0, a.d, col[i], w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= w[e];
+      }
+      if (per_group) {
+        load_any<E>(a.mtype, per_group, g, which ? a.gld : a.scld, a.d, col[i], w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= which ? w[e] : 1.0f + w[e];
+      }
+    };
+    if constexpr (!LATE) {
+#pragma unroll
+      for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float v[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] = 1.0f;
+          times(which, i, v);
+#pragma unroll
+          for (int k = 0; k < PIECES; ++k) {
+            Part p;
+#pragma unroll
+            for (int e = 0; e < E / PIECES; ++e) p[e] = v[k * (E / PIECES) + e];
+            kept[which][i * PIECES + k][threadIdx.x] = p;
+          }
+        }
+    }
+    const auto apply = [&](int which, Row& v) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (LATE) {
+          times(which, i, v[i]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < PIECES; ++k) {
+            const Part p = kept[which][i * PIECES + k][threadIdx.x];
+#pragma unroll
+            for (int e = 0; e < E / PIECES; ++e) v[i][k * (E / PIECES) + e] *= p[e];
+          }
+        }
+      }
+    };
     // AHEAD: the next row's inputs are under way while one is worked on
     struct Inputs {
       Piece<TX> r[V], dr[V];
@@ -125,7 +181,7 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(const NormArgs 
         if (v_layer || w_layer) {
           ORBQ_EACH(s += v[i][e])
           if (both) ORBQ_EACH(u += w[i][e])
-          sum(&s, both ? &u : nullptr, place, turn);
+          sum(s, u, place, turn);
           const float mv = v_layer ? s / static_cast<float>(a.d) : 0.0f, mw = w_layer ? u / static_cast<float>(a.d) : 0.0f;
           ORBQ_EACH(v[i][e] = col[i] < a.d ? v[i][e] - mv : 0.0f)
           if (both) ORBQ_EACH(w[i][e] = col[i] < a.d ? w[i][e] - mw : 0.0f)
@@ -133,7 +189,7 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(const NormArgs 
         }
         ORBQ_EACH(s = __builtin_fmaf(v[i][e], v[i][e], s))
         if (both) ORBQ_EACH(u = __builtin_fmaf(w[i][e], w[i][e], u))
-        sum(&s, both ? &u : nullptr, place, turn);
+        sum(s, u, place, turn);
         *fv = 1.0f / __builtin_sqrtf(s / static_cast<float>(a.d) + v_eps);
         ORBQ_EACH(v[i][e] *= *fv)
         if (both) {
@@ -146,22 +202,9 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(const NormArgs 
       if (normed) {
         float m = 0.0f, p = 0.0f;
         ORBQ_EACH(A[i][e] = __builtin_fmaf(dh[i][e], r[i][e], A[i][e]); S[i][e] += dh[i][e])
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float w[E];
-          if (a.w) {
-            load_any<E>(a.wtype, a.w, 0, 0, a.d, col[i], w);
-#pragma unroll
-            for (int e = 0; e < E; ++e) dh[i][e] *= w[e];
-          }
-          if (a.scale) {
-            load_any<E>(a.mtype, a.scale, g, a.scld, a.d, col[i], w);
-#pragma unroll
-            for (int e = 0; e < E; ++e) dh[i][e] *= 1.0f + w[e];
-          }
-        }
+        apply(0, dh);
         ORBQ_EACH(m += dh[i][e]; p = __builtin_fmaf(dh[i][e], r[i][e], p))
-        sum(&p, layer ? &m : nullptr, place, turn);
+        sum(p, m, place, turn);
         m = layer ? m * each : 0.0f;
         p *= each;
         ORBQ_EACH(dr[i][e] = col[i] < a.d ? __builtin_fmaf(f, __builtin_fmaf(-r[i][e], p, dh[i][e] - m), dr[i][e]) : 0.0f)
@@ -174,24 +217,11 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(const NormArgs 
       if (posted && (LATE || !normed)) factors(y, y, false, post_layer, false, a.post_eps, 0.0f, &fy, &fy);
       ORBQ_EACH(B[i][e] = __builtin_fmaf(dr[i][e], y[i][e], B[i][e]))
       if (!a.dy) continue;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float w[E];
-        if (a.gate) {
-          load_any<E>(a.mtype, a.gate, g, a.gld, a.d, col[i], w);
-#pragma unroll
-          for (int e = 0; e < E; ++e) dr[i][e] *= w[e];
-        }
-        if (a.pw) {
-          load_any<E>(a.wtype, a.pw, 0, 0, a.d, col[i], w);
-#pragma unroll
-          for (int e = 0; e < E; ++e) dr[i][e] *= w[e];
-        }
-      }
+      apply(1, dr);
       if (posted) {
         float m = 0.0f, p = 0.0f;
         ORBQ_EACH(m += dr[i][e]; p = __builtin_fmaf(dr[i][e], y[i][e], p))
-        sum(&p, post_layer ? &m : nullptr, place, turn);
+        sum(p, m, place, turn);
         m = post_layer ? m * each : 0.0f;
         p *= each;
         ORBQ_EACH(dr[i][e] = fy * __builtin_fmaf(-y[i][e], p, dr[i][e] - m))
@@ -368,8 +398,8 @@ template <int TX, int TY> int by_width(const NormArgs& a, bool wide, hipStream_t
 
 }  // namespace
 
-// As many chunks as workgroups are resident at once (32760 rows of 1536, a stream in fp32: 2, 4 and 6 for each compute unit 226, 200
-// and 227 us; 9001 rows of 4096 in bf16: 2 and 4 134 and 139).
+// As many chunks as workgroups are resident at once (32760 rows of 1536, a stream in fp32, of the kernel at 200 us: 2, 4 and 6 for each
+// compute unit 226, 200 and 227; 9001 rows of 4096 in bf16, of the kernel at 134: 2 and 4 134 and 139).
 int32_t norm_chunk_rows(int64_t n, int32_t d, int cus) {
   const int each = d <= 512 ? 4 : d <= 1024 ? 6 : d <= 2048 ? 4 : d <= 4096 ? 2 : 1;
   const int64_t chunks = std::min<int64_t>(n, static_cast<int64_t>(cus) * each);

@@ -104,27 +104,35 @@ __device__ __forceinline__ float wave_sum(float x) {
   return (lane_of(x, 0) + lane_of(x, 16)) + (lane_of(x, 32) + lane_of(x, 48));
 }
 
-// Two sums at once over the W waves that hold a row.  `turn` tells successive sums apart: two places are enough, since
+// One or two sums over the W waves that hold a row.  `turn` tells successive sums apart: two places are enough, since
 // a wave writes a place again only behind the barrier of the sum between, which every wave reaches after reading.
 template <int W> struct RowSum {
-  __device__ __forceinline__ void operator()(float* a, float* b, float (*place)[W][2], int& turn) const {
-    *a = wave_sum(*a);
-    if (b) *b = wave_sum(*b);
+  __device__ __forceinline__ void operator()(float& a, float (*place)[W][2], int& turn) const {
+    a = wave_sum(a);
     if constexpr (W > 1) {
-      const int wave = threadIdx.x >> 6;
+      if ((threadIdx.x & 63) == 0) place[turn][threadIdx.x >> 6][0] = a;
+      __syncthreads();
+      a = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) a += place[turn][w][0];
+      turn ^= 1;
+    }
+  }
+  __device__ __forceinline__ void operator()(float& a, float& b, float (*place)[W][2], int& turn) const {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (W > 1) {
       if ((threadIdx.x & 63) == 0) {
-        place[turn][wave][0] = *a;
-        if (b) place[turn][wave][1] = *b;
+        place[turn][threadIdx.x >> 6][0] = a;
+        place[turn][threadIdx.x >> 6][1] = b;
       }
       __syncthreads();
-      float s = 0.0f, t = 0.0f;
+      a = b = 0.0f;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        s += place[turn][w][0];
-        if (b) t += place[turn][w][1];
+        a += place[turn][w][0];
+        b += place[turn][w][1];
       }
-      *a = s;
-      if (b) *b = t;
       turn ^= 1;
     }
   }
