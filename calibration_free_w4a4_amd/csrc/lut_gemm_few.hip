@@ -16,7 +16,7 @@ namespace {
 //   1536 -> 8960, 5 and 128 tokens            6.4 / 5.9 / -         25 / 23 / 20
 // 32 tokens x 32 rows never came out ahead of x 16 (1536 -> 8960: 8.5 against 8.3).
 FewPlan plan_few(int64_t n, int64_t m, int64_t d) {
-  const int64_t cus = device_cus(), nss = d / kFewSS;
+  const int64_t cus = device_cus(), nss = (d + kFewSS - 1) / kFewSS;
   FewPlan p;
   p.tokens = n <= 16 ? 16 : n <= 32 ? 32 : 64;
   const auto blocks = [&](int cb) { return (n + p.tokens - 1) / p.tokens * ((m + 16 * cb - 1) / (16 * cb)); };
@@ -36,9 +36,9 @@ FewPlan plan_few(int64_t n, int64_t m, int64_t d) {
 // 512 tokens 29 / 42 and 53 / 43 us; 4096 -> 4096, 1024 and 2048 tokens 78 / 88 and 136 / 90; other bit widths are within a
 // third of that, and on the same side but for A6 x W4 (512 tokens of the former 78 / 100).
 bool takes_few_rows(int64_t n, int64_t m, int64_t d) {
-  if (d % kFewSS || n > 4096) return false;
+  if (n > 4096) return false;
   if (n <= 64) return true;
-  const int64_t cus = device_cus(), nss = d / kFewSS;
+  const int64_t cus = device_cus(), nss = (d + kFewSS - 1) / kFewSS;
   const int64_t tiles = (n + 255) / 256 * ((m + 255) / 256), blocks = (n + 63) / 64 * ((m + 31) / 32);
   return blocks * (nss + 18) < 12 * ((tiles + cus - 1) / cus) * cus * (nss + 4);
 }
@@ -57,7 +57,8 @@ int launch_lut_gemm_few(const uint8_t* x_codes, const float* x_norms, const Deco
   a.n = static_cast<int32_t>(n);
   a.xrb = static_cast<int32_t>(d * da.bits / 8);
   a.wrb = static_cast<int32_t>(d * dw.bits / 8);
-  a.nss = static_cast<int32_t>(d / kFewSS);
+  a.nss = static_cast<int32_t>((d + kFewSS - 1) / kFewSS);
+  a.half = d % kFewSS != 0;
   const FewPlan p = plan_few(n, m, d);
   a.per = (a.nss + p.splits - 1) / p.splits;
   a.splits = (a.nss + a.per - 1) / a.per;

@@ -7,7 +7,8 @@
 // As in the weight-only product (a16_gemm.hip) a workgroup owns 16 CB weight rows and its waves take one split of the K
 // range each; a super-step covers 128 codes, of which lane (m = l % 16, g = l / 16) holds codes 32 g .. 32 g + 31 of one
 // row, tokens and weights alike, decodes them 8 at a time and gives them to v_mfma_f32_16x16x32_bf16.  The splits' sums
-// meet in LDS and are added in split order.  The next super-step's codes are under way while one is multiplied.
+// meet in LDS and are added in split order.  The next super-step's codes are under way while one is multiplied.  Of a last half
+// super-step the tokens' other half is made zeros, whatever the codes there are.
 #pragma once
 
 #include <algorithm>
@@ -33,14 +34,16 @@ struct FewArgs {
   int64_t ldy, m;
   int32_t n, xrb, wrb;             // tokens; code bytes of a row
   int32_t nss, per, splits;        // super-steps, of a split, splits
+  int32_t half;                    // the last super-step is half one
   int32_t act, y_bf16;
   Tab4 ta, tw;
   uint16_t mag_a[32], mag_w[32];
   EpilogueArgs e;
 };
 
-// TB, CB: 16-row blocks of tokens and of weights; blockIdx.y counts the 16 TB tokens
-template <int BA, int BW, int TB, int CB, int SPLITS>
+// TB, CB: 16-row blocks of tokens and of weights; blockIdx.y counts the 16 TB tokens.  HALF: d ends with half a super-step
+// (looked for in one kernel for both, it took 15 % of 64 tokens' time)
+template <int BA, int BW, int TB, int CB, int SPLITS, bool HALF>
 __global__ __launch_bounds__(64 * SPLITS) void k_few(const FewArgs a) {
   constexpr int kRows = 16 * CB;
   __shared__ __align__(16) unsigned char lut_a[BA == 6 ? 4096 * 4 : 16];
@@ -83,11 +86,16 @@ __global__ __launch_bounds__(64 * SPLITS) void k_few(const FewArgs a) {
   if (ss0 < ss1) load(now, ss0);
   for (int ss = ss0; ss < ss1; ++ss) {
     if (ss + 1 < ss1) load(next, ss + 1);
+    const bool tail = HALF && ss + 1 == a.nss;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       bf16x8_t x[TB];
 #pragma unroll
-      for (int t = 0; t < TB; ++t) x[t] = __builtin_bit_cast(bf16x8_t, now.x[t].get(s, a.ta, lut_a));
+      for (int t = 0; t < TB; ++t) {
+        uint4 v = now.x[t].get(s, a.ta, lut_a);
+        if (HALF && tail) v = g < 2 ? v : uint4{0, 0, 0, 0};
+        x[t] = __builtin_bit_cast(bf16x8_t, v);
+      }
 #pragma unroll
       for (int c = 0; c < CB; ++c) {
         const bf16x8_t w = __builtin_bit_cast(bf16x8_t, now.w[c].get(s, a.tw, lut_w));
@@ -121,7 +129,8 @@ __global__ __launch_bounds__(64 * SPLITS) void k_few(const FewArgs a) {
 template <int BA, int BW, int TB, int CB, int SPLITS> hipError_t launch_few_form(const FewArgs& a, hipStream_t st) {
   const dim3 grid(static_cast<uint32_t>((a.m + 16 * CB - 1) / (16 * CB)), (a.n + 16 * TB - 1) / (16 * TB)), block(64 * a.splits);
   const size_t lds = static_cast<size_t>(a.splits) * std::min(a.n, 16 * TB) * 16 * CB * sizeof(float);
-  hipLaunchKernelGGL((k_few<BA, BW, TB, CB, SPLITS>), grid, block, lds, st, a);
+  if (a.half) hipLaunchKernelGGL((k_few<BA, BW, TB, CB, SPLITS, true>), grid, block, lds, st, a);
+  else hipLaunchKernelGGL((k_few<BA, BW, TB, CB, SPLITS, false>), grid, block, lds, st, a);
   return hipGetLastError();
 }
 

@@ -276,9 +276,9 @@ typedef struct {
 } orbq_epilogue;
 
 /* orbq_lut_gemm, orbq_linear and orbq_linear_a16 with that epilogue; arguments and errors as theirs.  An epilogue
- * without bias, gate and residual gives orbq_lut_gemm_act's bits.  With one of them, and d a multiple of 128, products of up
- * to 64 token rows, and of up to 4096 that orbq_lut_gemm's tiles would leave much of the chip idle with, take a form of
- * their own, whose sums are in another order; the other products' sums are orbq_lut_gemm's.  orbq_linear_a16_fused's
+ * without bias, gate and residual gives orbq_lut_gemm_act's bits.  With one of them, products of up to 64 token
+ * rows, and of up to 4096 that orbq_lut_gemm's tiles would leave much of the chip idle with, take a form of their own, whose
+ * sums are in another order; the other products' sums are orbq_lut_gemm's.  orbq_linear_a16_fused's
  * products are orbq_linear_a16's. */
 int orbq_lut_gemm_fused(const uint8_t* x_codes, const float* x_norms, const orbq_codebook* cb_a, const uint8_t* w_codes,
                         const void* w_norms, const orbq_codebook* cb_w, int64_t n, int64_t m, int64_t d,

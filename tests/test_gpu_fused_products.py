@@ -143,6 +143,50 @@ def test_either_side_of_the_few_rows(orbq):
         c.check(c.call(ALL, "none", "bf16"), ALL, "none", "bf16")
 
 
+# more rows than the few-row form has: tiles, of either shape, whole and ragged, with an odd count of K tiles
+TILES = [(4100, 72, 320, 4, 4, 2, None), (4608, 192, 256, 4, 4, 1, None), (5000, 256, 192, 2, 4, 2, None), (4300, 520, 448, 3, 3, 3, [0, 100, 100, 4300]),
+         (4400, 760, 256, 6, 4, 4, [7, 300, 1500, 2700, 4390]), (4200, 1000, 128, 4, 2, 4200, None), (4700, 264, 576, 6, 6, 2, None),
+         (4097, 8, 64, 4, 6, 1, None), (6000, 1536, 192, 2, 2, 3, [0, 900, 1900, 6000])]
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("n,m,d,ba,bw,groups,cu", TILES)
+def test_tiles(orbq, n, m, d, ba, bw, groups, cu, name):
+    log(f"lut_gemm fused tiles {name} n={n} m={m} d={d} A{ba} W{bw} groups={groups} cu={cu}")
+    c = Case(orbq, n, m, d, ba, bw, groups, cu, vectors="f32" if n % 2 else "bf16", seed=7)
+    for parts, act in ((ALL, "none"), (("bias",), "gelu_tanh"), (("gate", "residual"), "gelu_erf")):
+        c.check(c.call(parts, act, name), parts, act, name)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_tiles_in_place(orbq, name):
+    """Tiles that write a part of a wider tensor, onto the residual, and leave rows alone."""
+    torch = torch_mod()
+    n, m, d = 4300, 200, 192
+    c = Case(orbq, n, m, d, 4, 4, 3, [2, n // 2, n // 2, n - 3], seed=8)
+    want = c.call(ALL, "gelu_tanh", name)
+    res = torch.full((n, m + 24), 7.0, dtype=dtype_of(name), device="cuda")
+    r, rows = res[:, :m], slice(2, n - 3)
+    r.copy_(c.t["residual"][name])
+    before = r.clone()
+    c.t["residual"][name] = r
+    assert c.call(ALL, "gelu_tanh", name, out=r) is r
+    assert torch.equal(r[rows], want[rows]) and torch.equal(r[:2], before[:2]) and torch.equal(r[n - 3:], before[n - 3:])
+    assert bool((res[:, m:] == 7).all())
+    c.cu = [9, -4, 2 ** 31 - 1, 1]
+    c.call(ALL, "none", name, out=r)
+    assert bool((res[:, m:] == 7).all())
+
+
+@pytest.mark.parametrize("ba,bw", [(2, 2), (3, 3), (4, 4), (6, 6), (4, 6), (6, 2)])
+def test_half_a_super_step(orbq, ba, bw):
+    """Depths that are odd multiples of 64 in every few-row form."""
+    for n, m, d in ((7, 72, 64), (13, 4200, 192), (20, 72, 2112), (50, 88, 704), (70, 2200, 320), (200, 2200, 448)):
+        c = Case(orbq, n, m, d, ba, bw, 2, [0, n // 3, n], seed=9)
+        for name in ("f32", "bf16"):
+            c.check(c.call(ALL, "gelu_tanh", name), ALL, "gelu_tanh", name)
+
+
 @pytest.mark.parametrize("name", ["f32", "bf16"])
 @pytest.mark.parametrize("n,m,d", [(9, 104, 256), (64, 1000, 128), (200, 104, 256), (800, 1000, 128)])
 def test_strides_in_place_and_rows_left_alone(orbq, n, m, d, name):
@@ -215,6 +259,22 @@ def test_linear_a16(orbq, n, m, d, bw, block, passes):
     y = c.t["residual"]["f32"].clone()
     orbq.linear_a16(*args, out=y, residual=y, bias=c.t["bias"])
     assert torch.equal(y, orbq.linear_a16(*args, residual=c.t["residual"]["f32"], bias=c.t["bias"]))
+
+
+def test_graph_of_tiles(orbq):
+    torch = torch_mod()
+    c = Case(orbq, 4200, 72, 192, 4, 4, 2, [0, 1400, 4200], seed=10)
+    how, y = c.how(ALL, "bf16"), torch.empty((4200, 72), dtype=torch.bfloat16, device="cuda")
+    call = lambda out: orbq.lut_gemm(*c.x, c.cb_a, *c.w, c.cb_w, 192, out=out, act="gelu_erf", **how)  # noqa: E731
+    call(y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(y)
+    for k in range(3):
+        how["residual"].add_(1)
+        how["cu"].copy_(torch.tensor([0, 1400 + k, 4200], dtype=torch.int32))
+        graph.replay()
+        assert torch.equal(y, call(torch.empty_like(y)))
 
 
 def test_no_rows_and_no_columns(orbq):
