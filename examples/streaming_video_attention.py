@@ -7,7 +7,7 @@ over it.  Each step takes the tokens of some new frames; every token sees its ow
 
 Weights and activations are random (this repository has no trained ones); the sizes are those of the
 video layers in workloads/.  The normalisation of q and k that such layers have before the rotary
-positions is left out.
+positions is left out (video_transformer_block.py has it, in the append).
 """
 from __future__ import annotations
 
