@@ -162,9 +162,6 @@ ORBQ_API int orbq_block_norm(const orbq_norms* norms, int64_t n, int32_t d, cons
   a.rld = r_ld;
   a.hld = h_ld;
   const bool wide = vectors_fit(a) && fits(x, x_ld, ss) && fits(y, y_ld, bs) && fits(a.r, r_ld, ss) && fits(h, h_ld, bs);
-  // entry by entry, the root mean square of such wide rows comes out wrong: not offered
-  if (!wide && d > 4096 && norms->norm == ORBQ_NORM_RMS)
-    return set_error(ORBQ_ERR_UNSUPPORTED, "%s: rms norm of more than 4096 entries needs 16-byte columns", what);
   return hip_status(orbq::launch_block_norm(a, stream_type, branch_type, wide, static_cast<hipStream_t>(stream)), what);
 }
 

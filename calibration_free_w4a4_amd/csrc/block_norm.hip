@@ -22,20 +22,22 @@ template <int E, int V, int W>
 __device__ __forceinline__ void normalise(float (&v)[V][E], const int32_t (&col)[V], int32_t d, bool layer, float eps,
                                           float (*place)[W][2], int& turn) {
   const RowSum<W> sum;
-  float s = 0.0f;
+  // The mean is taken away either way: with the entries themselves on two paths, the compiler (ROCm 7.2) lost the copies of 14 of
+  // 16 on one of them (rms of rows beyond 4096 entries, entry by entry), and the squares were of what the registers held.
+  float s = 0.0f, mean = 0.0f;
   if (layer) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int e = 0; e < E; ++e) s += v[i][e];
     sum(s, place, turn);
-    const float mean = s / static_cast<float>(d);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[i][e] = col[i] < d ? v[i][e] - mean : 0.0f;
+    mean = s / static_cast<float>(d);
     s = 0.0f;
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[i][e] = col[i] < d ? v[i][e] - mean : 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll

@@ -478,9 +478,7 @@ int orbq_kv_attention(const orbq_kv_cache* cache, const orbq_page_table* table, 
  *               array is read, never validated: whatever it holds, no access leaves the buffers
  * Sums, statistics and products are in fp32, in an order that depends on d alone; r is rounded to stream_type, and h is
  * taken from the rounded r, so that it is what a later reader of r would get; h is rounded once.  Squares are
- * summed in fp32: magnitudes of 2^60 and above may overflow them.
- * orbq_block_norm refuses (ORBQ_ERR_UNSUPPORTED) norm ORBQ_NORM_RMS of rows beyond 4096 entries whose width, strides or
- * addresses are not multiples of 16 bytes. */
+ * summed in fp32: magnitudes of 2^60 and above may overflow them. */
 typedef enum { ORBQ_NORM_NONE = 0, ORBQ_NORM_LAYER = 1, ORBQ_NORM_RMS = 2 } orbq_norm_kind;
 typedef struct {
   orbq_norm_kind norm, post;

@@ -208,12 +208,12 @@ def test_both_ways(orbq, n, d, groups, cu, types, norm, post):
 
 
 @pytest.mark.parametrize("types", range(len(TYPES)))
-@pytest.mark.parametrize("d", [512, 1000, 1536, 2040, 4096, 8184, 16384, 509, 4001])
+@pytest.mark.parametrize("d", [512, 1000, 1536, 2040, 4096, 8184, 16384, 509, 4001, 9001])
 def test_every_form(orbq, d, types):
     """Each split of a row over registers, lanes and waves, in each type, with as many rows as make a workgroup take several."""
     log(f"block_norm forms d={d} {TYPES[types]}")
     for n, groups, cu, norm, post in ((1100, 2, [0, 500, 1100], "layer", "rms") if d < 1000 else (11, 2, [1, 4, 11], "layer", "rms"),
-                                      (9, 3, None, "rms", "layer"), (5, 1, None, "layer", None)):
+                                      (9, 3, None, "rms", "layer"), (5, 1, None, "layer", None), (6, 2, None, "rms", "rms"), (3, 1, None, "rms", None)):
         c = Case(n, d, groups, cu, *TYPES[types], norm, post, seed=types)
         r, h = orbq.block_norm(c.t["x"], dtype=dtype_of(c.branch), **c.how())
         c.check_forward(r, h)
