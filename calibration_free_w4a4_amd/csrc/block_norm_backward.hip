@@ -177,16 +177,18 @@ __global__ __launch_bounds__(threads_of(W)) void k_norm_backward(const NormArgs 
       }
       // v becomes the normalised row, and with it w where both are there
       const auto factors = [&](Row& v, Row& w, bool both, bool v_layer, bool w_layer, float v_eps, float w_eps, float* fv, float* fw) {
-        float s = 0.0f, u = 0.0f;
+        float s = 0.0f, u = 0.0f, mv = 0.0f, mw = 0.0f;
         if (v_layer || w_layer) {
           ORBQ_EACH(s += v[i][e])
           if (both) ORBQ_EACH(u += w[i][e])
           sum(s, u, place, turn);
-          const float mv = v_layer ? s / static_cast<float>(a.d) : 0.0f, mw = w_layer ? u / static_cast<float>(a.d) : 0.0f;
-          ORBQ_EACH(v[i][e] = col[i] < a.d ? v[i][e] - mv : 0.0f)
-          if (both) ORBQ_EACH(w[i][e] = col[i] < a.d ? w[i][e] - mw : 0.0f)
+          mv = v_layer ? s / static_cast<float>(a.d) : 0.0f;
+          mw = w_layer ? u / static_cast<float>(a.d) : 0.0f;
           s = u = 0.0f;
         }
+        // on one path for both norms, as in block_norm.hip
+        ORBQ_EACH(v[i][e] = col[i] < a.d ? v[i][e] - mv : 0.0f)
+        if (both) ORBQ_EACH(w[i][e] = col[i] < a.d ? w[i][e] - mw : 0.0f)
         ORBQ_EACH(s = __builtin_fmaf(v[i][e], v[i][e], s))
         if (both) ORBQ_EACH(u = __builtin_fmaf(w[i][e], w[i][e], u))
         sum(s, u, place, turn);
